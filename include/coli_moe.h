@@ -422,6 +422,188 @@ int coli_moe_forward_noalloc(const coli_moe_layer* layer, const void* x,
                              coli_dtype xt, int32_t T, float* y,
                              coli_stream_t stream);
 
+/* ------------------------------------------------------------------------ */
+/* Operators around the experts                                              */
+/* ------------------------------------------------------------------------ */
+/* A block built from them: coli_moe_block_norm -> coli_moe_route ->
+ * coli_moe_sort, coli_moe_dispatch -> (coli_moe_fp4_quantize ->
+ * coli_moe_fp4_product) for gate and up, again with SwiGLU for down ->
+ * coli_moe_combine -> coli_moe_block_norm.  (The source pages have no
+ * counterpart to these calls.)
+ *
+ * Matrices are row-major and contiguous.  Unless a call says otherwise its
+ * buffers must not overlap one another.  A call for zero tokens or rows
+ * succeeds and writes nothing (coli_moe_sort writes its offsets). */
+
+/* Picks sorted by expert.  idx device i32 [T, k]: the experts of every token;
+ * a pick is computed when 0 <= idx < E and, with w (device f32 [T, k] or
+ * NULL), w != 0 - the convention of coli_moe_forward_ex's w_out, where top-p
+ * and expert ranges report dropped picks as 0.  Outputs (device i32):
+ *   offsets [E+1]    exclusive prefix of the experts' counts; offsets[E] = the
+ *                    number n of computed picks
+ *   pair_tok [T*k]   token of row p < n, rows in the order of (expert, token,
+ *   pair_slot [T*k]  slot); its slot.  Entries n .. T*k-1 are left untouched.
+ *                    Either may be NULL.
+ *   inv [T, k]       row of each pick, -1 for a pick not computed
+ * Unlike coli_moe_union there is no limit from E * T: 1 <= k <= 32, 1 <= E <=
+ * 1024, T * k <= 2^30.  ws: device, coli_moe_sort_workspace_size bytes, 4-byte
+ * aligned. */
+int coli_moe_sort_workspace_size(int32_t T, int32_t k, int32_t E, size_t* bytes);
+int coli_moe_sort(const int32_t* idx, const float* w, int32_t T, int32_t k, int32_t E,
+                  int32_t* offsets, int32_t* pair_tok, int32_t* pair_slot, int32_t* inv,
+                  void* ws, size_t ws_bytes, coli_stream_t stream);
+
+/* Tokens copied into the order of their picks: xs[inv[t, j]] = x[t].  x device
+ * [T, H], xs device [T*k, H], both of type xt (f32 or bf16), any H >= 1.  Rows
+ * of xs that no pick names are left untouched.  An entry of inv outside
+ * [0, T*k) counts as a pick not computed, here and in the calls below. */
+int coli_moe_dispatch(const void* x, coli_dtype xt, int32_t T, int32_t H, int32_t k,
+                      const int32_t* inv, void* xs, coli_stream_t stream);
+
+/* Gradient of coli_moe_dispatch: dx[t] = sum_j dxs[inv[t, j]] over the computed
+ * picks, summed in f32 in slot order, rounded once to xt (0 for a token with no
+ * computed pick). */
+int coli_moe_dispatch_backward(const void* dxs, coli_dtype xt, int32_t T, int32_t H, int32_t k,
+                               const int32_t* inv, void* dx, coli_stream_t stream);
+
+/* Rows back to their tokens: y[t] = residual[t] + sum_j w[t, j] * o[inv[t, j]]
+ * over the computed picks, in f32 in slot order, rounded once to yt.  o device
+ * [T*k, H] of type ot; w device f32 [T, k] or NULL (all 1); residual device
+ * [T, H] of type yt or NULL, and may alias y. */
+int coli_moe_combine(const void* o, coli_dtype ot, int32_t T, int32_t H, int32_t k,
+                     const int32_t* inv, const float* w, const void* residual, void* y,
+                     coli_dtype yt, coli_stream_t stream);
+
+/* Gradients of coli_moe_combine for dy device [T, H] of type yt:
+ *   d_o[inv[t, j]] = w[t, j] * dy[t]   [T*k, H] of type ot; rows that no pick
+ *                                      names are left untouched
+ *   dw[t, j] = sum_h o[inv[t, j], h] * dy[t, h]   f32 [T, k], f32 sums; 0 for
+ *                                      a pick not computed
+ * The gradient of the residual is dy itself.  d_o or dw may be NULL (o is
+ * needed for dw alone and may be NULL without it). */
+int coli_moe_combine_backward(const void* dy, coli_dtype yt, const void* o, coli_dtype ot,
+                              int32_t T, int32_t H, int32_t k, const int32_t* inv,
+                              const float* w, void* d_o, float* dw, coli_stream_t stream);
+
+/* The step from one block to the next on a residual stream:
+ *   u     = o / sqrt(mean(o^2) + eps) * post_gain     (post_norm; else u = o)
+ *   x_out = x + alpha * gate * u                      rounded to xt
+ *   n_out = x_out / sqrt(mean(x_out^2) + eps) * pre_gain   (of the rounded
+ *           x_out, so that it equals the norm of what is stored), rounded to bt
+ * means over H, all arithmetic in f32. */
+typedef enum coli_gate {
+    COLI_GATE_NONE = 0,    /* 1                                  */
+    COLI_GATE_CHANNEL = 1, /* f32 [H], the same for every token  */
+    COLI_GATE_TOKEN = 2,   /* f32 [T], the same for every channel */
+    COLI_GATE_FULL = 3     /* f32 [T, H]                         */
+} coli_gate;
+
+typedef struct coli_norm_desc {
+    int32_t H;              /* 1 .. 16384                                      */
+    int32_t xt;             /* coli_dtype of x and x_out (and their gradients) */
+    int32_t bt;             /* coli_dtype of o and n_out (and their gradients);
+                               f32 with a bf16 stream is COLI_E_UNSUPPORTED    */
+    int32_t post_norm;      /* 1: o is normalised first                        */
+    int32_t gate_kind;      /* coli_gate                                       */
+    float alpha;            /* residual scale                                  */
+    float eps;              /* > 0                                             */
+    const float* post_gain; /* device f32 [H], NULL: 1                         */
+    const float* pre_gain;  /* device f32 [H], NULL: 1                         */
+} coli_norm_desc;
+
+/* x [T, H] xt; o [T, H] bt, or NULL before the first block (then x_out = x is
+ * not written and may be NULL); x_out [T, H] xt, may alias x; n_out [T, H] bt,
+ * or NULL after the last block; gate as desc->gate_kind says (NULL for none).
+ * rstd_post, rstd_pre (device f32 [T] or NULL) receive 1 / sqrt(mean + eps) of
+ * the two norms for the backward pass. */
+int coli_moe_block_norm(const coli_norm_desc* desc, const void* x, const void* o,
+                        const float* gate, int32_t T, void* x_out, void* n_out,
+                        float* rstd_post, float* rstd_pre, coli_stream_t stream);
+
+/* Gradients, from the x_out (or x when o was NULL), o, gate and rstd of the
+ * forward call and the gradients dx_out (xt) and dn (bt) of its outputs, either
+ * of which may be NULL for none (with neither: COLI_E_INVAL):
+ *   dx [T, H] xt     gradient of x; may alias dx_out
+ *   d_o [T, H] bt    gradient of o (NULL exactly when o is NULL)
+ *   dpost_gain, dpre_gain f32 [H], dgate f32 of gate's shape: gradients of the
+ *                    gains and of the gate, summed over what each is shared
+ *                    by, in an order that does not change between calls.  Each
+ *                    may be NULL.
+ * ws: device, coli_moe_block_norm_backward_workspace_size bytes, 16-byte
+ * aligned. */
+int coli_moe_block_norm_backward_workspace_size(const coli_norm_desc* desc, int32_t T,
+                                                size_t* bytes);
+int coli_moe_block_norm_backward(const coli_norm_desc* desc, const void* x_out, const void* o,
+                                 const float* gate, int32_t T, const float* rstd_post,
+                                 const float* rstd_pre, const void* dx_out, const void* dn,
+                                 void* dx, void* d_o, float* dpost_gain, float* dgate,
+                                 float* dpre_gain, void* ws, size_t ws_bytes,
+                                 coli_stream_t stream);
+
+/* 4-bit floating point in blocks with a shared scale.  A value is E2M1 (sign,
+ * magnitudes 0 0.5 1 1.5 2 3 4 6) times the scale of its block:
+ *   COLI_MXFP4  blocks of 32 columns, E8M0 scale byte b = 2^(b - 127) (255: NaN);
+ *               b = floor(log2 max|v|) - 2 + 127 clamped to [0, 254], 0 for a block of zeros
+ *               (the OCP Microscaling rule: magnitudes above 6 * 2^(b-127) saturate)
+ *   COLI_NVFP4  blocks of 16 columns, E4M3 scale s under one f32 scale g of the
+ *               whole matrix: s = e4m3(min(max|v| / (6 g), 448)), d = s * g,
+ *               code = e2m1(v * (1 / d)), all in f32 with the products 6 g, s g
+ *               and v * (1 / d) and both divisions rounded to f32; d == 0 gives
+ *               codes 0
+ * e2m1 and e4m3 round to nearest, ties to even; a block with an infinity or a
+ * NaN gets a NaN scale and codes 0.
+ *
+ * A matrix [rows, K] (K a multiple of 32) is
+ *   codes   [rows, K/2] bytes, column c in byte c/2, even c in the low nibble
+ *           (bit 3 the sign, bits 0-2 the index of the magnitude)
+ *   scales  tiles of 128 rows by 4 blocks: with C = ceil(K / block / 4), the
+ *           byte of (row r, block b) is at ((r/128 * C + b/4) * 32 + r%32) * 16
+ *           + r%128/32 * 4 + b%4; the bytes of blocks past K/block are 0 (of
+ *           rows past the last: anything)
+ * of the sizes that coli_moe_fp4_bytes reports; both 16-byte aligned. */
+typedef enum coli_fp4 { COLI_MXFP4 = 0, COLI_NVFP4 = 1 } coli_fp4;
+typedef enum coli_act {
+    COLI_ACT_NONE = 0,
+    COLI_ACT_SWIGLU = 1 /* v = silu(a) * b of rows [a | b] of 2 K columns, in f32 */
+} coli_act;
+
+int coli_moe_fp4_bytes(coli_fp4 fmt, int64_t rows, int32_t K, size_t* code_bytes,
+                       size_t* scale_bytes);
+
+/* Quantise rows.  x device of type xt, [n_src, K] (SwiGLU: [n_src, 2K]),
+ * 16-byte aligned; row r comes from x[src[r]] (src device i32 [rows]; an entry outside
+ * [0, n_src) gives a row of zeros) or, with src NULL, from x[r] (n_src >=
+ * rows).  count (device i32 or NULL): only rows r < *count are written, e.g.
+ * offsets + E of coli_moe_sort.  gscale (device f32, NULL: 1) is NVFP4's g,
+ * positive and finite, at least 2^-100; MXFP4 takes NULL only.  values (device,
+ * [rows, K] of type xt, or NULL) receives what codes and scales stand for,
+ * e2m1 * d in f32 rounded to xt. */
+int coli_moe_fp4_quantize(coli_fp4 fmt, const void* x, coli_dtype xt, int64_t n_src,
+                          int64_t rows, int32_t K, coli_act act, const int32_t* src,
+                          const int32_t* count, const float* gscale, void* codes, void* scales,
+                          void* values, coli_stream_t stream);
+
+/* Grouped product of quantised rows with quantised weights, both of format fmt:
+ *   y[p, r] = alpha[e] * sum_c X[p, c] * W[e R + r, c]
+ * for offsets[e] <= p < offsets[e+1].  x_codes, x_scales: P rows; w_codes,
+ * w_scales: E * R rows (R a multiple of 128 unless E = 1); offsets device i32
+ * [E+1], ascending, from 0 to at most P, or NULL with E = 1 for all P rows;
+ * alpha device f32 [E] or NULL (1): for NVFP4 the product of the two g (X and W
+ * above are without them).  y device [P, R] of type yt; rows that no expert has
+ * are left untouched.  Products are exact, sums in f32 in an order that depends
+ * on offsets and sizes alone; one rounding to yt.  1 <= E <= 1024, P < 2^31,
+ * E * R < 2^31, K a multiple of 32.  ws: device, 16-byte aligned,
+ * coli_moe_fp4_product_workspace_size bytes.  coli_moe_fp4_product_status is
+ * coli_moe_status for these calls: it synchronises the stream and reports
+ * whether a bounded wait gave up in the last call that used ws. */
+int coli_moe_fp4_product_workspace_size(coli_fp4 fmt, int64_t P, int32_t K, int32_t E, int32_t R,
+                                        size_t* bytes);
+int coli_moe_fp4_product(coli_fp4 fmt, const void* x_codes, const void* x_scales, int64_t P,
+                         int32_t K, const void* w_codes, const void* w_scales, int32_t E,
+                         int32_t R, const int32_t* offsets, const float* alpha, void* y,
+                         coli_dtype yt, void* ws, size_t ws_bytes, coli_stream_t stream);
+int coli_moe_fp4_product_status(const void* ws, int32_t* flags, coli_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -23,6 +23,14 @@ __all__ = [
     "coli_moe_stack_workspace_size", "coli_moe_stack_forward", "coli_moe_dequant_debug",
     "coli_moe_forward_noalloc", "NOALLOC_SCRATCH_BYTES", "coli_moe_status", "Desc",
     "coli_moe_layer_set_topp", "coli_moe_layer_set_partition",
+    "COLI_GATE_NONE", "COLI_GATE_CHANNEL", "COLI_GATE_TOKEN", "COLI_GATE_FULL", "NormDesc",
+    "COLI_MXFP4", "COLI_NVFP4", "COLI_ACT_NONE", "COLI_ACT_SWIGLU",
+    "coli_moe_sort_workspace_size", "coli_moe_sort", "coli_moe_dispatch",
+    "coli_moe_dispatch_backward", "coli_moe_combine", "coli_moe_combine_backward",
+    "coli_moe_block_norm", "coli_moe_block_norm_backward_workspace_size",
+    "coli_moe_block_norm_backward", "coli_moe_fp4_bytes", "coli_moe_fp4_quantize",
+    "coli_moe_fp4_product_workspace_size", "coli_moe_fp4_product",
+    "coli_moe_fp4_product_status",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -30,6 +38,9 @@ LIB_PATH = os.path.join(_HERE, "libcolimoe.so")
 
 COLI_F32, COLI_BF16 = 0, 1
 COLI_PATH_AUTO, COLI_PATH_GEMV, COLI_PATH_GEMM, COLI_PATH_FUSED, COLI_PATH_TWOPASS = 0, 1, 2, 3, 4
+COLI_GATE_NONE, COLI_GATE_CHANNEL, COLI_GATE_TOKEN, COLI_GATE_FULL = 0, 1, 2, 3
+COLI_MXFP4, COLI_NVFP4 = 0, 1
+COLI_ACT_NONE, COLI_ACT_SWIGLU = 0, 1
 
 # every symbol include/coli_moe.h declares
 EXPORTS = (
@@ -43,6 +54,12 @@ EXPORTS = (
     "coli_moe_quantize_expert_fp8_device", "coli_moe_quantize8", "coli_moe_expert_bytes8",
     "coli_moe_pack_expert8", "coli_moe_layer_set_topp", "coli_moe_layer_set_partition",
     "coli_moe_quantize_expert8_device", "coli_moe_layer_set_wait_test", "coli_moe_union_readback",
+    "coli_moe_sort_workspace_size", "coli_moe_sort", "coli_moe_dispatch",
+    "coli_moe_dispatch_backward", "coli_moe_combine", "coli_moe_combine_backward",
+    "coli_moe_block_norm", "coli_moe_block_norm_backward_workspace_size",
+    "coli_moe_block_norm_backward", "coli_moe_fp4_bytes", "coli_moe_fp4_quantize",
+    "coli_moe_fp4_product_workspace_size", "coli_moe_fp4_product",
+    "coli_moe_fp4_product_status",
 )
 
 
@@ -59,6 +76,14 @@ class Desc(ctypes.Structure):
                 ("norm_topk", ctypes.c_int32), ("router_w", ctypes.c_void_p),
                 ("router_b", ctypes.c_void_p), ("experts", ctypes.c_void_p),
                 ("bits", ctypes.c_int32)]
+
+
+class NormDesc(ctypes.Structure):
+    """coli_norm_desc; post_gain and pre_gain are device addresses or None."""
+    _fields_ = [("H", ctypes.c_int32), ("xt", ctypes.c_int32), ("bt", ctypes.c_int32),
+                ("post_norm", ctypes.c_int32), ("gate_kind", ctypes.c_int32),
+                ("alpha", ctypes.c_float), ("eps", ctypes.c_float),
+                ("post_gain", ctypes.c_void_p), ("pre_gain", ctypes.c_void_p)]
 
 
 from . import build as _build  # noqa: E402
@@ -109,6 +134,29 @@ _SIGS = {
     "coli_moe_stack_host_workspace_size": ([_P, _I32, _I32, ctypes.POINTER(_SZ)], ctypes.c_int),
     "coli_moe_stack_forward_host": ([_P, _I32, _P, _P, _I32, ctypes.c_float, ctypes.c_int, _P,
                                      _SZ, _P], ctypes.c_int),
+    "coli_moe_sort_workspace_size": ([_I32, _I32, _I32, ctypes.POINTER(_SZ)], ctypes.c_int),
+    "coli_moe_sort": ([_P, _P, _I32, _I32, _I32, _P, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
+    "coli_moe_dispatch": ([_P, ctypes.c_int, _I32, _I32, _I32, _P, _P, _P], ctypes.c_int),
+    "coli_moe_dispatch_backward": ([_P, ctypes.c_int, _I32, _I32, _I32, _P, _P, _P], ctypes.c_int),
+    "coli_moe_combine": ([_P, ctypes.c_int, _I32, _I32, _I32, _P, _P, _P, _P, ctypes.c_int, _P],
+                         ctypes.c_int),
+    "coli_moe_combine_backward": ([_P, ctypes.c_int, _P, ctypes.c_int, _I32, _I32, _I32, _P, _P,
+                                   _P, _P, _P], ctypes.c_int),
+    "coli_moe_block_norm": ([ctypes.POINTER(NormDesc), _P, _P, _P, _I32, _P, _P, _P, _P, _P],
+                            ctypes.c_int),
+    "coli_moe_block_norm_backward_workspace_size": ([ctypes.POINTER(NormDesc), _I32,
+                                                     ctypes.POINTER(_SZ)], ctypes.c_int),
+    "coli_moe_block_norm_backward": ([ctypes.POINTER(NormDesc), _P, _P, _P, _I32, _P, _P, _P, _P,
+                                      _P, _P, _P, _P, _P, _P, _SZ, _P], ctypes.c_int),
+    "coli_moe_fp4_bytes": ([ctypes.c_int, _I64, _I32, ctypes.POINTER(_SZ), ctypes.POINTER(_SZ)],
+                           ctypes.c_int),
+    "coli_moe_fp4_quantize": ([ctypes.c_int, _P, ctypes.c_int, _I64, _I64, _I32, ctypes.c_int, _P,
+                               _P, _P, _P, _P, _P, _P], ctypes.c_int),
+    "coli_moe_fp4_product_workspace_size": ([ctypes.c_int, _I64, _I32, _I32, _I32,
+                                             ctypes.POINTER(_SZ)], ctypes.c_int),
+    "coli_moe_fp4_product": ([ctypes.c_int, _P, _P, _I64, _I32, _P, _P, _I32, _I32, _P, _P, _P,
+                              ctypes.c_int, _P, _SZ, _P], ctypes.c_int),
+    "coli_moe_fp4_product_status": ([_P, ctypes.POINTER(_I32), _P], ctypes.c_int),
 }
 for _name, (_args, _res) in _SIGS.items():
     _f = getattr(lib, _name)
@@ -365,3 +413,191 @@ def coli_moe_forward_noalloc(layer, x, T, y, stream=None):
     memory: the library's built-in scratch array is used instead (see the header
     for its limit and for the rule that overlapping calls must be serialised)."""
     _ok(lib.coli_moe_forward_noalloc(layer, _ptr(x), _xtype(x), T, _ptr(y), _stream(stream)))
+
+
+# ---------------------------------------------------------------------------
+# Operators around the experts (see the header).  Tensors are checked against
+# the sizes given, so that a wrong shape raises here instead of reading past a
+# buffer on the device.
+# ---------------------------------------------------------------------------
+def _buf(name, a, dtype, count):
+    """Address of a contiguous CUDA tensor of `count` elements of dtype (None passes)."""
+    if a is None:
+        return None
+    if a.dtype != dtype:
+        raise TypeError(f"{name}: {a.dtype}, expected {dtype}")
+    if a.numel() < count or not a.is_contiguous():
+        raise ValueError(f"{name}: {tuple(a.shape)} (contiguous: {a.is_contiguous()}), "
+                         f"expected {count} contiguous elements")
+    if not a.is_cuda or a.device.index != _current_device():
+        raise ValueError(f"{name}: on {a.device}, expected the current CUDA device")
+    return a.data_ptr()
+
+
+def _current_device():
+    import torch
+    return torch.cuda.current_device()
+
+
+def _raw(name, a, count):
+    import torch
+    return _buf(name, a, torch.uint8, count)
+
+
+def _i32(name, a, count):
+    import torch
+    return _buf(name, a, torch.int32, count)
+
+
+def _f32(name, a, count):
+    import torch
+    return _buf(name, a, torch.float32, count)
+
+
+def _code_of(dtype):
+    import torch
+    if dtype == torch.float32:
+        return COLI_F32
+    if dtype == torch.bfloat16:
+        return COLI_BF16
+    raise TypeError(f"rows must be float32 or bfloat16, got {dtype}")
+
+
+def _workspace(ws):
+    return (None, 0) if ws is None else (_raw("ws", ws, 0), ws.numel())
+
+
+def coli_moe_sort_workspace_size(T: int, k: int, E: int) -> int:
+    out = _SZ()
+    _ok(lib.coli_moe_sort_workspace_size(T, k, E, ctypes.byref(out)))
+    return out.value
+
+
+def coli_moe_sort(idx, T, k, E, offsets, pair_tok, pair_slot, inv, ws, w=None, stream=None):
+    """pair_tok and pair_slot may be None; ws: uint8 of coli_moe_sort_workspace_size bytes."""
+    p, n = _workspace(ws)
+    _ok(lib.coli_moe_sort(_i32("idx", idx, T * k), _f32("w", w, T * k), T, k, E,
+                          _i32("offsets", offsets, E + 1), _i32("pair_tok", pair_tok, T * k),
+                          _i32("pair_slot", pair_slot, T * k), _i32("inv", inv, T * k), p, n,
+                          _stream(stream)))
+
+
+def coli_moe_dispatch(x, T, H, k, inv, xs, stream=None):
+    _ok(lib.coli_moe_dispatch(_buf("x", x, x.dtype, T * H), _code_of(x.dtype), T, H, k,
+                              _i32("inv", inv, T * k), _buf("xs", xs, x.dtype, T * k * H),
+                              _stream(stream)))
+
+
+def coli_moe_dispatch_backward(dxs, T, H, k, inv, dx, stream=None):
+    _ok(lib.coli_moe_dispatch_backward(_buf("dxs", dxs, dxs.dtype, T * k * H), _code_of(dxs.dtype),
+                                       T, H, k, _i32("inv", inv, T * k),
+                                       _buf("dx", dx, dxs.dtype, T * H), _stream(stream)))
+
+
+def coli_moe_combine(o, T, H, k, inv, w, y, residual=None, stream=None):
+    _ok(lib.coli_moe_combine(_buf("o", o, o.dtype, T * k * H), _code_of(o.dtype), T, H, k,
+                             _i32("inv", inv, T * k), _f32("w", w, T * k),
+                             _buf("residual", residual, y.dtype, T * H),
+                             _buf("y", y, y.dtype, T * H), _code_of(y.dtype), _stream(stream)))
+
+
+def coli_moe_combine_backward(dy, o, T, H, k, inv, w, d_o, dw, stream=None):
+    """o, d_o or dw may be None (see the header)."""
+    like = d_o if d_o is not None else o
+    if like is None:
+        raise ValueError("combine_backward: neither o nor d_o")
+    _ok(lib.coli_moe_combine_backward(_buf("dy", dy, dy.dtype, T * H), _code_of(dy.dtype),
+                                      _buf("o", o, like.dtype, T * k * H), _code_of(like.dtype),
+                                      T, H, k, _i32("inv", inv, T * k), _f32("w", w, T * k),
+                                      _buf("d_o", d_o, like.dtype, T * k * H),
+                                      _f32("dw", dw, T * k), _stream(stream)))
+
+
+def _norm_types(desc):
+    import torch
+    types = {COLI_F32: torch.float32, COLI_BF16: torch.bfloat16}
+    if desc.xt not in types or desc.bt not in types:
+        raise ValueError(f"NormDesc: types {desc.xt}, {desc.bt}")
+    return types[desc.xt], types[desc.bt]
+
+
+def _gate_size(desc, T):
+    return {COLI_GATE_CHANNEL: desc.H, COLI_GATE_TOKEN: T, COLI_GATE_FULL: T * desc.H}.get(
+        desc.gate_kind, 0)
+
+
+def coli_moe_block_norm(desc, x, o, T, x_out, n_out, gate=None, rstd_post=None, rstd_pre=None,
+                        stream=None):
+    xt, bt = _norm_types(desc)
+    n = T * desc.H
+    _ok(lib.coli_moe_block_norm(ctypes.byref(desc), _buf("x", x, xt, n), _buf("o", o, bt, n),
+                                _f32("gate", gate, _gate_size(desc, T)), T,
+                                _buf("x_out", x_out, xt, n), _buf("n_out", n_out, bt, n),
+                                _f32("rstd_post", rstd_post, T), _f32("rstd_pre", rstd_pre, T),
+                                _stream(stream)))
+
+
+def coli_moe_block_norm_backward_workspace_size(desc, T: int) -> int:
+    out = _SZ()
+    _ok(lib.coli_moe_block_norm_backward_workspace_size(ctypes.byref(desc), T, ctypes.byref(out)))
+    return out.value
+
+
+def coli_moe_block_norm_backward(desc, x_out, o, T, dx_out, dn, dx, d_o, ws, gate=None,
+                                 rstd_post=None, rstd_pre=None, dpost_gain=None, dgate=None,
+                                 dpre_gain=None, stream=None):
+    xt, bt = _norm_types(desc)
+    n, ng = T * desc.H, _gate_size(desc, T)
+    p, size = _workspace(ws)
+    _ok(lib.coli_moe_block_norm_backward(
+        ctypes.byref(desc), _buf("x_out", x_out, xt, n), _buf("o", o, bt, n),
+        _f32("gate", gate, ng), T, _f32("rstd_post", rstd_post, T), _f32("rstd_pre", rstd_pre, T),
+        _buf("dx_out", dx_out, xt, n), _buf("dn", dn, bt, n), _buf("dx", dx, xt, n),
+        _buf("d_o", d_o, bt, n), _f32("dpost_gain", dpost_gain, desc.H),
+        _f32("dgate", dgate, ng), _f32("dpre_gain", dpre_gain, desc.H), p, size,
+        _stream(stream)))
+
+
+def coli_moe_fp4_bytes(fmt: int, rows: int, K: int):
+    """(bytes of the codes, bytes of the scales) of a matrix [rows, K]."""
+    nc, ns = _SZ(), _SZ()
+    _ok(lib.coli_moe_fp4_bytes(fmt, rows, K, ctypes.byref(nc), ctypes.byref(ns)))
+    return nc.value, ns.value
+
+
+def coli_moe_fp4_quantize(fmt, x, rows, K, codes, scales, act=COLI_ACT_NONE, src=None, count=None,
+                          gscale=None, values=None, stream=None):
+    """x: [n, K] rows ([n, 2K] for SwiGLU), n >= rows unless src picks them."""
+    nc, ns = coli_moe_fp4_bytes(fmt, rows, K)
+    n_src = x.numel() // (2 * K if act == COLI_ACT_SWIGLU else K)
+    _ok(lib.coli_moe_fp4_quantize(fmt, _buf("x", x, x.dtype, 0), _code_of(x.dtype), n_src, rows, K,
+                                  act, _i32("src", src, rows), _i32("count", count, 1),
+                                  _f32("gscale", gscale, 1), _raw("codes", codes, nc),
+                                  _raw("scales", scales, ns),
+                                  _buf("values", values, x.dtype, rows * K), _stream(stream)))
+
+
+def coli_moe_fp4_product_workspace_size(fmt: int, P: int, K: int, E: int, R: int) -> int:
+    out = _SZ()
+    _ok(lib.coli_moe_fp4_product_workspace_size(fmt, P, K, E, R, ctypes.byref(out)))
+    return out.value
+
+
+def coli_moe_fp4_product(fmt, x_codes, x_scales, P, K, w_codes, w_scales, E, R, y, ws,
+                         offsets=None, alpha=None, stream=None):
+    xc, xs = coli_moe_fp4_bytes(fmt, P, K)
+    wc, wsc = coli_moe_fp4_bytes(fmt, E * R, K)
+    p, n = _workspace(ws)
+    _ok(lib.coli_moe_fp4_product(fmt, _raw("x_codes", x_codes, xc), _raw("x_scales", x_scales, xs),
+                                 P, K, _raw("w_codes", w_codes, wc),
+                                 _raw("w_scales", w_scales, wsc), E, R,
+                                 _i32("offsets", offsets, E + 1), _f32("alpha", alpha, E),
+                                 _buf("y", y, y.dtype, P * R), _code_of(y.dtype), p, n,
+                                 _stream(stream)))
+
+
+def coli_moe_fp4_product_status(ws, stream=None) -> int:
+    """Error flags of the last product that used ws (raises on a timeout)."""
+    flags = _I32(0)
+    _ok(lib.coli_moe_fp4_product_status(_raw("ws", ws, 4), ctypes.byref(flags), _stream(stream)))
+    return flags.value

@@ -1,0 +1,309 @@
+// block.cu - C ABI of the operators around the experts (see include/coli_moe.h):
+// sort, dispatch and combine with their gradients, and the norms between blocks.
+// Host code validates arguments and launches the kernels of rows.cuh and
+// norm.cuh on the caller's stream.
+#include <algorithm>
+#include <cmath>
+
+#include "coli_moe.h"
+#include "common.cuh"
+#include "host.cuh"
+#include "norm.cuh"
+#include "rows.cuh"
+
+using namespace coli;
+
+namespace {
+
+bool type_ok(int t) { return t == COLI_F32 || t == COLI_BF16; }
+int type_size(int t) { return t == COLI_F32 ? 4 : 2; }
+
+bool aligned(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+
+// what every call on picks checks
+int picks_ok(const char* what, int T, int k) {
+    if (T < 0 || k < 1 || k > 32 || (int64_t)T * k > (1 << 30))
+        return fail(COLI_E_INVAL, "%s: bad sizes T=%d k=%d", what, T, k);
+    return COLI_OK;
+}
+
+int rows_ok(const char* what, int T, int H, int k) {
+    const int rc = picks_ok(what, T, k);
+    if (rc) return rc;
+    if (H < 1 || (int64_t)T * ((H + 255) / 256) > INT32_MAX)  // one CTA per 256 columns at most
+        return fail(COLI_E_INVAL, "%s: bad sizes T=%d H=%d", what, T, H);
+    return COLI_OK;
+}
+
+int64_t sort_chunk(int64_t P) {
+    const int64_t group = 32 * kSortWarps;
+    return ((P + kSortMaxChunks - 1) / kSortMaxChunks + group - 1) / group * group;
+}
+
+template <typename V>
+int launch_dispatch(const void* x, int T, int nvec, int k, const int32_t* inv, void* xs, cudaStream_t st) {
+    const int per = (nvec + 255) / 256;
+    return launch_pdl(dispatch_kernel<V>, dim3((unsigned)T * per), 256, 0, st, "dispatch", (const V*)x,
+                      (int64_t)T * k, nvec, per, k, inv, (V*)xs);
+}
+
+template <typename OT, typename YT>
+int launch_rows_sum(const void* o, int T, int H, int k, const int32_t* inv, const float* w,
+                    const void* residual, void* y, cudaStream_t st) {
+    // 16 bytes of o per thread where rows and pointers allow it
+    constexpr int N = 16 / sizeof(OT);
+    constexpr int ya = N * sizeof(YT) < 16 ? N * sizeof(YT) : 16;
+    const bool wide = H % N == 0 && aligned(o, 16) && aligned(residual, ya) && aligned(y, ya);
+    const int nvec = wide ? H / N : H, per = (nvec + 255) / 256;
+    const auto kern = wide ? rows_sum_kernel<OT, YT, N> : rows_sum_kernel<OT, YT, 1>;
+    return launch_pdl(kern, dim3((unsigned)T * per), 256, 0, st, "combine", (const OT*)o, (int64_t)T * k,
+                      nvec, per, k, inv, w, (const YT*)residual, (YT*)y);
+}
+
+template <typename YT, typename OT>
+int launch_rows_sum_backward(const void* dy, const void* o, int T, int H, int k, const int32_t* inv,
+                             const float* w, void* d_o, float* dw, cudaStream_t st) {
+    constexpr int N = 16 / sizeof(OT);
+    constexpr int ya = N * sizeof(YT) < 16 ? N * sizeof(YT) : 16;
+    const bool wide = H % N == 0 && aligned(o, 16) && aligned(d_o, 16) && aligned(dy, ya);
+    const int nvec = wide ? H / N : H;
+    const auto kern = wide ? rows_sum_backward_kernel<YT, OT, N> : rows_sum_backward_kernel<YT, OT, 1>;
+    return launch_pdl(kern, dim3(T), 256, 0, st, "combine backward", (const YT*)dy, (const OT*)o,
+                      (int64_t)T * k, nvec, k, inv, w, (OT*)d_o, dw);
+}
+
+int norm_ok(const char* what, const coli_norm_desc* d, int T) {
+    if (!d) return fail(COLI_E_INVAL, "%s: NULL descriptor", what);
+    if (d->H < 1 || d->H > kNormMaxH || T < 0) return fail(COLI_E_INVAL, "%s: bad sizes T=%d H=%d", what, T, d->H);
+    if (!type_ok(d->xt) || !type_ok(d->bt)) return fail(COLI_E_INVAL, "%s: bad dtype", what);
+    if (d->xt == COLI_BF16 && d->bt == COLI_F32)
+        return fail(COLI_E_UNSUPPORTED, "%s: f32 blocks on a bf16 stream", what);
+    if (d->gate_kind < COLI_GATE_NONE || d->gate_kind > COLI_GATE_FULL)
+        return fail(COLI_E_INVAL, "%s: bad gate_kind %d", what, d->gate_kind);
+    if (!(d->eps > 0.0f) || !std::isfinite(d->eps) || !std::isfinite(d->alpha))
+        return fail(COLI_E_INVAL, "%s: eps must be positive, eps and alpha finite", what);
+    return COLI_OK;
+}
+
+NormArgs norm_args(const coli_norm_desc& d, const float* gate, int T) {
+    NormArgs a;
+    a.H = d.H; a.T = T;
+    a.post_norm = d.post_norm != 0;
+    a.gate_kind = d.gate_kind;
+    a.alpha = d.alpha; a.eps = d.eps;
+    a.post_gain = d.post_gain; a.pre_gain = d.pre_gain;
+    a.gate = gate;
+    return a;
+}
+
+// elements per vector, vectors per thread and threads of a row
+struct NormShape { int V, N, threads; };
+NormShape norm_shape(int H, bool wide) {
+    NormShape s;
+    s.V = wide ? 4 : 1;
+    const int vecs = H / s.V, small = wide ? 4 : 16;
+    s.N = vecs <= small * kNormMaxThreads ? small : 2 * small;
+    s.threads = ((vecs + s.N - 1) / s.N + 31) / 32 * 32;
+    return s;
+}
+
+// calls f with the kernel's type and shape parameters as template arguments
+template <template <typename, typename, int, int> class K, typename... A>
+int norm_dispatch(const coli_norm_desc& d, const NormShape& s, A... args) {
+#define COLI_NORM_CASE(XT, BT)                                          \
+    if (s.V == 4) {                                                     \
+        if (s.N == 4) return K<XT, BT, 4, 4>::launch(s, args...);       \
+        return K<XT, BT, 4, 8>::launch(s, args...);                     \
+    }                                                                   \
+    if (s.N == 16) return K<XT, BT, 1, 16>::launch(s, args...);         \
+    return K<XT, BT, 1, 32>::launch(s, args...);
+    if (d.xt == COLI_F32 && d.bt == COLI_F32) { COLI_NORM_CASE(float, float) }
+    if (d.xt == COLI_F32) { COLI_NORM_CASE(float, __nv_bfloat16) }
+    COLI_NORM_CASE(__nv_bfloat16, __nv_bfloat16)
+#undef COLI_NORM_CASE
+}
+
+template <typename XT, typename BT, int V, int N>
+struct NormForward {
+    static int launch(const NormShape& s, const NormArgs& a, const void* x, const void* o, void* x_out,
+                      void* n_out, float* rstd_post, float* rstd_pre, cudaStream_t st) {
+        return launch_pdl(block_norm_kernel<XT, BT, V, N>, dim3(a.T), s.threads, 0, st, "block norm", a,
+                          (const XT*)x, (const BT*)o, (XT*)x_out, (BT*)n_out, rstd_post, rstd_pre);
+    }
+};
+
+template <typename XT, typename BT, int V, int N>
+struct NormBackward {
+    static int launch(const NormShape& s, const NormArgs& a, const void* x_out, const void* o,
+                      const float* rstd_post, const float* rstd_pre, const void* dx_out, const void* dn,
+                      void* dx, void* d_o, float* dgate, float* partial, int grid, cudaStream_t st) {
+        return launch_pdl(block_norm_backward_kernel<XT, BT, V, N>, dim3(grid), s.threads, 0, st,
+                          "block norm backward", a, (const XT*)x_out, (const BT*)o, rstd_post, rstd_pre,
+                          (const XT*)dx_out, (const BT*)dn, (XT*)dx, (BT*)d_o, dgate, partial);
+    }
+};
+
+// CTAs of the backward pass: two per SM, so that one's loads cover the other's
+// sums over the row
+constexpr int kNormBackwardCtas = 296;
+
+}  // namespace
+
+extern "C" {
+
+int coli_moe_sort_workspace_size(int32_t T, int32_t k, int32_t E, size_t* bytes) {
+    if (!bytes) return fail(COLI_E_INVAL, "sort_workspace_size: NULL pointer");
+    const int rc = picks_ok("sort_workspace_size", T, k);
+    if (rc) return rc;
+    if (E < 1 || E > 1024) return fail(COLI_E_INVAL, "sort_workspace_size: E=%d outside [1, 1024]", E);
+    const int64_t P = (int64_t)T * k;
+    *bytes = P <= kSortOneCta ? 0 : (size_t)((P + sort_chunk(P) - 1) / sort_chunk(P)) * E * 4;
+    return COLI_OK;
+}
+
+int coli_moe_sort(const int32_t* idx, const float* w, int32_t T, int32_t k, int32_t E,
+                  int32_t* offsets, int32_t* pair_tok, int32_t* pair_slot, int32_t* inv, void* ws,
+                  size_t ws_bytes, coli_stream_t stream) {
+    size_t need;
+    int rc = coli_moe_sort_workspace_size(T, k, E, &need);
+    if (rc) return rc;
+    if (!offsets || (T > 0 && (!idx || !inv))) return fail(COLI_E_INVAL, "sort: NULL pointer");
+    if (need && (!ws || ws_bytes < need || !aligned(ws, 4)))
+        return fail(COLI_E_WORKSPACE, "sort: workspace of %zu bytes, %zu needed", ws ? ws_bytes : 0, need);
+    const int64_t P = (int64_t)T * k;
+    const int one_smem = (kSortWarps * E + E + 1) * 4, place_smem = one_smem + E * 4;
+    if (P <= kSortOneCta) {
+        if ((rc = set_smem((const void*)sort_one_kernel, one_smem))) return rc;
+        return launch_pdl(sort_one_kernel, dim3(1), kSortThreads, one_smem, S(stream), "sort", idx, w, (int)P,
+                          (int)k, (int)E, offsets, pair_tok, pair_slot, inv);
+    }
+    const int64_t chunk = sort_chunk(P);
+    const dim3 grid((unsigned)((P + chunk - 1) / chunk));
+    int32_t* counts = static_cast<int32_t*>(ws);
+    const int count_smem = kSortWarps * E * 4;
+    if ((rc = set_smem((const void*)sort_count_kernel, count_smem))) return rc;
+    if ((rc = set_smem((const void*)sort_place_kernel, place_smem))) return rc;
+    if ((rc = launch_pdl(sort_count_kernel, grid, kSortThreads, count_smem, S(stream), "sort count", idx, w, P,
+                         chunk, (int)E, counts)))
+        return rc;
+    return launch_pdl(sort_place_kernel, grid, kSortThreads, place_smem, S(stream), "sort place", idx, w, P, chunk,
+                      (int)k, (int)E, (const int32_t*)counts, offsets, pair_tok, pair_slot, inv);
+}
+
+int coli_moe_dispatch(const void* x, coli_dtype xt, int32_t T, int32_t H, int32_t k,
+                      const int32_t* inv, void* xs, coli_stream_t stream) {
+    int rc = rows_ok("dispatch", T, H, k);
+    if (rc) return rc;
+    if (!type_ok(xt)) return fail(COLI_E_INVAL, "dispatch: bad dtype");
+    if (T == 0) return COLI_OK;
+    if (!x || !inv || !xs) return fail(COLI_E_INVAL, "dispatch: NULL pointer");
+    const int64_t bytes = (int64_t)H * type_size(xt);
+    if (bytes % 16 == 0 && aligned(x, 16) && aligned(xs, 16))
+        return launch_dispatch<uint4>(x, T, (int)(bytes / 16), k, inv, xs, S(stream));
+    if (xt == COLI_F32) return launch_dispatch<uint32_t>(x, T, H, k, inv, xs, S(stream));
+    return launch_dispatch<uint16_t>(x, T, H, k, inv, xs, S(stream));
+}
+
+int coli_moe_dispatch_backward(const void* dxs, coli_dtype xt, int32_t T, int32_t H, int32_t k,
+                               const int32_t* inv, void* dx, coli_stream_t stream) {
+    return coli_moe_combine(dxs, xt, T, H, k, inv, nullptr, nullptr, dx, xt, stream);
+}
+
+int coli_moe_combine(const void* o, coli_dtype ot, int32_t T, int32_t H, int32_t k,
+                     const int32_t* inv, const float* w, const void* residual, void* y,
+                     coli_dtype yt, coli_stream_t stream) {
+    int rc = rows_ok("combine", T, H, k);
+    if (rc) return rc;
+    if (!type_ok(ot) || !type_ok(yt)) return fail(COLI_E_INVAL, "combine: bad dtype");
+    if (T == 0) return COLI_OK;
+    if (!o || !inv || !y) return fail(COLI_E_INVAL, "combine: NULL pointer");
+    if (ot == COLI_F32)
+        return yt == COLI_F32 ? launch_rows_sum<float, float>(o, T, H, k, inv, w, residual, y, S(stream))
+                              : launch_rows_sum<float, __nv_bfloat16>(o, T, H, k, inv, w, residual, y, S(stream));
+    return yt == COLI_F32 ? launch_rows_sum<__nv_bfloat16, float>(o, T, H, k, inv, w, residual, y, S(stream))
+                          : launch_rows_sum<__nv_bfloat16, __nv_bfloat16>(o, T, H, k, inv, w, residual, y, S(stream));
+}
+
+int coli_moe_combine_backward(const void* dy, coli_dtype yt, const void* o, coli_dtype ot, int32_t T,
+                              int32_t H, int32_t k, const int32_t* inv, const float* w, void* d_o,
+                              float* dw, coli_stream_t stream) {
+    int rc = rows_ok("combine_backward", T, H, k);
+    if (rc) return rc;
+    if (!type_ok(ot) || !type_ok(yt)) return fail(COLI_E_INVAL, "combine_backward: bad dtype");
+    if (T == 0) return COLI_OK;
+    if (!dy || !inv || (!d_o && !dw) || (dw && !o)) return fail(COLI_E_INVAL, "combine_backward: NULL pointer");
+    if (yt == COLI_F32)
+        return ot == COLI_F32 ? launch_rows_sum_backward<float, float>(dy, o, T, H, k, inv, w, d_o, dw, S(stream))
+                              : launch_rows_sum_backward<float, __nv_bfloat16>(dy, o, T, H, k, inv, w, d_o, dw, S(stream));
+    return ot == COLI_F32
+               ? launch_rows_sum_backward<__nv_bfloat16, float>(dy, o, T, H, k, inv, w, d_o, dw, S(stream))
+               : launch_rows_sum_backward<__nv_bfloat16, __nv_bfloat16>(dy, o, T, H, k, inv, w, d_o, dw, S(stream));
+}
+
+int coli_moe_block_norm(const coli_norm_desc* desc, const void* x, const void* o, const float* gate,
+                        int32_t T, void* x_out, void* n_out, float* rstd_post, float* rstd_pre,
+                        coli_stream_t stream) {
+    int rc = norm_ok("block_norm", desc, T);
+    if (rc) return rc;
+    if (T == 0) return COLI_OK;
+    if (!x || (o && !x_out) || (!o && !n_out)) return fail(COLI_E_INVAL, "block_norm: NULL pointer");
+    if (o && (desc->gate_kind != COLI_GATE_NONE) != (gate != nullptr))
+        return fail(COLI_E_INVAL, "block_norm: gate and gate_kind disagree");
+    const int xa = 4 * type_size(desc->xt), ba = 4 * type_size(desc->bt);
+    const bool wide = desc->H % 4 == 0 && aligned(x, xa) && aligned(x_out, xa) && aligned(o, ba) &&
+                      aligned(n_out, ba) && aligned(desc->post_gain, 16) && aligned(desc->pre_gain, 16) &&
+                      aligned(gate, 16);
+    const NormArgs a = norm_args(*desc, gate, T);
+    return norm_dispatch<NormForward>(*desc, norm_shape(desc->H, wide), a, x, o, x_out, n_out, rstd_post, rstd_pre,
+                                      S(stream));
+}
+
+int coli_moe_block_norm_backward_workspace_size(const coli_norm_desc* desc, int32_t T, size_t* bytes) {
+    int rc = norm_ok("block_norm_backward_workspace_size", desc, T);
+    if (rc) return rc;
+    if (!bytes) return fail(COLI_E_INVAL, "block_norm_backward_workspace_size: NULL pointer");
+    *bytes = (size_t)std::min(T, kNormBackwardCtas) * 3 * desc->H * 4;
+    return COLI_OK;
+}
+
+int coli_moe_block_norm_backward(const coli_norm_desc* desc, const void* x_out, const void* o,
+                                 const float* gate, int32_t T, const float* rstd_post,
+                                 const float* rstd_pre, const void* dx_out, const void* dn, void* dx,
+                                 void* d_o, float* dpost_gain, float* dgate, float* dpre_gain, void* ws,
+                                 size_t ws_bytes, coli_stream_t stream) {
+    size_t need;
+    int rc = norm_ok("block_norm_backward", desc, T);
+    if (rc) return rc;
+    if ((rc = coli_moe_block_norm_backward_workspace_size(desc, T, &need))) return rc;
+    if (!dx || (!dx_out && !dn) || (dn && (!x_out || !rstd_pre)) || (o != nullptr) != (d_o != nullptr) ||
+        (o && desc->post_norm && !rstd_post))
+        return fail(COLI_E_INVAL, "block_norm_backward: NULL pointer");
+    if (o && (desc->gate_kind != COLI_GATE_NONE) != (gate != nullptr))
+        return fail(COLI_E_INVAL, "block_norm_backward: gate and gate_kind disagree");
+    if ((dgate && (!o || desc->gate_kind == COLI_GATE_NONE)) || (dpost_gain && (!o || !desc->post_norm)) ||
+        (dpre_gain && !dn))
+        return fail(COLI_E_INVAL, "block_norm_backward: gradient of an input that this call does not have");
+    // sums over tokens: partial rows in the workspace, then the second kernel
+    const bool channel = dgate && desc->gate_kind == COLI_GATE_CHANNEL;
+    const bool sums = dpost_gain || channel || dpre_gain;
+    if (sums && (!ws || ws_bytes < need || !aligned(ws, 16)))
+        return fail(COLI_E_WORKSPACE, "block_norm_backward: workspace of %zu bytes, %zu needed", ws ? ws_bytes : 0,
+                    need);
+    const int grid = std::min(T, kNormBackwardCtas);
+    float* partial = sums ? static_cast<float*>(ws) : nullptr;
+    if (T > 0) {
+        const int xa = 4 * type_size(desc->xt), ba = 4 * type_size(desc->bt);
+        const bool wide = desc->H % 4 == 0 && aligned(x_out, xa) && aligned(dx_out, xa) && aligned(dx, xa) &&
+                          aligned(o, ba) && aligned(dn, ba) && aligned(d_o, ba) && aligned(desc->post_gain, 16) &&
+                          aligned(desc->pre_gain, 16) && aligned(gate, 16) && aligned(dgate, 16);
+        const NormArgs a = norm_args(*desc, gate, T);
+        rc = norm_dispatch<NormBackward>(*desc, norm_shape(desc->H, wide), a, x_out, o, rstd_post, rstd_pre, dx_out,
+                                         dn, dx, d_o, dgate, partial, grid, S(stream));
+        if (rc) return rc;
+    }
+    if (!sums) return COLI_OK;
+    return launch_pdl(norm_reduce_kernel, dim3((desc->H + 31) / 32, 3), 256, 0, S(stream), "block norm sums",
+                      (const float*)partial, grid, (int)desc->H, dpost_gain, channel ? dgate : nullptr, dpre_gain);
+}
+
+}  // extern "C"

@@ -4,18 +4,17 @@
 // kernels of route.cuh, gemv.cuh, gemm.cuh and misc.cuh on the caller's
 // stream.  Nothing here synchronises the host or allocates device memory.
 #include <cmath>
-#include <cstdarg>
 #include <cstdio>
 #include <cstring>
 #include <mutex>
 #include <vector>
-#include <string>
 
 #include "coli_moe.h"
 #include "common.cuh"
 #include "fused.cuh"
 #include "gemm.cuh"
 #include "gemv.cuh"
+#include "host.cuh"
 #include "misc.cuh"
 #include "route.cuh"
 #include "split.cuh"
@@ -37,26 +36,6 @@ struct coli_moe_layer {
 };
 
 namespace {
-
-thread_local std::string g_err;
-
-int fail(int code, const char* fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof(buf), fmt, ap);
-    va_end(ap);
-    g_err = buf;
-    return code;
-}
-
-int check_launch(const char* what) {
-    const cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return fail(COLI_E_CUDA, "%s: %s", what, cudaGetErrorString(e));
-    return COLI_OK;
-}
-
-cudaStream_t S(coli_stream_t s) { return reinterpret_cast<cudaStream_t>(s); }
 
 bool shape_ok(int H, int I, int group) {
     return H > 0 && I > 0 && H % 128 == 0 && I % 128 == 0 && (group == 0 || group == 64);
@@ -151,48 +130,6 @@ int tokens_ok(const coli_moe_desc& d, int T) {
         return fail(COLI_E_UNSUPPORTED, "E*ceil(T/32)=%lld exceeds 24576 (union bitmap)",
                     (long long)words);
     return COLI_OK;
-}
-
-// Raise a kernel's dynamic shared-memory limit to `bytes` (static + dynamic
-// above 48 KB needs the opt-in).  The largest value set per (device, kernel) is
-// remembered so that a forward normally makes no attribute call.
-int set_smem(const void* fn, int bytes) {
-    struct Entry { int dev; const void* fn; int bytes; };
-    static std::mutex mu;
-    static std::vector<Entry> done;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return fail(COLI_E_CUDA, "smem attribute: no device");
-    std::lock_guard<std::mutex> lock(mu);
-    for (const Entry& en : done)
-        if (en.dev == dev && en.fn == fn && en.bytes >= bytes) return COLI_OK;
-    const cudaError_t e =
-        cudaFuncSetAttribute(fn, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-    if (e != cudaSuccess) return fail(COLI_E_CUDA, "smem attribute: %s", cudaGetErrorString(e));
-    for (Entry& en : done)
-        if (en.dev == dev && en.fn == fn) { en.bytes = bytes; return COLI_OK; }
-    done.push_back({dev, fn, bytes});
-    return COLI_OK;
-}
-
-// Launch as a programmatic dependent of the previous kernel in the stream: the
-// kernel may start while that one finishes and waits (griddepcontrol.wait)
-// before it reads what that one wrote.
-template <typename... Args>
-int launch_pdl(void (*kern)(Args...), dim3 grid, int threads, int smem, cudaStream_t st,
-               const char* what, Args... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, args...);
-    if (e != cudaSuccess) return fail(COLI_E_CUDA, "%s: %s", what, cudaGetErrorString(e));
-    return check_launch(what);
 }
 
 // Router logits into zpart ([*ks_out][T][E] K slices; the small-batch router
@@ -300,24 +237,6 @@ int launch_select(const coli_moe_desc& d, const PickFilter& f, const float* zpar
 // ---------------------------------------------------------------------------
 // tensor-core path
 // ---------------------------------------------------------------------------
-typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-    static EncodeTiledFn fn = nullptr;
-    static std::once_flag once;
-    std::call_once(once, [] {
-        void* f = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &f, cudaEnableDefault, &q) == cudaSuccess &&
-            q == cudaDriverEntryPointSuccess)
-            fn = reinterpret_cast<EncodeTiledFn>(f);
-    });
-    return fn;
-}
-
 // [rows][cols] fp16, boxes of 64 rows x 64 columns, 128-byte swizzle
 int encode_b_map(CUtensorMap* m, const void* base, int64_t rows, int64_t cols) {
     EncodeTiledFn fn = encode_fn();
@@ -690,7 +609,7 @@ int noalloc_scratch(void** out) {
 // ===========================================================================
 extern "C" {
 
-const char* coli_moe_last_error(void) { return g_err.c_str(); }
+const char* coli_moe_last_error(void) { return g_err; }
 
 int coli_moe_quantize(const float* w, int64_t rows, int64_t cols, int32_t group,
                       uint8_t* packed, float* scales) {

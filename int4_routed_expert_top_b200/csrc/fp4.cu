@@ -1,0 +1,174 @@
+// fp4.cu - C ABI of the 4-bit floating point operators (see include/coli_moe.h):
+// the quantiser of rows and the grouped product with quantised weights.
+#include <algorithm>
+
+#include "coli_moe.h"
+#include "common.cuh"
+#include "fp4.cuh"
+#include "host.cuh"
+
+using namespace coli;
+
+namespace {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+int block_of(coli_fp4 fmt) { return fmt == COLI_NVFP4 ? 16 : 32; }
+int words_of(coli_fp4 fmt, int K) { return (K / block_of(fmt) + 3) / 4; }
+
+int fp4_ok(const char* what, coli_fp4 fmt, int64_t rows, int K) {
+    if (fmt != COLI_MXFP4 && fmt != COLI_NVFP4) return fail(COLI_E_INVAL, "%s: bad format %d", what, (int)fmt);
+    if (rows < 0 || rows > INT32_MAX) return fail(COLI_E_INVAL, "%s: %lld rows", what, (long long)rows);
+    if (K < 32 || K % 32 || K > (1 << 20)) return fail(COLI_E_INVAL, "%s: K=%d is no multiple of 32 in [32, 2^20]", what, K);
+    return COLI_OK;
+}
+
+int sm_count() {
+    int dev = 0, sms = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1)
+        sms = 148;
+    return sms;
+}
+constexpr int kMaxGrid = 160;  // B200 has 148 SMs; the workspace is sized for this many
+
+// Rows of an expert per tile: 32 streams the weights with the deepest ring, 192
+// makes the most of each weight byte.
+constexpr int kFpSmallNT = 32, kFpLargeNT = 192;
+int tile_rows(int64_t P, int E) { return P > (int64_t)48 * E ? kFpLargeNT : kFpSmallNT; }
+
+// bytes [rows][K/2], boxes of 128 bytes x box_rows, 128-byte swizzle
+int encode_codes_map(CUtensorMap* m, const void* base, int64_t rows, int K, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return fail(COLI_E_CUDA, "cuTensorMapEncodeTiled is not available");
+    const cuuint64_t dims[2] = {(cuuint64_t)K / 2, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)K / 2};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(COLI_E_CUDA, "codes tensor map encode failed (%d)", (int)r);
+    return COLI_OK;
+}
+
+template <int NT, bool NV, typename YT>
+int launch_product(const FpArgs& a, const void* x_codes, const void* w_codes, void* y, cudaStream_t st) {
+    using C = FpShape<NT, NV>;
+    CUtensorMap wmap, xmap;
+    int rc;
+    if ((rc = encode_codes_map(&wmap, w_codes, (int64_t)a.E * a.R, a.K, 128))) return rc;
+    if ((rc = encode_codes_map(&xmap, x_codes, a.P, a.K, C::box))) return rc;
+    if ((rc = set_smem((const void*)fp4_product_kernel<NT, NV, YT>, C::smem))) return rc;
+    const int grid = std::min(sm_count(), kMaxGrid);
+    if ((rc = launch_pdl(fp4_product_kernel<NT, NV, YT>, dim3(grid), kFpThreads, C::smem, st, "fp4 product", wmap, xmap,
+                         a, (YT*)y)))
+        return rc;
+    return launch_pdl(fp4_join_kernel<NT, YT>, dim3(grid, NT / 32), kFpThreads, 0, st, "fp4 join", a, grid, (YT*)y);
+}
+
+template <int NT>
+int launch_product_t(coli_fp4 fmt, coli_dtype yt, const FpArgs& a, const void* x_codes, const void* w_codes, void* y,
+                     cudaStream_t st) {
+    if (fmt == COLI_NVFP4)
+        return yt == COLI_F32 ? launch_product<NT, true, float>(a, x_codes, w_codes, y, st)
+                              : launch_product<NT, true, __nv_bfloat16>(a, x_codes, w_codes, y, st);
+    return yt == COLI_F32 ? launch_product<NT, false, float>(a, x_codes, w_codes, y, st)
+                          : launch_product<NT, false, __nv_bfloat16>(a, x_codes, w_codes, y, st);
+}
+
+}  // namespace
+
+extern "C" {
+
+int coli_moe_fp4_bytes(coli_fp4 fmt, int64_t rows, int32_t K, size_t* code_bytes, size_t* scale_bytes) {
+    const int rc = fp4_ok("fp4_bytes", fmt, rows, K);
+    if (rc) return rc;
+    if (!code_bytes || !scale_bytes) return fail(COLI_E_INVAL, "fp4_bytes: NULL pointer");
+    *code_bytes = (size_t)rows * (K / 2);
+    *scale_bytes = (size_t)((rows + 127) / 128) * words_of(fmt, K) * 512;
+    return COLI_OK;
+}
+
+int coli_moe_fp4_quantize(coli_fp4 fmt, const void* x, coli_dtype xt, int64_t n_src, int64_t rows, int32_t K,
+                          coli_act act, const int32_t* src, const int32_t* count, const float* gscale, void* codes,
+                          void* scales, void* values, coli_stream_t stream) {
+    const int rc = fp4_ok("fp4_quantize", fmt, rows, K);
+    if (rc) return rc;
+    if (xt != COLI_F32 && xt != COLI_BF16) return fail(COLI_E_INVAL, "fp4_quantize: bad dtype");
+    if (act != COLI_ACT_NONE && act != COLI_ACT_SWIGLU) return fail(COLI_E_INVAL, "fp4_quantize: bad act %d", (int)act);
+    if (gscale && fmt == COLI_MXFP4) return fail(COLI_E_INVAL, "fp4_quantize: MXFP4 has no f32 scale");
+    if (n_src < 0 || (!src && n_src < rows))
+        return fail(COLI_E_INVAL, "fp4_quantize: %lld source rows", (long long)n_src);
+    if (rows == 0) return COLI_OK;
+    if ((!x && n_src > 0) || !codes || !scales) return fail(COLI_E_INVAL, "fp4_quantize: NULL pointer");
+    if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) || !aligned16(values))
+        return fail(COLI_E_INVAL, "fp4_quantize: buffers must be 16-byte aligned");
+    Fp4QuantArgs a;
+    a.n_src = n_src; a.rows = rows;
+    a.K = K; a.words = words_of(fmt, K);
+    a.swiglu = act == COLI_ACT_SWIGLU;
+    a.src = src; a.count = count; a.gscale = gscale;
+    a.codes = static_cast<uint8_t*>(codes);
+    a.scales = static_cast<uint32_t*>(scales);
+    const int64_t warps = rows * ((K + 255) / 256), ctas = (warps + 7) / 8;
+    if (ctas > INT32_MAX) return fail(COLI_E_UNSUPPORTED, "fp4_quantize: %lld x %d is too large", (long long)rows, K);
+    const dim3 grid((unsigned)ctas);
+    if (xt == COLI_F32)
+        return launch_pdl(fmt == COLI_NVFP4 ? fp4_quantize_kernel<float, true> : fp4_quantize_kernel<float, false>, grid,
+                          256, 0, S(stream), "fp4 quantize", a, (const float*)x, (float*)values);
+    return launch_pdl(fmt == COLI_NVFP4 ? fp4_quantize_kernel<__nv_bfloat16, true>
+                                        : fp4_quantize_kernel<__nv_bfloat16, false>,
+                      grid, 256, 0, S(stream), "fp4 quantize", a, (const __nv_bfloat16*)x, (__nv_bfloat16*)values);
+}
+
+int coli_moe_fp4_product_workspace_size(coli_fp4 fmt, int64_t P, int32_t K, int32_t E, int32_t R, size_t* bytes) {
+    const int rc = fp4_ok("fp4_product", fmt, P, K);
+    if (rc) return rc;
+    if (!bytes) return fail(COLI_E_INVAL, "fp4_product_workspace_size: NULL pointer");
+    if (E < 1 || E > kFpMaxE || R < 1 || (E > 1 && R % 128) || (int64_t)E * R > INT32_MAX)
+        return fail(COLI_E_INVAL, "fp4_product: bad sizes E=%d R=%d", E, R);
+    *bytes = kFpHeadBytes + (size_t)kMaxGrid * 2 * 128 * tile_rows(P, E) * 4;
+    return COLI_OK;
+}
+
+int coli_moe_fp4_product(coli_fp4 fmt, const void* x_codes, const void* x_scales, int64_t P, int32_t K,
+                         const void* w_codes, const void* w_scales, int32_t E, int32_t R, const int32_t* offsets,
+                         const float* alpha, void* y, coli_dtype yt, void* ws, size_t ws_bytes, coli_stream_t stream) {
+    size_t need;
+    const int rc = coli_moe_fp4_product_workspace_size(fmt, P, K, E, R, &need);
+    if (rc) return rc;
+    if (yt != COLI_F32 && yt != COLI_BF16) return fail(COLI_E_INVAL, "fp4_product: bad dtype");
+    if (!offsets && E > 1) return fail(COLI_E_INVAL, "fp4_product: %d experts need offsets", E);
+    if (P == 0) return COLI_OK;
+    if (!x_codes || !x_scales || !w_codes || !w_scales || !y) return fail(COLI_E_INVAL, "fp4_product: NULL pointer");
+    if (!aligned16(x_codes) || !aligned16(x_scales) || !aligned16(w_codes) || !aligned16(w_scales))
+        return fail(COLI_E_INVAL, "fp4_product: codes and scales must be 16-byte aligned");
+    if (!ws || ws_bytes < need || !aligned16(ws))
+        return fail(COLI_E_WORKSPACE, "fp4_product: workspace of %zu bytes, %zu needed", ws ? ws_bytes : 0, need);
+    FpArgs a;
+    a.xs = static_cast<const uint32_t*>(x_scales);
+    a.ws = static_cast<const uint8_t*>(w_scales);
+    a.P = P;
+    a.K = K; a.E = E; a.R = R;
+    a.KS = (K + 255) / 256;
+    a.xwords = a.wwords = words_of(fmt, K);
+    a.offsets = offsets; a.alpha = alpha;
+    a.err = static_cast<int32_t*>(ws);
+    a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kFpHeadBytes);
+    if (tile_rows(P, E) == kFpLargeNT)
+        return launch_product_t<kFpLargeNT>(fmt, yt, a, x_codes, w_codes, y, S(stream));
+    return launch_product_t<kFpSmallNT>(fmt, yt, a, x_codes, w_codes, y, S(stream));
+}
+
+int coli_moe_fp4_product_status(const void* ws, int32_t* flags, coli_stream_t stream) {
+    if (!ws || !flags) return fail(COLI_E_INVAL, "fp4_product_status: NULL pointer");
+    int32_t f = 0;
+    cudaError_t e = cudaMemcpyAsync(&f, ws, 4, cudaMemcpyDeviceToHost, S(stream));
+    if (e == cudaSuccess) e = cudaStreamSynchronize(S(stream));
+    if (e != cudaSuccess) return fail(COLI_E_CUDA, "fp4_product_status: %s", cudaGetErrorString(e));
+    *flags = f;
+    if (f & kErrWaitTimeout) return fail(COLI_E_TIMEOUT, "fp4_product: a bounded wait gave up");
+    return COLI_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,168 @@
+"""Refusals of the operators around the experts (status codes before any launch),
+their sizes, and the plain 4-bit formats that the GPU tests use.  No GPU."""
+import ctypes
+import math
+
+import numpy as np
+import pytest
+
+import int4_routed_expert_top_b200 as cm
+from tests import fp4_format as ff
+
+INVAL, UNSUPPORTED, WORKSPACE = -1, -4, -5
+A = 1 << 20  # an aligned address that no refused call touches
+
+
+def code(name, *args):
+    return getattr(cm.lib, name)(*args)
+
+
+SORT = dict(idx=A, w=None, T=4, k=2, E=8, off=A, tok=A, slot=A, inv=A, ws=None, n=0, s=None)
+DISPATCH = dict(x=A, xt=0, T=4, H=64, k=2, inv=A, xs=A, s=None)
+COMBINE = dict(o=A, ot=0, T=4, H=64, k=2, inv=A, w=A, res=None, y=A, yt=0, s=None)
+COMBINE_B = dict(dy=A, yt=0, o=A, ot=0, T=4, H=64, k=2, inv=A, w=A, do=A, dw=A, s=None)
+QUANT = dict(fmt=0, x=A, xt=0, n=8, rows=8, K=64, act=0, src=None, count=None, g=None, c=A, sc=A, v=None, s=None)
+PRODUCT = dict(fmt=0, xc=A, xs=A, P=8, K=64, wc=A, ws=A, E=2, R=128, off=A, al=None, y=A, yt=0, w=A,
+               n=1 << 40, s=None)
+
+
+@pytest.mark.parametrize("name,good,change,want", [
+    ("coli_moe_sort", SORT, dict(idx=None), INVAL),
+    ("coli_moe_sort", SORT, dict(off=None), INVAL),
+    ("coli_moe_sort", SORT, dict(inv=None), INVAL),
+    ("coli_moe_sort", SORT, dict(k=0), INVAL),
+    ("coli_moe_sort", SORT, dict(k=33), INVAL),
+    ("coli_moe_sort", SORT, dict(E=0), INVAL),
+    ("coli_moe_sort", SORT, dict(E=1025), INVAL),
+    ("coli_moe_sort", SORT, dict(T=-1), INVAL),
+    ("coli_moe_sort", SORT, dict(T=1 << 30), INVAL),
+    ("coli_moe_sort", SORT, dict(T=8192, k=8), WORKSPACE),
+    ("coli_moe_sort", SORT, dict(T=8192, k=8, ws=A, n=4), WORKSPACE),
+    ("coli_moe_dispatch", DISPATCH, dict(x=None), INVAL),
+    ("coli_moe_dispatch", DISPATCH, dict(xs=None), INVAL),
+    ("coli_moe_dispatch", DISPATCH, dict(xt=2), INVAL),
+    ("coli_moe_dispatch", DISPATCH, dict(H=0), INVAL),
+    ("coli_moe_dispatch", DISPATCH, dict(T=1 << 24, k=32, H=1 << 17), INVAL),
+    ("coli_moe_dispatch_backward", DISPATCH, dict(inv=None), INVAL),
+    ("coli_moe_combine", COMBINE, dict(o=None), INVAL),
+    ("coli_moe_combine", COMBINE, dict(y=None), INVAL),
+    ("coli_moe_combine", COMBINE, dict(yt=7), INVAL),
+    ("coli_moe_combine_backward", COMBINE_B, dict(dy=None), INVAL),
+    ("coli_moe_combine_backward", COMBINE_B, dict(do=None, dw=None), INVAL),
+    ("coli_moe_combine_backward", COMBINE_B, dict(o=None), INVAL),
+    ("coli_moe_fp4_quantize", QUANT, dict(fmt=2), INVAL),
+    ("coli_moe_fp4_quantize", QUANT, dict(K=48), INVAL),
+    ("coli_moe_fp4_quantize", QUANT, dict(K=0), INVAL),
+    ("coli_moe_fp4_quantize", QUANT, dict(rows=-1), INVAL),
+    ("coli_moe_fp4_quantize", QUANT, dict(n=7), INVAL),
+    ("coli_moe_fp4_quantize", QUANT, dict(act=2), INVAL),
+    ("coli_moe_fp4_quantize", QUANT, dict(g=A), INVAL),
+    ("coli_moe_fp4_quantize", QUANT, dict(x=A + 8), INVAL),
+    ("coli_moe_fp4_quantize", QUANT, dict(v=A + 4), INVAL),
+    ("coli_moe_fp4_quantize", QUANT, dict(c=None), INVAL),
+    ("coli_moe_fp4_product", PRODUCT, dict(R=100), INVAL),
+    ("coli_moe_fp4_product", PRODUCT, dict(E=1025), INVAL),
+    ("coli_moe_fp4_product", PRODUCT, dict(off=None), INVAL),
+    ("coli_moe_fp4_product", PRODUCT, dict(K=100), INVAL),
+    ("coli_moe_fp4_product", PRODUCT, dict(yt=3), INVAL),
+    ("coli_moe_fp4_product", PRODUCT, dict(E=1 << 9, R=1 << 23), INVAL),
+    ("coli_moe_fp4_product", PRODUCT, dict(xc=A + 4), INVAL),
+    ("coli_moe_fp4_product", PRODUCT, dict(y=None), INVAL),
+    ("coli_moe_fp4_product", PRODUCT, dict(w=None), WORKSPACE),
+    ("coli_moe_fp4_product", PRODUCT, dict(n=1000), WORKSPACE),
+])
+def test_refusals(name, good, change, want):
+    assert code(name, *{**good, **change}.values()) == want
+    assert cm.coli_moe_last_error()
+
+
+def norm(**kw):
+    d = dict(H=64, xt=0, bt=1, post_norm=1, gate_kind=1, alpha=1.0, eps=1e-5, post_gain=A, pre_gain=A)
+    d.update(kw)
+    return ctypes.byref(cm.NormDesc(*d.values()))
+
+
+NORM = dict(desc=norm(), x=A, o=A, gate=A, T=4, xo=A, no=A, rp=None, rx=None, s=None)
+NORM_B = dict(desc=norm(), xo=A, o=A, gate=A, T=4, rp=A, rx=A, dxo=A, dn=A, dx=A, do=A, dpost=A, dgate=A, dpre=A,
+              ws=A, n=1 << 40, s=None)
+
+
+@pytest.mark.parametrize("name,good,change,want", [
+    ("coli_moe_block_norm", NORM, dict(desc=None), INVAL),
+    ("coli_moe_block_norm", NORM, dict(desc=norm(H=0)), INVAL),
+    ("coli_moe_block_norm", NORM, dict(desc=norm(H=16385)), INVAL),
+    ("coli_moe_block_norm", NORM, dict(desc=norm(xt=1, bt=0)), UNSUPPORTED),
+    ("coli_moe_block_norm", NORM, dict(desc=norm(gate_kind=4)), INVAL),
+    ("coli_moe_block_norm", NORM, dict(desc=norm(eps=0.0)), INVAL),
+    ("coli_moe_block_norm", NORM, dict(desc=norm(eps=math.nan)), INVAL),
+    ("coli_moe_block_norm", NORM, dict(desc=norm(alpha=math.inf)), INVAL),
+    ("coli_moe_block_norm", NORM, dict(gate=None), INVAL),
+    ("coli_moe_block_norm", NORM, dict(desc=norm(gate_kind=0)), INVAL),
+    ("coli_moe_block_norm", NORM, dict(x=None), INVAL),
+    ("coli_moe_block_norm", NORM, dict(xo=None), INVAL),
+    ("coli_moe_block_norm", NORM, dict(o=None, no=None), INVAL),
+    ("coli_moe_block_norm", NORM, dict(T=-1), INVAL),
+    ("coli_moe_block_norm_backward", NORM_B, dict(dx=None), INVAL),
+    ("coli_moe_block_norm_backward", NORM_B, dict(dxo=None, dn=None), INVAL),
+    ("coli_moe_block_norm_backward", NORM_B, dict(do=None), INVAL),
+    ("coli_moe_block_norm_backward", NORM_B, dict(o=None), INVAL),
+    ("coli_moe_block_norm_backward", NORM_B, dict(rx=None), INVAL),
+    ("coli_moe_block_norm_backward", NORM_B, dict(rp=None), INVAL),
+    ("coli_moe_block_norm_backward", NORM_B, dict(desc=norm(post_norm=0)), INVAL),   # dpost_gain asked for
+    ("coli_moe_block_norm_backward", NORM_B, dict(desc=norm(gate_kind=0), gate=None), INVAL),
+    ("coli_moe_block_norm_backward", NORM_B, dict(ws=None), WORKSPACE),
+    ("coli_moe_block_norm_backward", NORM_B, dict(n=16), WORKSPACE),
+])
+def test_norm_refusals(name, good, change, want):
+    assert code(name, *{**good, **change}.values()) == want
+    assert cm.coli_moe_last_error()
+
+
+def test_nothing_to_do_succeeds():
+    assert code("coli_moe_dispatch", *{**DISPATCH, "T": 0, "x": None}.values()) == 0
+    assert code("coli_moe_combine", *{**COMBINE, "T": 0}.values()) == 0
+    assert code("coli_moe_combine_backward", *{**COMBINE_B, "T": 0}.values()) == 0
+    assert code("coli_moe_block_norm", *{**NORM, "T": 0}.values()) == 0
+    assert code("coli_moe_fp4_quantize", *{**QUANT, "rows": 0}.values()) == 0
+    assert code("coli_moe_fp4_product", *{**PRODUCT, "P": 0}.values()) == 0
+
+
+def test_sizes():
+    assert cm.coli_moe_sort_workspace_size(1, 8, 256) == 0
+    assert cm.coli_moe_sort_workspace_size(8192, 8, 256) >= 256 * 4
+    assert cm.coli_moe_fp4_bytes(cm.COLI_MXFP4, 130, 160) == (130 * 80, 2 * 2 * 512)
+    assert cm.coli_moe_fp4_bytes(cm.COLI_NVFP4, 130, 160) == (130 * 80, 2 * 3 * 512)
+    small = cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, 8, 64, 256, 128)
+    assert small < cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, 1 << 16, 64, 32, 128)
+
+
+def test_plain_format_hand_values():
+    # one block of each kind by hand: max 6.5 = 1.625 * 2^2 -> scale 2^0, 6.5 saturates to 6;
+    # 2.5, 0.25, 5 tie to even (2, 0, 4); 3.5 -> 4; -0.75 -> -1
+    x = np.zeros((1, 32), np.float32)
+    x[0, :8] = [6.5, 2.5, 0.25, 5.0, 3.5, -0.75, 1.25, -1.75]
+    codes, byte, val = ff.quantize(x, "mx")
+    assert byte.tolist() == [[127]]
+    assert val[0, :8].tolist() == [6, 2, 0, 4, 4, -1, 1, -2]
+    assert codes[0, :4].tolist() == [7 | 4 << 4, 0 | 6 << 4, 6 | 10 << 4, 2 | 12 << 4]
+    # max 12 with g = 1: s = 2, exactly representable
+    x = np.zeros((1, 16), np.float32)
+    x[0, :4] = [12, 5, -1, 0.5]
+    codes, byte, val = ff.quantize(x, "nv")
+    assert ff.E4M3[byte[0, 0]] == 2 and val[0, :4].tolist() == [12, 4, -1, 0]  # 2.5 and 0.25 tie to even
+
+
+def test_plain_format_round_trip_and_layout():
+    rng = np.random.default_rng(5)
+    for fmt in ("mx", "nv"):
+        x = rng.standard_normal((133, 160)).astype(np.float32)
+        codes, byte, val = ff.quantize(x, fmt)
+        again = ff.quantize(val, fmt)  # the values are representable: blocks keep their largest magnitude
+        np.testing.assert_array_equal(ff.values(codes, byte, fmt).astype(np.float32), val)
+        np.testing.assert_array_equal(ff.untile_scales(ff.tile_scales(byte), 133, byte.shape[1])[:, :byte.shape[1]], byte)
+        if fmt == "nv":
+            np.testing.assert_array_equal(again[2], val)
+        # a magnitude is within half of the widest step (2) below 6, or saturated
+        err = np.abs(val - x)
+        d = np.repeat(np.abs(x).reshape(133, -1, ff.BLOCK[fmt]).max(2), ff.BLOCK[fmt], 1)
+        assert (err <= 0.26 * d).all()

@@ -1,0 +1,230 @@
+"""The 4-bit floating point quantiser (bit for bit) and the grouped product against
+their plain forms."""
+import numpy as np
+import pytest
+import torch
+
+import int4_routed_expert_top_b200 as cm
+from tests import fp4_format as ff
+
+pytestmark = pytest.mark.gpu
+
+FMT = {"mx": cm.COLI_MXFP4, "nv": cm.COLI_NVFP4}
+F, B = torch.float32, torch.bfloat16
+HALF = {F: 2.0 ** -24, B: 2.0 ** -8}
+
+
+def dev(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def quantize(fmt, x, rows, K, fill=0xAA, **kw):
+    nc, ns = cm.coli_moe_fp4_bytes(FMT[fmt], rows, K)
+    codes = torch.full((nc,), fill, dtype=torch.uint8, device="cuda")
+    scales = torch.full((ns,), fill, dtype=torch.uint8, device="cuda")
+    cm.coli_moe_fp4_quantize(FMT[fmt], x, rows, K, codes, scales, **kw)
+    return codes, scales
+
+
+def check_codes(fmt, codes, scales, want, rows, K):
+    c0, b0, _ = want
+    np.testing.assert_array_equal(codes.cpu().numpy().reshape(rows, K // 2), c0)
+    nb = K // ff.BLOCK[fmt]
+    got = ff.untile_scales(scales.cpu().numpy(), rows, nb)
+    np.testing.assert_array_equal(got[:, :nb], b0)
+    assert (got[:, nb:] == 0).all()   # blocks past the row's end
+
+
+def hard_rows(K, seed=1):
+    """Rows of every sort: ordinary, ties, powers of two, tiny, huge, zero, outliers."""
+    rng = np.random.default_rng(seed)
+    rows = [rng.standard_normal(K), rng.standard_normal(K) * 2.0 ** rng.integers(-12, 12, K), np.zeros(K),
+            rng.choice([0.25, 0.75, 1.25, 1.75, 2.5, 3.5, 5.0, 6.0, 7.0, 8.0, -0.25, -5.0], K),
+            2.0 ** rng.integers(-6, 7, K).astype(float), np.full(K, 1e-38), np.full(K, -3e38),
+            rng.standard_normal(K) * 1e-40, np.where(np.arange(K) % 37 == 0, 300.0, 1e-3), -np.zeros(K),
+            rng.standard_normal(K) * 1e-30, np.full(K, 6.0 * 448)]
+    return np.stack(rows).astype(np.float32)
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("dt", [F, B])
+@pytest.mark.parametrize("K", [32, 64, 96, 160, 256, 288, 1024, 6144])
+def test_quantize_bits(fmt, dt, K):
+    x = dev(hard_rows(K)).to(dt)
+    rows = x.shape[0]
+    for g in ([None] if fmt == "mx" else [None, 0.0125, 2.0 ** -20, 3.7]):
+        want = ff.quantize(x.float().cpu().numpy(), fmt, g)
+        gs = None if g is None else torch.tensor([g], device="cuda")
+        vals = torch.full((rows, K), 9.0, dtype=dt, device="cuda")
+        codes, scales = quantize(fmt, x, rows, K, gscale=gs, values=vals)
+        check_codes(fmt, codes, scales, want, rows, K)
+        assert torch.equal(vals, dev(want[2]).to(dt))
+        c2, s2 = quantize(fmt, x, rows, K, gscale=gs)
+        assert torch.equal(c2, codes)
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("rows", [1, 127, 128, 129, 300])
+def test_quantize_many_rows(fmt, rows):
+    x = np.random.default_rng(rows).standard_normal((rows, 224)).astype(np.float32)
+    codes, scales = quantize(fmt, dev(x), rows, 224)
+    check_codes(fmt, codes, scales, ff.quantize(x, fmt), rows, 224)
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_quantize_blocks_without_a_number(fmt):
+    x = np.random.default_rng(2).standard_normal((4, 128)).astype(np.float32)
+    x[0, 5], x[1, 40], x[2, 100] = np.inf, -np.inf, np.nan
+    vals = torch.empty(4, 128, device="cuda")
+    codes, scales = quantize(fmt, dev(x), 4, 128, values=vals)
+    want = ff.quantize(x, fmt)
+    check_codes(fmt, codes, scales, want, 4, 128)
+    assert np.array_equal(vals.cpu().numpy(), want[2], equal_nan=True) and np.isnan(want[2]).any()
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("act", [cm.COLI_ACT_NONE, cm.COLI_ACT_SWIGLU])
+def test_quantize_picked_rows_and_count(fmt, act):
+    K, n, rows = 96, 5, 9
+    x = np.random.default_rng(3).integers(-8, 9, (n, K * (1 + act))).astype(np.float32)
+    src = np.array([4, 0, 0, 2, -1, 5, 3, 1, 2], np.int32)
+    count = torch.tensor([7], dtype=torch.int32, device="cuda")
+    nc, ns = cm.coli_moe_fp4_bytes(FMT[fmt], rows, K)
+    codes, scales = (torch.full((m,), 0xAA, dtype=torch.uint8, device="cuda") for m in (nc, ns))
+    vals = torch.full((rows, K), 9.0, device="cuda")
+    cm.coli_moe_fp4_quantize(FMT[fmt], dev(x), rows, K, codes, scales, act=act, src=dev(src), count=count, values=vals)
+    if act:
+        # the same SwiGLU in f32 through the library's plain rows: any rounding of silu is its own
+        t = dev(x)
+        a = t[:, :K]
+        x = ((a / (1 + torch.exp(-a))) * t[:, K:]).cpu().numpy()
+    rowsx = np.where(((src >= 0) & (src < n))[:, None], x[np.clip(src, 0, n - 1)], 0)
+    _, _, v = ff.quantize(rowsx, fmt)
+    got = vals.cpu().numpy()
+    assert (got[7:] == 9.0).all() and (codes.cpu().numpy().reshape(rows, -1)[7:] == 0xAA).all()
+    assert (got[4:6] == 0).all()
+    if not act:
+        np.testing.assert_array_equal(got[:7], v[:7])
+    else:
+        # silu to a few roundings: a value may land one code further where it is next to a
+        # tie: half the widest step (2 of 6) more than the rounding itself, on few values
+        amax = np.repeat(np.abs(rowsx).reshape(rows, -1, ff.BLOCK[fmt]).max(2), ff.BLOCK[fmt], 1)
+        assert (np.abs(got[:7] - v[:7]) <= 0.5 * amax[:7]).all()
+        assert (got[:7] != v[:7]).mean() <= 0.01
+
+
+def weights(fmt, n, K, rng, wide=False):
+    """Random codes and scale bytes (as values up to 2^4)."""
+    codes = rng.integers(0, 256, (n, K // 2)).astype(np.uint8)
+    nb = K // ff.BLOCK[fmt]
+    if fmt == "mx":
+        byte = rng.integers(100 if wide else 123, 150 if wide else 130, (n, nb))
+    else:
+        byte = rng.integers(1 if wide else 0x30, 0x7F if wide else 0x48, (n, nb))
+    return codes, byte.astype(np.uint8)
+
+
+def product(fmt, xc, xb, wc, wb, E, R, offsets, alpha, yt, P, K, fill=9.0):
+    y = torch.full((P, R), fill, dtype=yt, device="cuda")
+    ws = torch.full((cm.coli_moe_fp4_product_workspace_size(FMT[fmt], P, K, E, R),), 255, dtype=torch.uint8, device="cuda")
+    off = None if offsets is None else dev(np.asarray(offsets, np.int32))
+    args = (FMT[fmt], dev(xc.reshape(-1)), dev(ff.tile_scales(xb)), P, K, dev(wc.reshape(-1)), dev(ff.tile_scales(wb)), E, R)
+    cm.coli_moe_fp4_product(*args, y, ws, offsets=off, alpha=None if alpha is None else dev(alpha))
+    assert cm.coli_moe_fp4_product_status(ws) == 0
+    return y
+
+
+def check_product(fmt, E, R, K, sizes, yt=F, seed=0, wide=False, alpha=True):
+    rng = np.random.default_rng(seed)
+    offsets = np.concatenate([[0], np.cumsum(sizes)])
+    P = int(offsets[-1]) + (3 if E > 1 else 0)   # rows behind the last expert's
+    xc, xb = weights(fmt, P, K, rng, wide)
+    wc, wb = weights(fmt, E * R, K, rng, wide)
+    al = (0.5 + rng.random(E)).astype(np.float32) if alpha else None
+    y = product(fmt, xc, xb, wc, wb, E, R, offsets if E > 1 else None, al, yt, P, K)
+    X, W = dev(ff.values(xc, xb, fmt)), dev(ff.values(wc, wb, fmt))
+    off2 = 0.0
+    for e in range(E):
+        lo, hi = int(offsets[e]), int(offsets[e + 1])
+        a = 1.0 if al is None else float(al[e])
+        w = W[e * R:(e + 1) * R]
+        want, size = a * (X[lo:hi] @ w.T), a * (X[lo:hi].abs() @ w.abs().T)
+        err = (y[lo:hi].double() - want).abs()
+        # products are exact; one addition into the f32 accumulator per 64 columns, each off by
+        # at most two units of the last place of a partial sum (2^-22 of the terms' size), the
+        # joined pieces, the factor and the output's rounding
+        bound = (-(-K // 64) + 24) * 2.0 ** -22 * size + HALF[yt] * want.abs()
+        assert (err <= bound + 1e-30).all(), (e, float((err - bound).max()))
+        off2 += float(err.square().sum() / want.square().sum().clamp(min=1e-30)) / E if hi > lo else 0.0
+    assert (y[int(offsets[-1]):] == 9.0).all()
+    return off2 ** 0.5
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("R,K,n", [(128, 256, 1), (128, 32, 3), (128, 64, 16), (1, 256, 1), (5, 96, 2), (130, 160, 17),
+                                   (256, 512, 33), (384, 288, 48), (200, 1056, 31), (6144, 2048, 1)])
+def test_product_one_group(fmt, R, K, n):
+    for yt in (F, B):
+        check_product(fmt, 1, R, K, [n], yt)
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("R,K,n", [(128, 256, 49), (128, 512, 128), (256, 288, 129), (100, 1024, 192), (384, 2048, 193),
+                                   (1000, 96, 500), (256, 6144, 400)])
+def test_product_one_group_many_rows(fmt, R, K, n):
+    for yt in (F, B):
+        check_product(fmt, 1, R, K, [n], yt)
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("R,K,sizes", [
+    (128, 256, [0, 1, 0, 5, 2, 0]), (256, 512, [0] * 30 + [1] + [0] * 33), (128, 96, [31, 32, 33, 64, 65]),
+    (256, 1024, [7] * 9), (128, 512, [0, 300, 0, 1, 200, 17]), (384, 2048, [130, 259, 5, 0]),
+    (128, 64, [1] * 1024), (4096, 256, [1, 0, 0, 1, 1, 0, 2, 0] * 4)])
+def test_product_groups(fmt, R, K, sizes):
+    for yt in (F, B):
+        check_product(fmt, len(sizes), R, K, sizes, yt, seed=len(sizes))
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_product_wide_scales_and_no_alpha(fmt):
+    check_product(fmt, 3, 256, 512, [4, 70, 9], wide=True, alpha=False)
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_product_accuracy(fmt):
+    """The sum over 6144 columns in f32: near the rounding of one f32 sum, for few and many rows."""
+    assert check_product(fmt, 1, 256, 6144, [5]) <= 5e-6
+    assert check_product(fmt, 1, 256, 6144, [300]) <= 5e-6
+
+
+def test_product_nan_scale_stays_in_its_row():
+    rng = np.random.default_rng(8)
+    xc, xb = weights("mx", 40, 256, rng)
+    wc, wb = weights("mx", 256, 256, rng)
+    xb[7, 3], wb[100, 0] = 255, 255
+    y = product("mx", xc, xb, wc, wb, 1, 256, None, None, F, 40, 256).cpu().numpy()
+    want = np.zeros((40, 256), bool)
+    want[7], want[:, 100] = True, True
+    np.testing.assert_array_equal(np.isnan(y), want)
+
+
+def test_product_offsets_out_of_range_stay_in_bounds():
+    rng = np.random.default_rng(9)
+    xc, xb = weights("nv", 10, 128, rng)
+    wc, wb = weights("nv", 4 * 128, 128, rng)
+    good = product("nv", xc, xb, wc, wb, 4, 128, [0, 2, 5, 10, 10], None, F, 10, 128)
+    same = product("nv", xc, xb, wc, wb, 4, 128, [-3, 2, 5, 99, 50], None, F, 10, 128)
+    assert torch.equal(good, same)
+
+
+def test_product_is_the_same_every_time():
+    rng = np.random.default_rng(10)
+    xc, xb = weights("mx", 700, 1024, rng)
+    wc, wb = weights("mx", 8 * 256, 1024, rng)
+    off = [0, 100, 100, 350, 360, 400, 650, 651, 700]
+    a = product("mx", xc, xb, wc, wb, 8, 256, off, None, F, 700, 1024)
+    for _ in range(3):
+        assert torch.equal(a, product("mx", xc, xb, wc, wb, 8, 256, off, None, F, 700, 1024))
+    assert float((a[400:650] - product("mx", xc[400:650], xb[400:650], wc[5 * 256:6 * 256], wb[5 * 256:6 * 256], 1, 256,
+                                       None, None, F, 250, 1024)).abs().max()) <= 1e-5 * float(a.abs().max())
