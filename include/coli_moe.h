@@ -571,9 +571,9 @@ int coli_moe_fp4_bytes(coli_fp4 fmt, int64_t rows, int32_t K, size_t* code_bytes
                        size_t* scale_bytes);
 
 /* Quantise rows.  x device of type xt, [n_src, K] (SwiGLU: [n_src, 2K]),
- * 16-byte aligned; row r comes from x[src[r]] (src device i32 [rows]; an entry outside
- * [0, n_src) gives a row of zeros) or, with src NULL, from x[r] (n_src >=
- * rows).  count (device i32 or NULL): only rows r < *count are written, e.g.
+ * 32-byte aligned (as is values); row r comes from x[src[r]] (src device i32
+ * [rows]; an entry outside [0, n_src) gives a row of zeros) or, with src NULL,
+ * from x[r] (n_src >= rows).  count (device i32 or NULL): only rows r < *count are written, e.g.
  * offsets + E of coli_moe_sort.  gscale (device f32, NULL: 1) is NVFP4's g,
  * positive and finite, at least 2^-100; MXFP4 takes NULL only.  values (device,
  * [rows, K] of type xt, or NULL) receives what codes and scales stand for,

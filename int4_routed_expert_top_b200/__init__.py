@@ -420,51 +420,62 @@ def coli_moe_forward_noalloc(layer, x, T, y, stream=None):
 # the sizes given, so that a wrong shape raises here instead of reading past a
 # buffer on the device.
 # ---------------------------------------------------------------------------
-def _buf(name, a, dtype, count):
-    """Address of a contiguous CUDA tensor of `count` elements of dtype (None passes)."""
+_torch = None
+
+
+def _device():
+    """Index of the current CUDA device."""
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+        _torch.cuda.init()
+    return _torch._C._cuda_getDevice()
+
+
+def _queue(s, dev):
+    """Address of the stream s, or of the current one of the device."""
+    if s is None:
+        return _torch._C._cuda_getCurrentRawStream(dev)
+    return s if isinstance(s, int) else s.cuda_stream
+
+
+def _buf(name, a, dtype, count, dev):
+    """Address of a contiguous tensor of at least `count` elements of dtype on the CUDA device
+    dev (None passes)."""
     if a is None:
         return None
+    if a.dtype is dtype and a.is_cuda and a.get_device() == dev and a.is_contiguous() and a.numel() >= count:
+        return a.data_ptr()
     if a.dtype != dtype:
         raise TypeError(f"{name}: {a.dtype}, expected {dtype}")
-    if a.numel() < count or not a.is_contiguous():
-        raise ValueError(f"{name}: {tuple(a.shape)} (contiguous: {a.is_contiguous()}), "
-                         f"expected {count} contiguous elements")
-    if not a.is_cuda or a.device.index != _current_device():
-        raise ValueError(f"{name}: on {a.device}, expected the current CUDA device")
-    return a.data_ptr()
+    if not a.is_cuda or a.get_device() != dev:
+        raise ValueError(f"{name}: on {a.device}, expected the current CUDA device {dev}")
+    raise ValueError(f"{name}: {tuple(a.shape)} (contiguous: {a.is_contiguous()}), expected {count} contiguous elements")
 
 
-def _current_device():
-    import torch
-    return torch.cuda.current_device()
+def _raw(name, a, count, dev):
+    return _buf(name, a, _torch.uint8, count, dev)
 
 
-def _raw(name, a, count):
-    import torch
-    return _buf(name, a, torch.uint8, count)
+def _i32(name, a, count, dev):
+    return _buf(name, a, _torch.int32, count, dev)
 
 
-def _i32(name, a, count):
-    import torch
-    return _buf(name, a, torch.int32, count)
-
-
-def _f32(name, a, count):
-    import torch
-    return _buf(name, a, torch.float32, count)
+def _f32(name, a, count, dev):
+    return _buf(name, a, _torch.float32, count, dev)
 
 
 def _code_of(dtype):
-    import torch
-    if dtype == torch.float32:
-        return COLI_F32
-    if dtype == torch.bfloat16:
+    if dtype is _torch.bfloat16:
         return COLI_BF16
+    if dtype is _torch.float32:
+        return COLI_F32
     raise TypeError(f"rows must be float32 or bfloat16, got {dtype}")
 
 
-def _workspace(ws):
-    return (None, 0) if ws is None else (_raw("ws", ws, 0), ws.numel())
+def _workspace(ws, dev):
+    return (None, 0) if ws is None else (_raw("ws", ws, 0, dev), ws.numel())
 
 
 def coli_moe_sort_workspace_size(T: int, k: int, E: int) -> int:
@@ -475,30 +486,35 @@ def coli_moe_sort_workspace_size(T: int, k: int, E: int) -> int:
 
 def coli_moe_sort(idx, T, k, E, offsets, pair_tok, pair_slot, inv, ws, w=None, stream=None):
     """pair_tok and pair_slot may be None; ws: uint8 of coli_moe_sort_workspace_size bytes."""
-    p, n = _workspace(ws)
-    _ok(lib.coli_moe_sort(_i32("idx", idx, T * k), _f32("w", w, T * k), T, k, E,
-                          _i32("offsets", offsets, E + 1), _i32("pair_tok", pair_tok, T * k),
-                          _i32("pair_slot", pair_slot, T * k), _i32("inv", inv, T * k), p, n,
-                          _stream(stream)))
+    d, n = _device(), T * k
+    p, size = _workspace(ws, d)
+    _ok(lib.coli_moe_sort(_i32("idx", idx, n, d), _f32("w", w, n, d), T, k, E,
+                          _i32("offsets", offsets, E + 1, d), _i32("pair_tok", pair_tok, n, d),
+                          _i32("pair_slot", pair_slot, n, d), _i32("inv", inv, n, d), p, size,
+                          _queue(stream, d)))
 
 
 def coli_moe_dispatch(x, T, H, k, inv, xs, stream=None):
-    _ok(lib.coli_moe_dispatch(_buf("x", x, x.dtype, T * H), _code_of(x.dtype), T, H, k,
-                              _i32("inv", inv, T * k), _buf("xs", xs, x.dtype, T * k * H),
-                              _stream(stream)))
+    d = _device()
+    _ok(lib.coli_moe_dispatch(_buf("x", x, x.dtype, T * H, d), _code_of(x.dtype), T, H, k,
+                              _i32("inv", inv, T * k, d), _buf("xs", xs, x.dtype, T * k * H, d),
+                              _queue(stream, d)))
 
 
 def coli_moe_dispatch_backward(dxs, T, H, k, inv, dx, stream=None):
-    _ok(lib.coli_moe_dispatch_backward(_buf("dxs", dxs, dxs.dtype, T * k * H), _code_of(dxs.dtype),
-                                       T, H, k, _i32("inv", inv, T * k),
-                                       _buf("dx", dx, dxs.dtype, T * H), _stream(stream)))
+    d = _device()
+    _ok(lib.coli_moe_dispatch_backward(_buf("dxs", dxs, dxs.dtype, T * k * H, d),
+                                       _code_of(dxs.dtype), T, H, k, _i32("inv", inv, T * k, d),
+                                       _buf("dx", dx, dxs.dtype, T * H, d), _queue(stream, d)))
 
 
 def coli_moe_combine(o, T, H, k, inv, w, y, residual=None, stream=None):
-    _ok(lib.coli_moe_combine(_buf("o", o, o.dtype, T * k * H), _code_of(o.dtype), T, H, k,
-                             _i32("inv", inv, T * k), _f32("w", w, T * k),
-                             _buf("residual", residual, y.dtype, T * H),
-                             _buf("y", y, y.dtype, T * H), _code_of(y.dtype), _stream(stream)))
+    d = _device()
+    _ok(lib.coli_moe_combine(_buf("o", o, o.dtype, T * k * H, d), _code_of(o.dtype), T, H, k,
+                             _i32("inv", inv, T * k, d), _f32("w", w, T * k, d),
+                             _buf("residual", residual, y.dtype, T * H, d),
+                             _buf("y", y, y.dtype, T * H, d), _code_of(y.dtype),
+                             _queue(stream, d)))
 
 
 def coli_moe_combine_backward(dy, o, T, H, k, inv, w, d_o, dw, stream=None):
@@ -506,56 +522,59 @@ def coli_moe_combine_backward(dy, o, T, H, k, inv, w, d_o, dw, stream=None):
     like = d_o if d_o is not None else o
     if like is None:
         raise ValueError("combine_backward: neither o nor d_o")
-    _ok(lib.coli_moe_combine_backward(_buf("dy", dy, dy.dtype, T * H), _code_of(dy.dtype),
-                                      _buf("o", o, like.dtype, T * k * H), _code_of(like.dtype),
-                                      T, H, k, _i32("inv", inv, T * k), _f32("w", w, T * k),
-                                      _buf("d_o", d_o, like.dtype, T * k * H),
-                                      _f32("dw", dw, T * k), _stream(stream)))
+    d = _device()
+    _ok(lib.coli_moe_combine_backward(_buf("dy", dy, dy.dtype, T * H, d), _code_of(dy.dtype),
+                                      _buf("o", o, like.dtype, T * k * H, d),
+                                      _code_of(like.dtype), T, H, k, _i32("inv", inv, T * k, d),
+                                      _f32("w", w, T * k, d),
+                                      _buf("d_o", d_o, like.dtype, T * k * H, d),
+                                      _f32("dw", dw, T * k, d), _queue(stream, d)))
 
 
-def _norm_types(desc):
-    import torch
-    types = {COLI_F32: torch.float32, COLI_BF16: torch.bfloat16}
-    if desc.xt not in types or desc.bt not in types:
-        raise ValueError(f"NormDesc: types {desc.xt}, {desc.bt}")
-    return types[desc.xt], types[desc.bt]
+def _norm_type(code):
+    if code == COLI_F32:
+        return _torch.float32
+    if code == COLI_BF16:
+        return _torch.bfloat16
+    raise ValueError(f"NormDesc: bad type {code}")
 
 
 def _gate_size(desc, T):
-    return {COLI_GATE_CHANNEL: desc.H, COLI_GATE_TOKEN: T, COLI_GATE_FULL: T * desc.H}.get(
-        desc.gate_kind, 0)
+    kind = desc.gate_kind
+    return (desc.H if kind == COLI_GATE_CHANNEL else T if kind == COLI_GATE_TOKEN
+            else T * desc.H if kind == COLI_GATE_FULL else 0)
 
 
 def coli_moe_block_norm(desc, x, o, T, x_out, n_out, gate=None, rstd_post=None, rstd_pre=None,
                         stream=None):
-    xt, bt = _norm_types(desc)
-    n = T * desc.H
-    _ok(lib.coli_moe_block_norm(ctypes.byref(desc), _buf("x", x, xt, n), _buf("o", o, bt, n),
-                                _f32("gate", gate, _gate_size(desc, T)), T,
-                                _buf("x_out", x_out, xt, n), _buf("n_out", n_out, bt, n),
-                                _f32("rstd_post", rstd_post, T), _f32("rstd_pre", rstd_pre, T),
-                                _stream(stream)))
+    d, n = _device(), T * desc.H
+    xt, bt = _norm_type(desc.xt), _norm_type(desc.bt)
+    _ok(lib.coli_moe_block_norm(desc, _buf("x", x, xt, n, d), _buf("o", o, bt, n, d),
+                                _f32("gate", gate, _gate_size(desc, T), d), T,
+                                _buf("x_out", x_out, xt, n, d), _buf("n_out", n_out, bt, n, d),
+                                _f32("rstd_post", rstd_post, T, d),
+                                _f32("rstd_pre", rstd_pre, T, d), _queue(stream, d)))
 
 
 def coli_moe_block_norm_backward_workspace_size(desc, T: int) -> int:
     out = _SZ()
-    _ok(lib.coli_moe_block_norm_backward_workspace_size(ctypes.byref(desc), T, ctypes.byref(out)))
+    _ok(lib.coli_moe_block_norm_backward_workspace_size(desc, T, ctypes.byref(out)))
     return out.value
 
 
 def coli_moe_block_norm_backward(desc, x_out, o, T, dx_out, dn, dx, d_o, ws, gate=None,
                                  rstd_post=None, rstd_pre=None, dpost_gain=None, dgate=None,
                                  dpre_gain=None, stream=None):
-    xt, bt = _norm_types(desc)
-    n, ng = T * desc.H, _gate_size(desc, T)
-    p, size = _workspace(ws)
+    d, n, ng = _device(), T * desc.H, _gate_size(desc, T)
+    xt, bt = _norm_type(desc.xt), _norm_type(desc.bt)
+    p, size = _workspace(ws, d)
     _ok(lib.coli_moe_block_norm_backward(
-        ctypes.byref(desc), _buf("x_out", x_out, xt, n), _buf("o", o, bt, n),
-        _f32("gate", gate, ng), T, _f32("rstd_post", rstd_post, T), _f32("rstd_pre", rstd_pre, T),
-        _buf("dx_out", dx_out, xt, n), _buf("dn", dn, bt, n), _buf("dx", dx, xt, n),
-        _buf("d_o", d_o, bt, n), _f32("dpost_gain", dpost_gain, desc.H),
-        _f32("dgate", dgate, ng), _f32("dpre_gain", dpre_gain, desc.H), p, size,
-        _stream(stream)))
+        desc, _buf("x_out", x_out, xt, n, d), _buf("o", o, bt, n, d), _f32("gate", gate, ng, d), T,
+        _f32("rstd_post", rstd_post, T, d), _f32("rstd_pre", rstd_pre, T, d),
+        _buf("dx_out", dx_out, xt, n, d), _buf("dn", dn, bt, n, d), _buf("dx", dx, xt, n, d),
+        _buf("d_o", d_o, bt, n, d), _f32("dpost_gain", dpost_gain, desc.H, d),
+        _f32("dgate", dgate, ng, d), _f32("dpre_gain", dpre_gain, desc.H, d), p, size,
+        _queue(stream, d)))
 
 
 def coli_moe_fp4_bytes(fmt: int, rows: int, K: int):
@@ -565,16 +584,25 @@ def coli_moe_fp4_bytes(fmt: int, rows: int, K: int):
     return nc.value, ns.value
 
 
+def _fp4_sizes(fmt, rows, K):
+    """coli_moe_fp4_bytes without a call: the sizes that tensors are checked against here (the
+    library checks fmt, rows and K themselves)."""
+    words = -(-K // (64 if fmt == COLI_NVFP4 else 128))
+    return rows * K // 2, -(-rows // 128) * words * 512
+
+
 def coli_moe_fp4_quantize(fmt, x, rows, K, codes, scales, act=COLI_ACT_NONE, src=None, count=None,
                           gscale=None, values=None, stream=None):
     """x: [n, K] rows ([n, 2K] for SwiGLU), n >= rows unless src picks them."""
-    nc, ns = coli_moe_fp4_bytes(fmt, rows, K)
-    n_src = x.numel() // (2 * K if act == COLI_ACT_SWIGLU else K)
-    _ok(lib.coli_moe_fp4_quantize(fmt, _buf("x", x, x.dtype, 0), _code_of(x.dtype), n_src, rows, K,
-                                  act, _i32("src", src, rows), _i32("count", count, 1),
-                                  _f32("gscale", gscale, 1), _raw("codes", codes, nc),
-                                  _raw("scales", scales, ns),
-                                  _buf("values", values, x.dtype, rows * K), _stream(stream)))
+    d = _device()
+    nc, ns = _fp4_sizes(fmt, rows, K)
+    n_src = x.numel() // max(1, 2 * K if act == COLI_ACT_SWIGLU else K)
+    _ok(lib.coli_moe_fp4_quantize(fmt, _buf("x", x, x.dtype, 0, d), _code_of(x.dtype), n_src, rows,
+                                  K, act, _i32("src", src, rows, d), _i32("count", count, 1, d),
+                                  _f32("gscale", gscale, 1, d), _raw("codes", codes, nc, d),
+                                  _raw("scales", scales, ns, d),
+                                  _buf("values", values, x.dtype, rows * K, d),
+                                  _queue(stream, d)))
 
 
 def coli_moe_fp4_product_workspace_size(fmt: int, P: int, K: int, E: int, R: int) -> int:
@@ -585,19 +613,22 @@ def coli_moe_fp4_product_workspace_size(fmt: int, P: int, K: int, E: int, R: int
 
 def coli_moe_fp4_product(fmt, x_codes, x_scales, P, K, w_codes, w_scales, E, R, y, ws,
                          offsets=None, alpha=None, stream=None):
-    xc, xs = coli_moe_fp4_bytes(fmt, P, K)
-    wc, wsc = coli_moe_fp4_bytes(fmt, E * R, K)
-    p, n = _workspace(ws)
-    _ok(lib.coli_moe_fp4_product(fmt, _raw("x_codes", x_codes, xc), _raw("x_scales", x_scales, xs),
-                                 P, K, _raw("w_codes", w_codes, wc),
-                                 _raw("w_scales", w_scales, wsc), E, R,
-                                 _i32("offsets", offsets, E + 1), _f32("alpha", alpha, E),
-                                 _buf("y", y, y.dtype, P * R), _code_of(y.dtype), p, n,
-                                 _stream(stream)))
+    d = _device()
+    xc, xs = _fp4_sizes(fmt, P, K)
+    wc, wsc = _fp4_sizes(fmt, E * R, K)
+    p, n = _workspace(ws, d)
+    _ok(lib.coli_moe_fp4_product(fmt, _raw("x_codes", x_codes, xc, d),
+                                 _raw("x_scales", x_scales, xs, d), P, K,
+                                 _raw("w_codes", w_codes, wc, d),
+                                 _raw("w_scales", w_scales, wsc, d), E, R,
+                                 _i32("offsets", offsets, E + 1, d), _f32("alpha", alpha, E, d),
+                                 _buf("y", y, y.dtype, P * R, d), _code_of(y.dtype), p, n,
+                                 _queue(stream, d)))
 
 
 def coli_moe_fp4_product_status(ws, stream=None) -> int:
     """Error flags of the last product that used ws (raises on a timeout)."""
-    flags = _I32(0)
-    _ok(lib.coli_moe_fp4_product_status(_raw("ws", ws, 4), ctypes.byref(flags), _stream(stream)))
+    flags, d = _I32(0), _device()
+    _ok(lib.coli_moe_fp4_product_status(_raw("ws", ws, 4, d), ctypes.byref(flags),
+                                        _queue(stream, d)))
     return flags.value

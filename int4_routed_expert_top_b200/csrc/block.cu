@@ -52,24 +52,23 @@ int launch_rows_sum(const void* o, int T, int H, int k, const int32_t* inv, cons
                     const void* residual, void* y, cudaStream_t st) {
     // 16 bytes of o per thread where rows and pointers allow it
     constexpr int N = 16 / sizeof(OT);
-    constexpr int ya = N * sizeof(YT) < 16 ? N * sizeof(YT) : 16;
+    constexpr int ya = N * sizeof(YT);
     const bool wide = H % N == 0 && aligned(o, 16) && aligned(residual, ya) && aligned(y, ya);
-    const int nvec = wide ? H / N : H, per = (nvec + 255) / 256;
+    const int per = ((wide ? H / N : H) + 255) / 256;
     const auto kern = wide ? rows_sum_kernel<OT, YT, N> : rows_sum_kernel<OT, YT, 1>;
     return launch_pdl(kern, dim3((unsigned)T * per), 256, 0, st, "combine", (const OT*)o, (int64_t)T * k,
-                      nvec, per, k, inv, w, (const YT*)residual, (YT*)y);
+                      H, per, k, inv, w, (const YT*)residual, (YT*)y);
 }
 
 template <typename YT, typename OT>
 int launch_rows_sum_backward(const void* dy, const void* o, int T, int H, int k, const int32_t* inv,
                              const float* w, void* d_o, float* dw, cudaStream_t st) {
     constexpr int N = 16 / sizeof(OT);
-    constexpr int ya = N * sizeof(YT) < 16 ? N * sizeof(YT) : 16;
+    constexpr int ya = N * sizeof(YT);
     const bool wide = H % N == 0 && aligned(o, 16) && aligned(d_o, 16) && aligned(dy, ya);
-    const int nvec = wide ? H / N : H;
     const auto kern = wide ? rows_sum_backward_kernel<YT, OT, N> : rows_sum_backward_kernel<YT, OT, 1>;
     return launch_pdl(kern, dim3(T), 256, 0, st, "combine backward", (const YT*)dy, (const OT*)o,
-                      (int64_t)T * k, nvec, k, inv, w, (OT*)d_o, dw);
+                      (int64_t)T * k, H, k, inv, w, (OT*)d_o, dw);
 }
 
 int norm_ok(const char* what, const coli_norm_desc* d, int T) {
@@ -98,29 +97,39 @@ NormArgs norm_args(const coli_norm_desc& d, const float* gate, int T) {
 
 // elements per vector, vectors per thread and threads of a row
 struct NormShape { int V, N, threads; };
-NormShape norm_shape(int H, bool wide) {
+// Many tokens: about 256 threads a row, so that an SM holds several rows.  Few
+// (less than two rows per SM): one vector a thread (the time of one row is what counts).
+NormShape norm_shape(int H, int T, bool wide, bool backward) {
     NormShape s;
-    s.V = wide ? 4 : 1;
-    const int vecs = H / s.V, small = wide ? 4 : 16;
-    s.N = vecs <= small * kNormMaxThreads ? small : 2 * small;
+    s.V = wide ? 8 : 1;
+    const int vecs = H / s.V;
+    if (!wide)
+        s.N = vecs <= 16 * 512 ? 16 : 32;
+    else if (vecs <= 256 || (!backward && T < 2 * 148 && vecs <= 1024))
+        s.N = 1;
+    else
+        s.N = vecs <= 2 * 256 ? 2 : vecs <= 3 * 512 ? 3 : 4;
     s.threads = ((vecs + s.N - 1) / s.N + 31) / 32 * 32;
     return s;
 }
 
-// calls f with the kernel's type and shape parameters as template arguments
+// calls the kernel with its type and shape parameters as template arguments
+template <template <typename, typename, int, int> class K, typename XT, typename BT, typename... A>
+int norm_launch(const NormShape& s, A... args) {
+    if (s.V == 8) {
+        if (s.N == 1) return K<XT, BT, 8, 1>::launch(s, args...);
+        if (s.N == 2) return K<XT, BT, 8, 2>::launch(s, args...);
+        if (s.N == 3) return K<XT, BT, 8, 3>::launch(s, args...);
+        return K<XT, BT, 8, 4>::launch(s, args...);
+    }
+    if (s.N == 16) return K<XT, BT, 1, 16>::launch(s, args...);
+    return K<XT, BT, 1, 32>::launch(s, args...);
+}
 template <template <typename, typename, int, int> class K, typename... A>
 int norm_dispatch(const coli_norm_desc& d, const NormShape& s, A... args) {
-#define COLI_NORM_CASE(XT, BT)                                          \
-    if (s.V == 4) {                                                     \
-        if (s.N == 4) return K<XT, BT, 4, 4>::launch(s, args...);       \
-        return K<XT, BT, 4, 8>::launch(s, args...);                     \
-    }                                                                   \
-    if (s.N == 16) return K<XT, BT, 1, 16>::launch(s, args...);         \
-    return K<XT, BT, 1, 32>::launch(s, args...);
-    if (d.xt == COLI_F32 && d.bt == COLI_F32) { COLI_NORM_CASE(float, float) }
-    if (d.xt == COLI_F32) { COLI_NORM_CASE(float, __nv_bfloat16) }
-    COLI_NORM_CASE(__nv_bfloat16, __nv_bfloat16)
-#undef COLI_NORM_CASE
+    if (d.bt == COLI_F32) return norm_launch<K, float, float>(s, args...);
+    if (d.xt == COLI_F32) return norm_launch<K, float, __nv_bfloat16>(s, args...);
+    return norm_launch<K, __nv_bfloat16, __nv_bfloat16>(s, args...);
 }
 
 template <typename XT, typename BT, int V, int N>
@@ -132,20 +141,44 @@ struct NormForward {
     }
 };
 
+// CTAs of the backward pass: two per SM, so that one's loads cover the other's
+// sums over the row; clusters of four leave 74 partial rows
+constexpr int kNormBackwardCtas = 296;
+constexpr int kNormCluster = 4;
+int norm_backward_cluster(int grid) { return grid >= kNormCluster ? kNormCluster : 1; }
+int norm_backward_grid(int T) {
+    const int grid = std::min(T, kNormBackwardCtas);
+    return grid / norm_backward_cluster(grid) * norm_backward_cluster(grid);
+}
+
 template <typename XT, typename BT, int V, int N>
 struct NormBackward {
-    static int launch(const NormShape& s, const NormArgs& a, const void* x_out, const void* o,
+    static int launch(const NormShape& s, const NormArgs& a, const NormSums& keep, const void* x_out, const void* o,
                       const float* rstd_post, const float* rstd_pre, const void* dx_out, const void* dn,
                       void* dx, void* d_o, float* dgate, float* partial, int grid, cudaStream_t st) {
-        return launch_pdl(block_norm_backward_kernel<XT, BT, V, N>, dim3(grid), s.threads, 0, st,
-                          "block norm backward", a, (const XT*)x_out, (const BT*)o, rstd_post, rstd_pre,
-                          (const XT*)dx_out, (const BT*)dn, (XT*)dx, (BT*)d_o, dgate, partial);
+        const auto kern = block_norm_backward_kernel<XT, BT, V, N>;
+        const int smem = keep.n * a.H * 4;
+        int rc = set_smem((const void*)kern, smem);
+        if (rc) return rc;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(grid);
+        cfg.blockDim = dim3(s.threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = st;
+        cudaLaunchAttribute attr[2];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        attr[1].id = cudaLaunchAttributeClusterDimension;
+        attr[1].val.clusterDim.x = norm_backward_cluster(grid);
+        attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 2;
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, keep, (const XT*)x_out, (const BT*)o, rstd_post, rstd_pre,
+                                                 (const XT*)dx_out, (const BT*)dn, (XT*)dx, (BT*)d_o, dgate, partial);
+        if (e != cudaSuccess) return fail(COLI_E_CUDA, "block norm backward: %s", cudaGetErrorString(e));
+        return check_launch("block norm backward");
     }
 };
-
-// CTAs of the backward pass: two per SM, so that one's loads cover the other's
-// sums over the row
-constexpr int kNormBackwardCtas = 296;
 
 }  // namespace
 
@@ -249,12 +282,12 @@ int coli_moe_block_norm(const coli_norm_desc* desc, const void* x, const void* o
     if (!x || (o && !x_out) || (!o && !n_out)) return fail(COLI_E_INVAL, "block_norm: NULL pointer");
     if (o && (desc->gate_kind != COLI_GATE_NONE) != (gate != nullptr))
         return fail(COLI_E_INVAL, "block_norm: gate and gate_kind disagree");
-    const int xa = 4 * type_size(desc->xt), ba = 4 * type_size(desc->bt);
-    const bool wide = desc->H % 4 == 0 && aligned(x, xa) && aligned(x_out, xa) && aligned(o, ba) &&
-                      aligned(n_out, ba) && aligned(desc->post_gain, 16) && aligned(desc->pre_gain, 16) &&
-                      aligned(gate, 16);
+    const int xa = 8 * type_size(desc->xt), ba = 8 * type_size(desc->bt);
+    const bool wide = desc->H % 8 == 0 && aligned(x, xa) && aligned(x_out, xa) && aligned(o, ba) &&
+                      aligned(n_out, ba) && aligned(desc->post_gain, 32) && aligned(desc->pre_gain, 32) &&
+                      aligned(gate, 32);
     const NormArgs a = norm_args(*desc, gate, T);
-    return norm_dispatch<NormForward>(*desc, norm_shape(desc->H, wide), a, x, o, x_out, n_out, rstd_post, rstd_pre,
+    return norm_dispatch<NormForward>(*desc, norm_shape(desc->H, T, wide, false), a, x, o, x_out, n_out, rstd_post, rstd_pre,
                                       S(stream));
 }
 
@@ -262,7 +295,8 @@ int coli_moe_block_norm_backward_workspace_size(const coli_norm_desc* desc, int3
     int rc = norm_ok("block_norm_backward_workspace_size", desc, T);
     if (rc) return rc;
     if (!bytes) return fail(COLI_E_INVAL, "block_norm_backward_workspace_size: NULL pointer");
-    *bytes = (size_t)std::min(T, kNormBackwardCtas) * 3 * desc->H * 4;
+    const int grid = norm_backward_grid(T);
+    *bytes = (size_t)(grid / norm_backward_cluster(grid)) * kNormSums * desc->H * 4;
     return COLI_OK;
 }
 
@@ -285,25 +319,30 @@ int coli_moe_block_norm_backward(const coli_norm_desc* desc, const void* x_out, 
         return fail(COLI_E_INVAL, "block_norm_backward: gradient of an input that this call does not have");
     // sums over tokens: partial rows in the workspace, then the second kernel
     const bool channel = dgate && desc->gate_kind == COLI_GATE_CHANNEL;
-    const bool sums = dpost_gain || channel || dpre_gain;
-    if (sums && (!ws || ws_bytes < need || !aligned(ws, 16)))
+    NormSums keep;
+    keep.n = 0;
+    keep.at[0] = dpost_gain ? keep.n++ : -1;
+    keep.at[1] = channel ? keep.n++ : -1;
+    keep.at[2] = dpre_gain ? keep.n++ : -1;
+    if (keep.n && (!ws || ws_bytes < need || !aligned(ws, 16)))
         return fail(COLI_E_WORKSPACE, "block_norm_backward: workspace of %zu bytes, %zu needed", ws ? ws_bytes : 0,
                     need);
-    const int grid = std::min(T, kNormBackwardCtas);
-    float* partial = sums ? static_cast<float*>(ws) : nullptr;
+    const int grid = norm_backward_grid(T);
+    float* partial = static_cast<float*>(ws);
     if (T > 0) {
-        const int xa = 4 * type_size(desc->xt), ba = 4 * type_size(desc->bt);
-        const bool wide = desc->H % 4 == 0 && aligned(x_out, xa) && aligned(dx_out, xa) && aligned(dx, xa) &&
-                          aligned(o, ba) && aligned(dn, ba) && aligned(d_o, ba) && aligned(desc->post_gain, 16) &&
-                          aligned(desc->pre_gain, 16) && aligned(gate, 16) && aligned(dgate, 16);
+        const int xa = 8 * type_size(desc->xt), ba = 8 * type_size(desc->bt);
+        const bool wide = desc->H % 8 == 0 && aligned(x_out, xa) && aligned(dx_out, xa) && aligned(dx, xa) &&
+                          aligned(o, ba) && aligned(dn, ba) && aligned(d_o, ba) && aligned(desc->post_gain, 32) &&
+                          aligned(desc->pre_gain, 32) && aligned(gate, 32) && aligned(dgate, 32);
         const NormArgs a = norm_args(*desc, gate, T);
-        rc = norm_dispatch<NormBackward>(*desc, norm_shape(desc->H, wide), a, x_out, o, rstd_post, rstd_pre, dx_out,
-                                         dn, dx, d_o, dgate, partial, grid, S(stream));
+        rc = norm_dispatch<NormBackward>(*desc, norm_shape(desc->H, T, wide, true), a, keep, x_out, o, rstd_post,
+                                         rstd_pre, dx_out, dn, dx, d_o, dgate, partial, grid, S(stream));
         if (rc) return rc;
     }
-    if (!sums) return COLI_OK;
-    return launch_pdl(norm_reduce_kernel, dim3((desc->H + 31) / 32, 3), 256, 0, S(stream), "block norm sums",
-                      (const float*)partial, grid, (int)desc->H, dpost_gain, channel ? dgate : nullptr, dpre_gain);
+    if (!keep.n) return COLI_OK;
+    return launch_pdl(norm_reduce_kernel, dim3((desc->H + 31) / 32, kNormSums), 256, 0, S(stream), "block norm sums",
+                      (const float*)partial, grid / norm_backward_cluster(grid), (int)desc->H, keep, dpost_gain, dgate,
+                      dpre_gain);
 }
 
 }  // extern "C"

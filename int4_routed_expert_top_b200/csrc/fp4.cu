@@ -11,7 +11,8 @@ using namespace coli;
 
 namespace {
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+bool aligned_to(const void* p, int bytes) { return (reinterpret_cast<uintptr_t>(p) & (bytes - 1)) == 0; }
+bool aligned16(const void* p) { return aligned_to(p, 16); }
 int block_of(coli_fp4 fmt) { return fmt == COLI_NVFP4 ? 16 : 32; }
 int words_of(coli_fp4 fmt, int K) { return (K / block_of(fmt) + 3) / 4; }
 
@@ -29,7 +30,6 @@ int sm_count() {
         sms = 148;
     return sms;
 }
-constexpr int kMaxGrid = 160;  // B200 has 148 SMs; the workspace is sized for this many
 
 // Rows of an expert per tile: 32 streams the weights with the deepest ring, 192
 // makes the most of each weight byte.
@@ -59,11 +59,8 @@ int launch_product(const FpArgs& a, const void* x_codes, const void* w_codes, vo
     if ((rc = encode_codes_map(&wmap, w_codes, (int64_t)a.E * a.R, a.K, 128))) return rc;
     if ((rc = encode_codes_map(&xmap, x_codes, a.P, a.K, C::box))) return rc;
     if ((rc = set_smem((const void*)fp4_product_kernel<NT, NV, YT>, C::smem))) return rc;
-    const int grid = std::min(sm_count(), kMaxGrid);
-    if ((rc = launch_pdl(fp4_product_kernel<NT, NV, YT>, dim3(grid), kFpThreads, C::smem, st, "fp4 product", wmap, xmap,
-                         a, (YT*)y)))
-        return rc;
-    return launch_pdl(fp4_join_kernel<NT, YT>, dim3(grid, NT / 32), kFpThreads, 0, st, "fp4 join", a, grid, (YT*)y);
+    return launch_pdl(fp4_product_kernel<NT, NV, YT>, dim3(std::min(sm_count(), kFpMaxGrid)), kFpThreads, C::smem, st,
+                      "fp4 product", wmap, xmap, a, (YT*)y);
 }
 
 template <int NT>
@@ -101,8 +98,8 @@ int coli_moe_fp4_quantize(coli_fp4 fmt, const void* x, coli_dtype xt, int64_t n_
         return fail(COLI_E_INVAL, "fp4_quantize: %lld source rows", (long long)n_src);
     if (rows == 0) return COLI_OK;
     if ((!x && n_src > 0) || !codes || !scales) return fail(COLI_E_INVAL, "fp4_quantize: NULL pointer");
-    if (!aligned16(x) || !aligned16(codes) || !aligned16(scales) || !aligned16(values))
-        return fail(COLI_E_INVAL, "fp4_quantize: buffers must be 16-byte aligned");
+    if (!aligned_to(x, 32) || !aligned_to(codes, 16) || !aligned_to(scales, 16) || !aligned_to(values, 32))
+        return fail(COLI_E_INVAL, "fp4_quantize: x and values must be 32-byte aligned, codes and scales 16-byte");
     Fp4QuantArgs a;
     a.n_src = n_src; a.rows = rows;
     a.K = K; a.words = words_of(fmt, K);
@@ -110,15 +107,17 @@ int coli_moe_fp4_quantize(coli_fp4 fmt, const void* x, coli_dtype xt, int64_t n_
     a.src = src; a.count = count; a.gscale = gscale;
     a.codes = static_cast<uint8_t*>(codes);
     a.scales = static_cast<uint32_t*>(scales);
-    const int64_t warps = rows * ((K + 255) / 256), ctas = (warps + 7) / 8;
-    if (ctas > INT32_MAX) return fail(COLI_E_UNSUPPORTED, "fp4_quantize: %lld x %d is too large", (long long)rows, K);
-    const dim3 grid((unsigned)ctas);
+    // warps per row: a power of two, as many as have a chunk of 256 columns
+    const int chunks = (K + 255) / 256;
+    int rows_per = 8;
+    while (rows_per > 1 && 8 / rows_per < chunks) rows_per /= 2;
+    const dim3 grid((unsigned)((rows + rows_per - 1) / rows_per));
     if (xt == COLI_F32)
         return launch_pdl(fmt == COLI_NVFP4 ? fp4_quantize_kernel<float, true> : fp4_quantize_kernel<float, false>, grid,
-                          256, 0, S(stream), "fp4 quantize", a, (const float*)x, (float*)values);
+                          256, 0, S(stream), "fp4 quantize", a, rows_per, (const float*)x, (float*)values);
     return launch_pdl(fmt == COLI_NVFP4 ? fp4_quantize_kernel<__nv_bfloat16, true>
                                         : fp4_quantize_kernel<__nv_bfloat16, false>,
-                      grid, 256, 0, S(stream), "fp4 quantize", a, (const __nv_bfloat16*)x, (__nv_bfloat16*)values);
+                      grid, 256, 0, S(stream), "fp4 quantize", a, rows_per, (const __nv_bfloat16*)x, (__nv_bfloat16*)values);
 }
 
 int coli_moe_fp4_product_workspace_size(coli_fp4 fmt, int64_t P, int32_t K, int32_t E, int32_t R, size_t* bytes) {
@@ -127,7 +126,7 @@ int coli_moe_fp4_product_workspace_size(coli_fp4 fmt, int64_t P, int32_t K, int3
     if (!bytes) return fail(COLI_E_INVAL, "fp4_product_workspace_size: NULL pointer");
     if (E < 1 || E > kFpMaxE || R < 1 || (E > 1 && R % 128) || (int64_t)E * R > INT32_MAX)
         return fail(COLI_E_INVAL, "fp4_product: bad sizes E=%d R=%d", E, R);
-    *bytes = kFpHeadBytes + (size_t)kMaxGrid * 2 * 128 * tile_rows(P, E) * 4;
+    *bytes = kFpHeadBytes + (size_t)kFpMaxGrid * 128 * tile_rows(P, E) * 4;
     return COLI_OK;
 }
 
@@ -154,6 +153,7 @@ int coli_moe_fp4_product(coli_fp4 fmt, const void* x_codes, const void* x_scales
     a.xwords = a.wwords = words_of(fmt, K);
     a.offsets = offsets; a.alpha = alpha;
     a.err = static_cast<int32_t*>(ws);
+    a.flags = reinterpret_cast<uint64_t*>(static_cast<char*>(ws) + kFpFlagBytes);
     a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kFpHeadBytes);
     if (tile_rows(P, E) == kFpLargeNT)
         return launch_product_t<kFpLargeNT>(fmt, yt, a, x_codes, w_codes, y, S(stream));

@@ -14,9 +14,12 @@
 // (expert, 128 weight rows, NT of its rows); all units of all tiles, in the order
 // (expert, weight rows, rows, columns), are cut into equal runs, one per CTA,
 // so that every SM streams the same number of bytes whatever the routing.  A
-// tile that a run's border cuts leaves f32 partial sums in the workspace and
-// a second kernel adds them in the order of their columns: no atomics, the same
-// bits at every run.
+// tile that a run's border cuts leaves f32 partial sums in the workspace: every
+// CTA that does not begin the tile stores its piece and raises a flag, and the
+// one that begins it, whose piece is the last of its run, adds them in the
+// order of their columns.  No atomics, the same bits at every run; the others
+// take these pieces first, so the wait is short, and it is never for a CTA with
+// a lower index, so CTAs that are scheduled late cannot stop the earlier ones.
 //
 // CTA roles: warp 0 copies (codes by 2-D TMA with the 128-byte swizzle, the
 // weights' scales by bulk copy), warps 2-3 bring the rows' scales (rows of an
@@ -37,28 +40,6 @@ namespace coli {
 // ---------------------------------------------------------------------------
 // quantiser
 // ---------------------------------------------------------------------------
-template <typename T> __device__ __forceinline__ void load8(const T* p, float (&v)[8]);
-template <> __device__ __forceinline__ void load8<float>(const float* p, float (&v)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-template <> __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&v)[8]) {
-    const Vec<__nv_bfloat16, 8> a = *reinterpret_cast<const Vec<__nv_bfloat16, 8>*>(p);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = __bfloat162float(a.v[i]);
-}
-template <typename T> __device__ __forceinline__ void store8(T* p, const float (&v)[8]) {
-#pragma unroll
-    for (int h = 0; h < (int)(8 * sizeof(T) / 16); ++h) {
-        constexpr int n = 16 / sizeof(T);
-        Vec<T, n> a;
-#pragma unroll
-        for (int i = 0; i < n; ++i) a.v[i] = from_f32<T>(v[h * n + i]);
-        reinterpret_cast<Vec<T, n>*>(p)[h] = a;
-    }
-}
-
 struct Fp4QuantArgs {
     int64_t n_src, rows;
     int K, words;            // words: 4-block scale words per row
@@ -75,37 +56,31 @@ __device__ __forceinline__ int64_t scale_word(int64_t r, int w, int words) {
     return ((r >> 7) * words + w) * 128 + (r & 31) * 4 + ((r >> 5) & 3);
 }
 
-// A lane holds 8 columns of a row, a warp 256: 16 bytes of bf16 per load, a
-// block's maximum by one or two shuffles.  Bound by HBM (x once, codes, scales
-// and values once).
+// A lane holds 8 columns of a row, a warp 256 at a time: 16 bytes of bf16 (32
+// of f32) per load, a block's maximum by one or two shuffles.  A CTA's 8 warps
+// share out `rows_per` rows, 8 / rows_per warps each.  Bound by HBM (x once,
+// codes, scales and values once).
 template <typename T, bool NV>
-__global__ void __launch_bounds__(256)
-fp4_quantize_kernel(Fp4QuantArgs a, const T* __restrict__ x, T* __restrict__ values) {
+__device__ __forceinline__ void fp4_quantize_chunk(const Fp4QuantArgs& a, const T* __restrict__ x,
+                                                   T* __restrict__ values, int64_t r, int64_t from, int c,
+                                                   float g) {
     const int lane = threadIdx.x & 31;
-    const int chunks = (a.K + 255) / 256;
-    const int64_t id = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
-    const int64_t r = id / chunks;
-    const int c = (int)(id - r * chunks) * 256 + lane * 8;
-    pdl_trigger();
-    pdl_wait();
-    if (r >= a.rows || (a.count && r >= *a.count)) return;
-    const int64_t from = a.src ? a.src[r] : r;
     const bool in = c < a.K;
-    float v[8];
+    F<8> f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    for (int i = 0; i < 8; ++i) f.v[i] = 0.0f;
     if (in && from >= 0 && from < a.n_src) {
         if (a.swiglu) {
             const T* p = x + from * 2 * a.K + c;
-            float u[8];
-            load8(p, v);
-            load8(p + a.K, u);
+            f = ldf<T, 8>(p);
+            const F<8> u = ldf<T, 8>(p + a.K);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = silu_f(v[i]) * u[i];
+            for (int i = 0; i < 8; ++i) f.v[i] = silu_f(f.v[i]) * u.v[i];
         } else {
-            load8(x + from * a.K + c, v);
+            f = ldf<T, 8>(x + from * a.K + c);
         }
     }
+    const float (&v)[8] = f.v;
     // the largest magnitude as bits: infinities and NaN come out on top
     uint32_t m = 0;
 #pragma unroll
@@ -116,7 +91,6 @@ fp4_quantize_kernel(Fp4QuantArgs a, const T* __restrict__ x, T* __restrict__ val
     uint32_t byte;
     float d, r_d;  // what a code of 1 stands for, and its reciprocal
     if (NV) {
-        const float g = a.gscale ? *a.gscale : 1.0f;
         const float t = __fdiv_rn(__uint_as_float(m), __fmul_rn(6.0f, g));
         byte = __nv_cvt_float_to_fp8(fminf(t, 448.0f), __NV_SATFINITE, __NV_E4M3);
         d = __fmul_rn(__half2float(__half(__nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)byte, __NV_E4M3))), g);
@@ -150,16 +124,31 @@ fp4_quantize_kernel(Fp4QuantArgs a, const T* __restrict__ x, T* __restrict__ val
     if (lane == first) a.scales[scale_word(r, c / (32 * per), a.words)] = word;
     *reinterpret_cast<uint32_t*>(a.codes + (r * a.K + c) / 2) = code;
     if (values) {
-        float q[8];
+        F<8> q;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const __half2 h = __half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(code >> (8 * i)), __NV_E2M1));
-            q[2 * i] = __fmul_rn(__low2float(h), d);
-            q[2 * i + 1] = __fmul_rn(__high2float(h), d);
-            if (bad) q[2 * i] = q[2 * i + 1] = __uint_as_float(0x7fc00000u);
+            q.v[2 * i] = __fmul_rn(__low2float(h), d);
+            q.v[2 * i + 1] = __fmul_rn(__high2float(h), d);
+            if (bad) q.v[2 * i] = q.v[2 * i + 1] = __uint_as_float(0x7fc00000u);
         }
-        store8(values + r * a.K + c, q);
+        stf<T, 8>(values + r * a.K + c, q);
     }
+}
+
+template <typename T, bool NV>
+__global__ void __launch_bounds__(256)
+fp4_quantize_kernel(Fp4QuantArgs a, int rows_per, const T* __restrict__ x, T* __restrict__ values) {
+    const int warps = 8 / rows_per, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t r = (int64_t)blockIdx.x * rows_per + warp / warps;
+    pdl_trigger();
+    pdl_wait();
+    if (r >= a.rows || (a.count && r >= *a.count)) return;
+    const int64_t from = a.src ? a.src[r] : r;
+    const float g = NV && a.gscale ? *a.gscale : 1.0f;
+#pragma unroll 2
+    for (int c0 = (warp & (warps - 1)) * 256; c0 < a.K; c0 += warps * 256)
+        fp4_quantize_chunk<T, NV>(a, x, values, r, from, c0 + lane * 8, g);
 }
 
 // ---------------------------------------------------------------------------
@@ -168,7 +157,12 @@ fp4_quantize_kernel(Fp4QuantArgs a, const T* __restrict__ x, T* __restrict__ val
 constexpr int kFpThreads = 256;
 constexpr int kFpMaxE = 1024;
 constexpr int kFpMinUnits = 2;     // stages per CTA at least, before fewer CTAs take part
-constexpr int kFpHeadBytes = 256;  // of the workspace: error flags
+constexpr int kFpMaxGrid = 160;    // B200 has 148 SMs; the workspace is sized for this many
+// the workspace: error flags, a flag per CTA and store warp, then partial sums
+constexpr int kFpFlagBytes = 256;
+constexpr int kFpHeadBytes = kFpFlagBytes + kFpMaxGrid * 4 * 8;
+// a raised flag: a value that unset memory does not hold (0 after every call)
+constexpr uint64_t kFpRaised = 0x9d3ac1f5e8276b41ull;
 
 template <int NT, bool NV>
 struct FpShape {
@@ -197,11 +191,12 @@ struct FpArgs {
     int xwords, wwords;      // scale words per row
     const int32_t* offsets;
     const float* alpha;
+    uint64_t* flags;
     float* partial;
     int32_t* err;
 };
 
-// Where every expert's tiles start, in shared memory; the same in both kernels.
+// Where every expert's tiles start, in shared memory.
 struct FpPlan {
     int32_t begin[kFpMaxE + 1];
     int64_t tile0[kFpMaxE + 1];
@@ -348,6 +343,19 @@ __device__ __forceinline__ uint32_t elect_one() {
     return e;
 }
 
+// Warp-wide wait for a flag of another CTA's store warp, a second at most
+__device__ __forceinline__ bool fp_wait_flag(const uint64_t* flag, int32_t* err) {
+    int ok = 1;
+    if ((threadIdx.x & 31) == 0) {
+        uint64_t v = 0;
+        for (int i = 0; i < (1 << 21) && v != kFpRaised; ++i)
+            asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(flag) : "memory");
+        ok = v == kFpRaised;
+        if (!ok) atomicOr(err, kErrWaitTimeout);
+    }
+    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+}
+
 template <int NT, bool NV, typename YT>
 __global__ void __launch_bounds__(kFpThreads, 1)
 fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
@@ -462,56 +470,53 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         }
     } else if (warp < 4) {
         // ---------------- scales of the rows: atoms of one parity ----------------
+        // The loads of a stage are issued `ahead` stages before it is stored.
         constexpr int mine = C::atoms / 2;
         constexpr int words = NT / 32;        // per lane and atom
+        constexpr int ahead = NT > 64 ? 4 : 8;
         const int par = warp - 2;
-        uint32_t next[mine][words];
-        const auto load = [&](const FpTile& t, int k) {
+        uint32_t w[ahead][mine][words];
+        FpTile t;
+        q.k0 = q.k1 = 0;
+        const auto load = [&](uint32_t (&to)[mine][words]) {  // the next stage's words, if there is one
+            if (q.k0 == q.k1) {
+                if (!fp_next(u, hi, a.KS, q)) return;
+                t = fp_tile<NT>(plan, a.E, q.tile);
+            }
 #pragma unroll
             for (int i = 0; i < mine; ++i) {
-                const int ch = k * C::atoms + 2 * i + par;
+                const int ch = q.k0 * C::atoms + 2 * i + par;
 #pragma unroll
-                for (int w = 0; w < words; ++w) {
-                    const int64_t r = t.p0 + 32 * w + lane;
-                    next[i][w] = 0;
-                    if (ch < a.xwords && 32 * w < t.n && r < a.P) next[i][w] = __ldg(a.xs + scale_word(r, ch, a.xwords));
+                for (int j = 0; j < words; ++j) {
+                    const int64_t r = t.p0 + 32 * j + lane;
+                    to[i][j] = 0;
+                    if (ch < a.xwords && 32 * j < t.n && r < a.P) to[i][j] = __ldg(a.xs + scale_word(r, ch, a.xwords));
                 }
             }
+            ++q.k0;
         };
-        int cnt = 0;
-        bool have = fp_next(u, hi, a.KS, q);
-        FpTile t;
-        int k = q.k0;
-        if (have) {
-            t = fp_tile<NT>(plan, a.E, q.tile);
-            load(t, k);
-        }
-        while (have) {
-            uint32_t now[mine][words];
+        const int64_t total = hi - lo;
 #pragma unroll
-            for (int i = 0; i < mine; ++i)
+        for (int d = 0; d < ahead; ++d) load(w[d]);
+        for (int64_t base = 0; base < total; base += ahead) {
 #pragma unroll
-                for (int w = 0; w < words; ++w) now[i][w] = next[i][w];
-            // the next stage's loads are in flight while this one waits for its slot
-            if (++k == q.k1) {
-                have = fp_next(u, hi, a.KS, q);
-                if (have) t = fp_tile<NT>(plan, a.E, q.tile);
-                k = q.k0;
+            for (int d = 0; d < ahead; ++d) {
+                const int cnt = (int)base + d;
+                if (cnt >= total) break;
+                const int s = cnt % C::stages;
+                if (cnt >= C::stages && ok && !mbar_wait_warp(&empty[s], ((cnt / C::stages) - 1) & 1, a.err)) ok = false;
+                uint8_t* sfb = smem + s * C::stage + C::a_bytes + C::b_bytes + C::sfa_bytes;
+#pragma unroll
+                for (int i = 0; i < mine; ++i)
+#pragma unroll
+                    for (int j = 0; j < words; ++j)
+                        *reinterpret_cast<uint32_t*>(sfb + 512 * (C::nb * (2 * i + par) + j / 4) + 16 * lane + 4 * (j & 3)) =
+                            w[d][i][j];
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[s]);
+                load(w[d]);
             }
-            if (have) load(t, k);
-            const int s = cnt % C::stages;
-            if (cnt >= C::stages && ok && !mbar_wait_warp(&empty[s], ((cnt / C::stages) - 1) & 1, a.err)) ok = false;
-            uint8_t* sfb = smem + s * C::stage + C::a_bytes + C::b_bytes + C::sfa_bytes;
-#pragma unroll
-            for (int i = 0; i < mine; ++i)
-#pragma unroll
-                for (int w = 0; w < words; ++w)
-                    *reinterpret_cast<uint32_t*>(sfb + 512 * (C::nb * (2 * i + par) + w / 4) + 16 * lane + 4 * (w & 3)) =
-                        now[i][w];
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&full[s]);
-            ++cnt;
         }
     } else {
         // ---------------- stores: weight rows 32 quarter + lane of the tile ----------------
@@ -520,29 +525,52 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             const FpTile t = fp_tile<NT>(plan, a.E, q.tile);
             const int buf = piece & 1;
             const int row = t.rt * 128 + 32 * quarter + lane;
-            const bool whole = q.k0 == 0 && q.k1 == a.KS;
-            const float al = whole && a.alpha ? a.alpha[t.e] : 1.0f;
-            // a piece that starts a tile uses the CTA's second slot
-            float* slot = a.partial + ((int64_t)blockIdx.x * 2 + (q.k0 == 0 ? 1 : 0)) * (128 * NT) + 32 * quarter + lane;
+            const bool begins = q.k0 == 0;
+            const float al = begins && a.alpha ? a.alpha[t.e] : 1.0f;
+            float* part = a.partial + 32 * quarter + lane;
+            // the CTAs after this one with pieces of the tile: up to the first whose run
+            // starts at its end or later
+            int64_t last = blockIdx.x + 1;
+            if (begins && q.k1 < a.KS)
+                while (run.lo(last) < (q.tile + 1) * a.KS) ++last;
             if (ok && !mbar_wait_warp(&accfull[buf], (piece >> 1) & 1, a.err)) ok = false;
             tc_fence_after();
+            for (int64_t c = blockIdx.x + 1; c < last; ++c)
+                if (ok && !fp_wait_flag(a.flags + 4 * c + quarter, a.err)) ok = false;
             const uint32_t d = tmem + ((uint32_t)(32 * quarter) << 16) + NT * buf;
             for (int c0 = 0; c0 < t.n; c0 += 16) {
                 uint32_t v[16];
                 tmem_ld_32x32b_x16(d + c0, v);
                 tmem_wait_ld();
-                if (whole) {
-                    if (row < a.R) {
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (c0 + i < t.n)
-                                y[(t.p0 + c0 + i) * a.R + row] = from_f32<YT>(__uint_as_float(v[i]) * al);
-                    }
-                } else {
+                if (!begins) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        if (c0 + i < t.n) slot[(c0 + i) * 128] = __uint_as_float(v[i]);
+                        if (c0 + i < t.n) part[(int64_t)blockIdx.x * (128 * NT) + (c0 + i) * 128] = __uint_as_float(v[i]);
+                    continue;
                 }
+                for (int64_t c = blockIdx.x + 1; c < last; ++c)
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (c0 + i < t.n)
+                            v[i] = __float_as_uint(__uint_as_float(v[i]) + __ldcg(part + c * (128 * NT) + (c0 + i) * 128));
+                if (row < a.R) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (c0 + i < t.n)
+                            y[(t.p0 + c0 + i) * a.R + row] = from_f32<YT>(__uint_as_float(v[i]) * al);
+                }
+            }
+            if (!begins) {
+                __syncwarp();
+                if (lane == 0) {
+                    __threadfence();
+                    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(a.flags + 4 * blockIdx.x + quarter), "l"(kFpRaised)
+                                 : "memory");
+                }
+            } else {
+                __syncwarp();
+                for (int64_t c = blockIdx.x + 1; c < last; ++c)
+                    if (lane == 0) a.flags[4 * c + quarter] = 0;  // read once: down again for the next call
             }
             tc_fence_before();
             __syncwarp();
@@ -553,32 +581,6 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     __syncthreads();
     tc_fence_after();
     if (warp == 0) tmem_dealloc(tmem, C::cols);
-}
-
-// Tiles cut by the runs' borders: CTA b sums the pieces of the tile that run b
-// begins and does not end, in the order of their columns.
-template <int NT, typename YT>
-__global__ void __launch_bounds__(kFpThreads)
-fp4_join_kernel(FpArgs a, int grid, YT* y) {
-    __shared__ FpPlan plan;
-    pdl_trigger();
-    pdl_wait();
-    fp_plan<NT>(a, plan);
-    const FpRun run(a, plan, grid);
-    const int64_t lo = run.lo(blockIdx.x), hi = run.lo(blockIdx.x + 1);
-    if (lo >= hi) return;
-    const int64_t tile = (hi - 1) / a.KS, first = tile * a.KS, last = first + a.KS;
-    if (hi >= last || first < lo) return;
-    const FpTile t = fp_tile<NT>(plan, a.E, tile);
-    const float al = a.alpha ? a.alpha[t.e] : 1.0f;
-    for (int i = blockIdx.y * kFpThreads + threadIdx.x; i < t.n * 128; i += gridDim.y * kFpThreads) {
-        const int n = i >> 7, r = i & 127;
-        float s = a.partial[((int64_t)blockIdx.x * 2 + 1) * (128 * NT) + i];
-        for (int64_t c = blockIdx.x + 1; run.lo(c) < last; ++c)
-            s += a.partial[(c * 2) * (128 * NT) + i];
-        const int row = t.rt * 128 + r;
-        if (row < a.R) y[(t.p0 + n) * a.R + row] = from_f32<YT>(s * al);
-    }
 }
 
 }  // namespace coli

@@ -166,6 +166,7 @@ sort_place_kernel(const int32_t* idx, const float* w, int64_t P, int64_t chunk, 
     sort_count(idx, w, b, min(P, b + chunk), chunk / kSortWarps, E, cnt);
     for (int e = threadIdx.x; e < E; e += kSortThreads) {
         int all = 0, mine = 0;
+#pragma unroll 16
         for (int c = 0; c < (int)gridDim.x; ++c) {
             const int v = counts[(int64_t)c * E + e];
             if (c < (int)blockIdx.x) mine += v;
@@ -184,11 +185,20 @@ sort_place_kernel(const int32_t* idx, const float* w, int64_t P, int64_t chunk, 
     sort_place(idx, w, b, min(P, b + chunk), chunk / kSortWarps, k, E, cnt, pair_tok, pair_slot, inv);
 }
 
-// row of pick (t, j), -1 unless 0 <= row < P
-__device__ __forceinline__ int64_t pick_row(const int32_t* inv, int64_t i, int64_t P) {
-    const int64_t p = inv[i];
-    return p >= 0 && p < P ? p : -1;
-}
+// A warp's picks of one token: lane j holds pick j's row and weight; live has a
+// bit for each pick that is computed (0 <= row < P).
+struct Picks {
+    int row;
+    float w;
+    unsigned live;
+    __device__ __forceinline__ Picks(const int32_t* inv, const float* weights, int64_t t, int k, int64_t P) {
+        const int lane = threadIdx.x & 31;
+        row = lane < k ? inv[t * k + lane] : -1;
+        const bool in = row >= 0 && row < P;
+        w = in && weights ? weights[t * k + lane] : 1.0f;
+        live = __ballot_sync(0xffffffffu, in);
+    }
+};
 
 // xs[inv[t, j]] = x[t]: block = (token, run of 256 vectors)
 template <typename V>
@@ -199,41 +209,48 @@ dispatch_kernel(const V* __restrict__ x, int64_t P, int nvec, int per_row, int k
     const int c = (int)(blockIdx.x - t * per_row) * 256 + threadIdx.x;
     pdl_trigger();
     pdl_wait();
-    if (c >= nvec) return;
-    const V v = x[t * nvec + c];
-    for (int j = 0; j < k; ++j) {
-        const int64_t p = pick_row(inv, t * k + j, P);
-        if (p >= 0) xs[p * nvec + c] = v;
+    V v;
+    if (c < nvec) v = x[t * nvec + c];
+    const Picks picks(inv, nullptr, t, k, P);
+    for (unsigned live = picks.live; live; live &= live - 1) {
+        const int64_t p = __shfl_sync(0xffffffffu, picks.row, __ffs(live) - 1);
+        if (c < nvec) xs[p * nvec + c] = v;
     }
 }
 
 // y[t] = residual[t] + sum_j w[t, j] o[inv[t, j]]: a thread owns N columns of
-// one token; eight picks' loads are in flight at once
+// one token.  Picks are taken in slot order, eight at a time so that their
+// loads are in flight together; every warp reads the token's picks once, a lane
+// each, instead of every thread all of them.  64 registers keep 1024 threads
+// of an SM (128 KB of loads) busy: 4096 tokens x 8 picks of 6144 bf16 take
+// KERNEL_TIME.
 template <typename OT, typename YT, int N>
-__global__ void __launch_bounds__(256)
-rows_sum_kernel(const OT* __restrict__ o, int64_t P, int nvec, int per_row, int k,
+__global__ void __launch_bounds__(256, 3)
+rows_sum_kernel(const OT* __restrict__ o, int64_t P, int H, int per_row, int k,
                 const int32_t* __restrict__ inv, const float* __restrict__ w,
                 const YT* residual, YT* y) {
-    using VO = Vec<OT, N>;
-    using VY = Vec<YT, N>;
     const int64_t t = blockIdx.x / per_row;
-    const int c = (int)(blockIdx.x - t * per_row) * 256 + threadIdx.x;
+    const int c = ((int)(blockIdx.x - t * per_row) * 256 + threadIdx.x) * N;
     pdl_trigger();
     pdl_wait();
-    if (c >= nvec) return;
-    float acc[N];
+    const Picks picks(inv, w, t, k, P);
+    const bool in = c < H;
+    F<N> acc;
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc[i] = 0.0f;
-    for (int j0 = 0; j0 < k; j0 += 8) {
-        VO v[8];
+    for (int i = 0; i < N; ++i) acc.v[i] = 0.0f;
+    unsigned live = picks.live;
+    while (live) {
+        Vec<OT, N> v[8];
         float wj[8];
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            const int64_t p = j0 + j < k ? pick_row(inv, t * k + j0 + j, P) : -1;
             wj[j] = 0.0f;
-            if (p >= 0) {
-                v[j] = reinterpret_cast<const VO*>(o)[p * nvec + c];
-                wj[j] = w ? w[t * k + j0 + j] : 1.0f;
+            if (live) {
+                const int at = __ffs(live) - 1;
+                live &= live - 1;
+                const int64_t p = __shfl_sync(0xffffffffu, picks.row, at);
+                wj[j] = __shfl_sync(0xffffffffu, picks.w, at);
+                if (in) v[j] = ldv<OT, N>(o + p * H + c);
             } else {
 #pragma unroll
                 for (int i = 0; i < N; ++i) v[j].v[i] = from_f32<OT>(0.0f);
@@ -242,59 +259,73 @@ rows_sum_kernel(const OT* __restrict__ o, int64_t P, int nvec, int per_row, int 
 #pragma unroll
         for (int j = 0; j < 8; ++j)
 #pragma unroll
-            for (int i = 0; i < N; ++i) acc[i] = fmaf(wj[j], to_f32(v[j].v[i]), acc[i]);
+            for (int i = 0; i < N; ++i) acc.v[i] = fmaf(wj[j], to_f32(v[j].v[i]), acc.v[i]);
     }
-    VY out;
-    if (residual) out = reinterpret_cast<const VY*>(residual)[t * nvec + c];
+    if (!in) return;
+    if (residual) {
+        const F<N> r = ldf<YT, N>(residual + t * H + c);
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        out.v[i] = from_f32<YT>(residual ? to_f32(out.v[i]) + acc[i] : acc[i]);
-    reinterpret_cast<VY*>(y)[t * nvec + c] = out;
+        for (int i = 0; i < N; ++i) acc.v[i] += r.v[i];
+    }
+    stf<YT, N>(y + t * H + c, acc);
 }
 
 // Gradients of the weighted sum: one CTA per token, eight picks at a time; a
 // thread walks its columns of dy, writes w * dy into the picks' rows and keeps
 // their dot products with o, which the CTA then sums in a fixed order.
 template <typename YT, typename OT, int N>
-__global__ void __launch_bounds__(256)
-rows_sum_backward_kernel(const YT* __restrict__ dy, const OT* __restrict__ o, int64_t P, int nvec,
+__global__ void __launch_bounds__(256, 2)
+rows_sum_backward_kernel(const YT* __restrict__ dy, const OT* __restrict__ o, int64_t P, int H,
                          int k, const int32_t* __restrict__ inv, const float* __restrict__ w,
                          OT* __restrict__ d_o, float* __restrict__ dw) {
-    using VO = Vec<OT, N>;
-    using VY = Vec<YT, N>;
     __shared__ float part[8][8];
     const int64_t t = blockIdx.x;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     pdl_trigger();
     pdl_wait();
-    for (int j0 = 0; j0 < k; j0 += 8) {
-        int64_t row[8];
-        float wj[8], dot[8];
+    const Picks picks(inv, w, t, k, P);
+    if (dw && threadIdx.x < 32 && lane < k && !(picks.live >> lane & 1)) dw[t * k + lane] = 0.0f;
+    for (unsigned live = picks.live, next; live; live = next) {
+        float dot[8];
+        int n = 0;
+        next = live;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            row[j] = j0 + j < k ? pick_row(inv, t * k + j0 + j, P) : -1;
-            wj[j] = row[j] >= 0 && w ? w[t * k + j0 + j] : 1.0f;
             dot[j] = 0.0f;
+            if (next) { next &= next - 1; ++n; }
         }
-        for (int c = threadIdx.x; c < nvec; c += 256) {
-            const VY g = reinterpret_cast<const VY*>(dy)[t * nvec + c];
-            VO v[8];
+        for (int c0 = 0; c0 < H; c0 += 256 * N) {
+            const int c = c0 + (int)threadIdx.x * N;
+            const bool in = c < H;
+            F<N> g;
+            if (in) g = ldf<YT, N>(dy + t * H + c);
+            Vec<OT, N> v[8];
             if (dw) {
+                unsigned m = live;
 #pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (row[j] >= 0) v[j] = reinterpret_cast<const VO*>(o)[row[j] * nvec + c];
+                for (int j = 0; j < 8; ++j) {
+                    if (j >= n) break;
+                    const int64_t p = __shfl_sync(0xffffffffu, picks.row, __ffs(m) - 1);
+                    m &= m - 1;
+                    if (in) v[j] = ldv<OT, N>(o + p * H + c);
+                }
             }
+            unsigned m = live;
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                if (row[j] < 0) continue;
-                VO out;
+                if (j >= n) break;
+                const int at = __ffs(m) - 1;
+                m &= m - 1;
+                const int64_t p = __shfl_sync(0xffffffffu, picks.row, at);
+                const float wj = __shfl_sync(0xffffffffu, picks.w, at);
+                if (!in) continue;
+                F<N> out;
 #pragma unroll
                 for (int i = 0; i < N; ++i) {
-                    const float gi = to_f32(g.v[i]);
-                    if (dw) dot[j] = fmaf(to_f32(v[j].v[i]), gi, dot[j]);
-                    out.v[i] = from_f32<OT>(wj[j] * gi);
+                    if (dw) dot[j] = fmaf(to_f32(v[j].v[i]), g.v[i], dot[j]);
+                    out.v[i] = wj * g.v[i];
                 }
-                if (d_o) reinterpret_cast<VO*>(d_o)[row[j] * nvec + c] = out;
+                if (d_o) stf<OT, N>(d_o + p * H + c, out);
             }
         }
         if (!dw) continue;
@@ -304,11 +335,13 @@ rows_sum_backward_kernel(const YT* __restrict__ dy, const OT* __restrict__ o, in
             if (lane == 0) part[j][warp] = s;
         }
         __syncthreads();
-        if (threadIdx.x < 8 && j0 + (int)threadIdx.x < k) {
+        if (threadIdx.x < n) {
+            unsigned m = live;
+            for (int j = 0; j < (int)threadIdx.x; ++j) m &= m - 1;
             float s = 0.0f;
 #pragma unroll
             for (int i = 0; i < 8; ++i) s += part[threadIdx.x][i];
-            dw[t * k + j0 + threadIdx.x] = s;
+            dw[t * k + __ffs(m) - 1] = s;
         }
         __syncthreads();
     }
