@@ -54,10 +54,13 @@ int launch_rows_sum(const void* o, int T, int H, int k, const int32_t* inv, cons
     constexpr int N = 16 / sizeof(OT);
     constexpr int ya = N * sizeof(YT);
     const bool wide = H % N == 0 && aligned(o, 16) && aligned(residual, ya) && aligned(y, ya);
-    const int per = ((wide ? H / N : H) + 255) / 256;
+    const int cols = 32 * (wide ? N : 1);
+    const int64_t items = (int64_t)T * ((H + cols - 1) / cols);
     const auto kern = wide ? rows_sum_kernel<OT, YT, N> : rows_sum_kernel<OT, YT, 1>;
-    return launch_pdl(kern, dim3((unsigned)T * per), 256, 0, st, "combine", (const OT*)o, (int64_t)T * k,
-                      H, per, k, inv, w, (const YT*)residual, (YT*)y);
+    // as many CTAs as the SMs hold at three each, and no more than there are warps of work
+    const int grid = (int)std::min<int64_t>((items + 7) / 8, 3 * 148);
+    return launch_pdl(kern, dim3(grid), 256, 0, st, "combine", (const OT*)o, (int64_t)T * k, T, H, k, inv, w,
+                      (const YT*)residual, (YT*)y);
 }
 
 template <typename YT, typename OT>
@@ -67,7 +70,7 @@ int launch_rows_sum_backward(const void* dy, const void* o, int T, int H, int k,
     constexpr int ya = N * sizeof(YT);
     const bool wide = H % N == 0 && aligned(o, 16) && aligned(d_o, 16) && aligned(dy, ya);
     const auto kern = wide ? rows_sum_backward_kernel<YT, OT, N> : rows_sum_backward_kernel<YT, OT, 1>;
-    return launch_pdl(kern, dim3(T), 256, 0, st, "combine backward", (const YT*)dy, (const OT*)o,
+    return launch_pdl(kern, dim3((unsigned)(((int64_t)T * k + 7) / 8)), 256, 0, st, "combine backward", (const YT*)dy, (const OT*)o,
                       (int64_t)T * k, H, k, inv, w, (OT*)d_o, dw);
 }
 

@@ -111,7 +111,8 @@ int coli_moe_fp4_quantize(coli_fp4 fmt, const void* x, coli_dtype xt, int64_t n_
     const int chunks = (K + 255) / 256;
     int rows_per = 8;
     while (rows_per > 1 && 8 / rows_per < chunks) rows_per /= 2;
-    const dim3 grid((unsigned)((rows + rows_per - 1) / rows_per));
+    const int warps = 8 / rows_per;
+    const dim3 grid((unsigned)((rows + rows_per - 1) / rows_per), (chunks + warps - 1) / warps);
     if (xt == COLI_F32)
         return launch_pdl(fmt == COLI_NVFP4 ? fp4_quantize_kernel<float, true> : fp4_quantize_kernel<float, false>, grid,
                           256, 0, S(stream), "fp4 quantize", a, rows_per, (const float*)x, (float*)values);

@@ -11,10 +11,14 @@
 // pipe and the shared memory that feeds it.
 //
 // One unit of work is a stage: 256 columns (128 bytes) of one tile.  A tile is
-// (expert, 128 weight rows, NT of its rows); all units of all tiles, in the order
-// (expert, weight rows, rows, columns), are cut into equal runs, one per CTA,
-// so that every SM streams the same number of bytes whatever the routing.  A
-// tile that a run's border cuts leaves f32 partial sums in the workspace: every
+// (expert, 128 weight rows, NT of its rows), in the order (expert, weight rows,
+// rows).  As many whole waves of tiles as there are go to the CTAs in turn, so
+// that the SMs work on neighbouring tiles, whose weights and rows then come from
+// L2 (runs of tiles per CTA read 3.6 GB from HBM where this order reads
+// WAVE_READ, at 4096 tokens x 8 picks on 32 experts of 4096 x 6144).  The tiles
+// that are left over, all of them at few rows, are cut by units into equal runs, one
+// per CTA, so that every SM streams the same number of bytes.  A tile that a
+// run's border cuts leaves f32 partial sums in the workspace: every
 // CTA that does not begin the tile stores its piece and raises a flag, and the
 // one that begins it, whose piece is the last of its run, adds them in the
 // order of their columns.  No atomics, the same bits at every run; the others
@@ -58,8 +62,9 @@ __device__ __forceinline__ int64_t scale_word(int64_t r, int w, int words) {
 
 // A lane holds 8 columns of a row, a warp 256 at a time: 16 bytes of bf16 (32
 // of f32) per load, a block's maximum by one or two shuffles.  A CTA's 8 warps
-// share out `rows_per` rows, 8 / rows_per warps each.  Bound by HBM (x once,
-// codes, scales and values once).
+// share out `rows_per` rows, 8 / rows_per warps each; one chunk per warp, since
+// many small CTAs hide the loads better than a warp's loop over its row does.
+// Bound by HBM (x once, codes, scales and values once).
 template <typename T, bool NV>
 __device__ __forceinline__ void fp4_quantize_chunk(const Fp4QuantArgs& a, const T* __restrict__ x,
                                                    T* __restrict__ values, int64_t r, int64_t from, int c,
@@ -141,14 +146,12 @@ __global__ void __launch_bounds__(256)
 fp4_quantize_kernel(Fp4QuantArgs a, int rows_per, const T* __restrict__ x, T* __restrict__ values) {
     const int warps = 8 / rows_per, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t r = (int64_t)blockIdx.x * rows_per + warp / warps;
+    const int c0 = ((int)blockIdx.y * warps + (warp & (warps - 1))) * 256;
     pdl_trigger();
     pdl_wait();
-    if (r >= a.rows || (a.count && r >= *a.count)) return;
-    const int64_t from = a.src ? a.src[r] : r;
-    const float g = NV && a.gscale ? *a.gscale : 1.0f;
-#pragma unroll 2
-    for (int c0 = (warp & (warps - 1)) * 256; c0 < a.K; c0 += warps * 256)
-        fp4_quantize_chunk<T, NV>(a, x, values, r, from, c0 + lane * 8, g);
+    if (r >= a.rows || c0 >= a.K || (a.count && r >= *a.count)) return;
+    fp4_quantize_chunk<T, NV>(a, x, values, r, a.src ? a.src[r] : r, c0 + lane * 8,
+                              NV && a.gscale ? *a.gscale : 1.0f);
 }
 
 // ---------------------------------------------------------------------------
@@ -253,13 +256,16 @@ __device__ __forceinline__ void fp_plan(const FpArgs& a, FpPlan& p) {
     __syncthreads();
 }
 
-// run of CTA c: units [lo, hi)
+// The share of every CTA: tiles c, c + G, .. of the first waves * G, and units
+// [lo(c), lo(c + 1)) of the tiles from tile0 on.
 struct FpRun {
-    int64_t U;
-    int64_t G;
+    int64_t G, waves, tile0, U;
     __device__ __forceinline__ FpRun(const FpArgs& a, const FpPlan& p, int grid) {
-        U = p.tile0[a.E] * a.KS;
-        G = min((int64_t)grid, max((int64_t)1, U / kFpMinUnits));
+        const int64_t tiles = p.tile0[a.E];
+        G = min((int64_t)grid, max((int64_t)1, tiles * a.KS / kFpMinUnits));
+        waves = tiles / G;
+        tile0 = waves * G;
+        U = (tiles - tile0) * a.KS;
     }
     __device__ __forceinline__ int64_t lo(int64_t c) const { return c >= G ? U : U * c / G; }
 };
@@ -288,19 +294,42 @@ __device__ __forceinline__ FpTile fp_tile(const FpPlan& p, int E, int64_t tile) 
     return t;
 }
 
-// A run's pieces: (tile, stages [k0, k1) of it).
-struct FpPiece {
+// A CTA's pieces in order: (tile, stages [k0, k1) of it), the cut tiles first.
+struct FpPieces {
+    int64_t u, hi, tile0, left, at, step;
+    int KS;
     int64_t tile;
     int k0, k1;
+    __device__ __forceinline__ FpPieces(const FpArgs& a, const FpRun& r, int64_t c) {
+        u = r.lo(c);
+        hi = r.lo(c + 1);
+        tile0 = r.tile0;
+        left = c < r.G ? r.waves : 0;
+        at = c;
+        step = r.G;
+        KS = a.KS;
+        tile = 0;
+        k0 = k1 = 0;
+    }
+    __device__ __forceinline__ int64_t stages() const { return hi - u + left * KS; }  // before the first next()
+    __device__ __forceinline__ bool next() {
+        if (u < hi) {
+            tile = u / KS;
+            k0 = (int)(u - tile * KS);
+            k1 = (int)min((int64_t)KS, k0 + (hi - u));
+            u += k1 - k0;
+            tile += tile0;
+            return true;
+        }
+        if (left == 0) return false;
+        --left;
+        tile = at;
+        at += step;
+        k0 = 0;
+        k1 = KS;
+        return true;
+    }
 };
-__device__ __forceinline__ bool fp_next(int64_t& u, int64_t hi, int KS, FpPiece& q) {
-    if (u >= hi) return false;
-    q.tile = u / KS;
-    q.k0 = (int)(u - q.tile * KS);
-    q.k1 = (int)min((int64_t)KS, q.k0 + (hi - u));
-    u += q.k1 - q.k0;
-    return true;
-}
 
 // shared-memory descriptor of a 32-row, 16-byte-wide scale tile (no swizzle,
 // 8-row groups 128 bytes apart)
@@ -389,15 +418,13 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     tc_fence_after();
     const uint32_t tmem = tmem_slot;
     const FpRun run(a, plan, gridDim.x);
-    const int64_t lo = run.lo(blockIdx.x), hi = run.lo(blockIdx.x + 1);
+    FpPieces q(a, run, blockIdx.x);
     bool ok = true;  // cleared by a wait that gave up: then no further waits
-    int64_t u = lo;
-    FpPiece q;
 
     if (warp == 0) {
         // ---------------- copies (whole warp, elected lane issues) ----------------
         int cnt = 0;
-        while (fp_next(u, hi, a.KS, q)) {
+        while (q.next()) {
             const FpTile t = fp_tile<NT>(plan, a.E, q.tile);
             const int64_t wrow = (int64_t)t.e * a.R + (int64_t)t.rt * 128;
             const int boxes = (t.n + C::box - 1) / C::box;
@@ -423,7 +450,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         const uint32_t one = elect_one();
         const uint32_t sbase = smem_u32(smem);
         int cnt = 0, piece = 0;
-        for (; fp_next(u, hi, a.KS, q); ++piece) {
+        for (; q.next(); ++piece) {
             const FpTile t = fp_tile<NT>(plan, a.E, q.tile);
             const uint32_t idesc = idesc_fp4<NV>((t.n + 15) / 16 * 16);
             const int buf = piece & 1;
@@ -477,10 +504,10 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         const int par = warp - 2;
         uint32_t w[ahead][mine][words];
         FpTile t;
-        q.k0 = q.k1 = 0;
+        const int64_t total = q.stages();
         const auto load = [&](uint32_t (&to)[mine][words]) {  // the next stage's words, if there is one
             if (q.k0 == q.k1) {
-                if (!fp_next(u, hi, a.KS, q)) return;
+                if (!q.next()) return;
                 t = fp_tile<NT>(plan, a.E, q.tile);
             }
 #pragma unroll
@@ -495,7 +522,6 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             }
             ++q.k0;
         };
-        const int64_t total = hi - lo;
 #pragma unroll
         for (int d = 0; d < ahead; ++d) load(w[d]);
         for (int64_t base = 0; base < total; base += ahead) {
@@ -521,7 +547,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     } else {
         // ---------------- stores: weight rows 32 quarter + lane of the tile ----------------
         const int quarter = warp & 3;
-        for (int piece = 0; fp_next(u, hi, a.KS, q); ++piece) {
+        for (int piece = 0; q.next(); ++piece) {
             const FpTile t = fp_tile<NT>(plan, a.E, q.tile);
             const int buf = piece & 1;
             const int row = t.rt * 128 + 32 * quarter + lane;
@@ -532,7 +558,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             // starts at its end or later
             int64_t last = blockIdx.x + 1;
             if (begins && q.k1 < a.KS)
-                while (run.lo(last) < (q.tile + 1) * a.KS) ++last;
+                while (run.lo(last) < (q.tile + 1 - run.tile0) * a.KS) ++last;
             if (ok && !mbar_wait_warp(&accfull[buf], (piece >> 1) & 1, a.err)) ok = false;
             tc_fence_after();
             for (int64_t c = blockIdx.x + 1; c < last; ++c)

@@ -133,10 +133,10 @@ block_norm_kernel(NormArgs a, const XT* x, const BT* o, XT* x_out, BT* n_out, fl
 #pragma unroll
                 for (int j = 0; j < V; ++j) f.v[j] = f.v[j] * r * pg.v[j];
             }
-            // xv becomes the stored value, which the norm below reads
+            const F<V> xf = widen<XT, V>(xv[i]);
 #pragma unroll
-            for (int j = 0; j < V; ++j)
-                xv[i].v[j] = from_f32<XT>(fmaf(a.alpha * g.v[j], f.v[j], to_f32(xv[i].v[j])));
+            for (int j = 0; j < V; ++j) f.v[j] = fmaf(a.alpha * g.v[j], f.v[j], xf.v[j]);
+            xv[i] = narrow<XT, V>(f);  // the stored value, which the norm below reads
             stv<XT, V>(x_out + row + c, xv[i]);
         }
     }
@@ -259,12 +259,13 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, const XT* x_out, const BT*
                 const int c = c0 + i * step;
                 if (c >= a.H) continue;
                 const F<V> pg = gain_at<V>(a.pre_gain, c);
+                const F<V> xf = widen<XT, V>(xv[i]), gf = widen<BT, V>(gv[i]);
                 F<V> p;
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
-                    const float xh = to_f32(xv[i].v[j]) * rx, g = to_f32(gv[i].v[j]);
-                    p.v[j] = g * xh;
-                    const float v = g * pg.v[j];
+                    const float xh = xf.v[j] * rx;
+                    p.v[j] = gf.v[j] * xh;
+                    const float v = gf.v[j] * pg.v[j];
                     s1[0] = fmaf(v, xh, s1[0]);
                     d[i].v[j] = fmaf(rx, v, d[i].v[j]);
                 }
@@ -275,8 +276,9 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, const XT* x_out, const BT*
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 if (c0 + i * step >= a.H) continue;
+                const F<V> xf = widen<XT, V>(xv[i]);
 #pragma unroll
-                for (int j = 0; j < V; ++j) d[i].v[j] = fmaf(-m, to_f32(xv[i].v[j]) * rx, d[i].v[j]);
+                for (int j = 0; j < V; ++j) d[i].v[j] = fmaf(-m, xf.v[j] * rx, d[i].v[j]);
             }
         }
         float s2[2] = {0.0f, 0.0f};  // q oh, alpha u d (token gates)
@@ -288,10 +290,11 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, const XT* x_out, const BT*
             if (!o) continue;
             const F<V> g = gate_at<V>(a, t, c);
             const F<V> pg = a.post_norm ? gain_at<V>(a.post_gain, c) : ones<V>();
+            const F<V> of = widen<BT, V>(ov[i]);
             F<V> dg, dp;
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const float oh = to_f32(ov[i].v[j]) * ro;
+                const float oh = of.v[j] * ro;
                 const float ad = a.alpha * d[i].v[j];
                 dg.v[j] = ad * (oh * pg.v[j]);
                 s2[1] += dg.v[j];
@@ -316,9 +319,9 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, const XT* x_out, const BT*
             for (int i = 0; i < N; ++i) {
                 const int c = c0 + i * step;
                 if (c >= a.H) continue;
-                F<V> r;
+                F<V> r = widen<BT, V>(ov[i]);
 #pragma unroll
-                for (int j = 0; j < V; ++j) r.v[j] = ro * fmaf(-m, to_f32(ov[i].v[j]) * ro, d[i].v[j]);
+                for (int j = 0; j < V; ++j) r.v[j] = ro * fmaf(-m, r.v[j] * ro, d[i].v[j]);
                 stf<BT, V>(d_o + row + c, r);
             }
         }

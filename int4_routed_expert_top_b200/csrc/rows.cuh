@@ -218,132 +218,125 @@ dispatch_kernel(const V* __restrict__ x, int64_t P, int nvec, int per_row, int k
     }
 }
 
-// y[t] = residual[t] + sum_j w[t, j] o[inv[t, j]]: a thread owns N columns of
-// one token.  Picks are taken in slot order, eight at a time so that their
-// loads are in flight together; every warp reads the token's picks once, a lane
-// each, instead of every thread all of them.  64 registers keep 1024 threads
-// of an SM (128 KB of loads) busy: 4096 tokens x 8 picks of 6144 bf16 take
-// KERNEL_TIME.
+// y[t] = residual[t] + sum_j w[t, j] o[inv[t, j]]: a warp owns 32 N columns of
+// one token, then the next of its share.  Picks are taken in slot order, eight
+// at a time so that their loads are in flight together; the next item's picks
+// are read while this one's rows are on their way, and the residual is asked
+// for before them, so that a warp waits for HBM about once an item.
 template <typename OT, typename YT, int N>
 __global__ void __launch_bounds__(256, 3)
-rows_sum_kernel(const OT* __restrict__ o, int64_t P, int H, int per_row, int k,
+rows_sum_kernel(const OT* __restrict__ o, int64_t P, int T, int H, int k,
                 const int32_t* __restrict__ inv, const float* __restrict__ w,
                 const YT* residual, YT* y) {
-    const int64_t t = blockIdx.x / per_row;
-    const int c = ((int)(blockIdx.x - t * per_row) * 256 + threadIdx.x) * N;
+    const int per = (H + 32 * N - 1) / (32 * N);        // items of a token
+    const int64_t items = (int64_t)T * per, step = (int64_t)gridDim.x * 8;
+    int64_t item = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     pdl_trigger();
     pdl_wait();
-    const Picks picks(inv, w, t, k, P);
-    const bool in = c < H;
-    F<N> acc;
+    if (item >= items) return;
+    Picks picks(inv, w, item / per, k, P);
+    for (;;) {
+        const int64_t t = item / per;
+        const int c = ((int)(item - t * per) * 32 + (threadIdx.x & 31)) * N;
+        const bool in = c < H;
+        F<N> acc, res;
 #pragma unroll
-    for (int i = 0; i < N; ++i) acc.v[i] = 0.0f;
-    unsigned live = picks.live;
-    while (live) {
-        Vec<OT, N> v[8];
-        float wj[8];
+        for (int i = 0; i < N; ++i) acc.v[i] = 0.0f;
+        if (residual && in) res = ldf<YT, N>(residual + t * H + c);
+        item += step;
+        Picks after = picks;
+        bool first = true;
+        for (unsigned live = picks.live; live || first;) {
+            Vec<OT, N> v[8];
+            const unsigned group = live;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            wj[j] = 0.0f;
-            if (live) {
-                const int at = __ffs(live) - 1;
-                live &= live - 1;
-                const int64_t p = __shfl_sync(0xffffffffu, picks.row, at);
-                wj[j] = __shfl_sync(0xffffffffu, picks.w, at);
-                if (in) v[j] = ldv<OT, N>(o + p * H + c);
-            } else {
+            for (int j = 0; j < 8; ++j)
+                if (live) {
+                    const int64_t p = __shfl_sync(0xffffffffu, picks.row, __ffs(live) - 1);
+                    live &= live - 1;
+                    if (in) v[j] = ldv<OT, N>(o + p * H + c);
+                }
+            if (first && item < items) after = Picks(inv, w, item / per, k, P);
+            first = false;
+            unsigned m = group;
 #pragma unroll
-                for (int i = 0; i < N; ++i) v[j].v[i] = from_f32<OT>(0.0f);
-            }
+            for (int j = 0; j < 8; ++j)
+                if (m) {
+                    const float wj = __shfl_sync(0xffffffffu, picks.w, __ffs(m) - 1);
+                    m &= m - 1;
+                    const F<N> f = widen<OT, N>(v[j]);
+#pragma unroll
+                    for (int i = 0; i < N; ++i) acc.v[i] = fmaf(wj, f.v[i], acc.v[i]);
+                }
         }
+        if (in) {
+            if (residual) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j)
-#pragma unroll
-            for (int i = 0; i < N; ++i) acc.v[i] = fmaf(wj[j], to_f32(v[j].v[i]), acc.v[i]);
+                for (int i = 0; i < N; ++i) acc.v[i] += res.v[i];
+            }
+            stf<YT, N>(y + t * H + c, acc);
+        }
+        if (item >= items) return;
+        picks = after;
     }
-    if (!in) return;
-    if (residual) {
-        const F<N> r = ldf<YT, N>(residual + t * H + c);
-#pragma unroll
-        for (int i = 0; i < N; ++i) acc.v[i] += r.v[i];
-    }
-    stf<YT, N>(y + t * H + c, acc);
 }
 
-// Gradients of the weighted sum: one CTA per token, eight picks at a time; a
-// thread walks its columns of dy, writes w * dy into the picks' rows and keeps
-// their dot products with o, which the CTA then sums in a fixed order.
+// Gradients of the weighted sum: one warp per pick walks its row, writes w * dy
+// into it and keeps the dot product of dy and o, with no barrier; the warps of a
+// token's picks meet its dy in L1.
 template <typename YT, typename OT, int N>
-__global__ void __launch_bounds__(256, 2)
+__global__ void __launch_bounds__(256, 3)
 rows_sum_backward_kernel(const YT* __restrict__ dy, const OT* __restrict__ o, int64_t P, int H,
                          int k, const int32_t* __restrict__ inv, const float* __restrict__ w,
                          OT* __restrict__ d_o, float* __restrict__ dw) {
-    __shared__ float part[8][8];
-    const int64_t t = blockIdx.x;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr int U = 4;  // vectors of a lane in flight
+    const int lane = threadIdx.x & 31;
+    const int64_t i = (int64_t)blockIdx.x * 8 + (threadIdx.x >> 5);
     pdl_trigger();
     pdl_wait();
-    const Picks picks(inv, w, t, k, P);
-    if (dw && threadIdx.x < 32 && lane < k && !(picks.live >> lane & 1)) dw[t * k + lane] = 0.0f;
-    for (unsigned live = picks.live, next; live; live = next) {
-        float dot[8];
-        int n = 0;
-        next = live;
+    if (i >= P) return;
+    const int64_t p = inv[i];
+    if (p < 0 || p >= P) {
+        if (dw && lane == 0) dw[i] = 0.0f;
+        return;
+    }
+    const float wj = w ? w[i] : 1.0f;
+    const YT* g_row = dy + i / k * H;
+    const OT* o_row = o + p * H;
+    OT* d_row = d_o + p * H;
+    F<N> dot;  // a sum per element of the vector: N short chains
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            dot[j] = 0.0f;
-            if (next) { next &= next - 1; ++n; }
+    for (int e = 0; e < N; ++e) dot.v[e] = 0.0f;
+    for (int c0 = lane * N; c0 < H; c0 += 32 * N * U) {
+        F<N> g[U];
+        Vec<OT, N> v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * 32 * N;
+            if (c >= H) continue;
+            if (dw) v[u] = ldv<OT, N>(o_row + c);
+            g[u] = ldf<YT, N>(g_row + c);
         }
-        for (int c0 = 0; c0 < H; c0 += 256 * N) {
-            const int c = c0 + (int)threadIdx.x * N;
-            const bool in = c < H;
-            F<N> g;
-            if (in) g = ldf<YT, N>(dy + t * H + c);
-            Vec<OT, N> v[8];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const int c = c0 + u * 32 * N;
+            if (c >= H) continue;
             if (dw) {
-                unsigned m = live;
+                const F<N> f = widen<OT, N>(v[u]);
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    if (j >= n) break;
-                    const int64_t p = __shfl_sync(0xffffffffu, picks.row, __ffs(m) - 1);
-                    m &= m - 1;
-                    if (in) v[j] = ldv<OT, N>(o + p * H + c);
-                }
+                for (int e = 0; e < N; ++e) dot.v[e] = fmaf(f.v[e], g[u].v[e], dot.v[e]);
             }
-            unsigned m = live;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                if (j >= n) break;
-                const int at = __ffs(m) - 1;
-                m &= m - 1;
-                const int64_t p = __shfl_sync(0xffffffffu, picks.row, at);
-                const float wj = __shfl_sync(0xffffffffu, picks.w, at);
-                if (!in) continue;
-                F<N> out;
-#pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    if (dw) dot[j] = fmaf(to_f32(v[j].v[i]), g.v[i], dot[j]);
-                    out.v[i] = wj * g.v[i];
-                }
-                if (d_o) stf<OT, N>(d_o + p * H + c, out);
-            }
+            for (int e = 0; e < N; ++e) g[u].v[e] *= wj;
+            if (d_o) stf<OT, N>(d_row + c, g[u]);
         }
-        if (!dw) continue;
+    }
+    if (dw) {
+        float sum = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float s = warp_sum(dot[j]);
-            if (lane == 0) part[j][warp] = s;
-        }
-        __syncthreads();
-        if (threadIdx.x < n) {
-            unsigned m = live;
-            for (int j = 0; j < (int)threadIdx.x; ++j) m &= m - 1;
-            float s = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) s += part[threadIdx.x][i];
-            dw[t * k + __ffs(m) - 1] = s;
-        }
-        __syncthreads();
+        for (int e = 0; e < N; ++e) sum += dot.v[e];
+        sum = warp_sum(sum);
+        if (lane == 0) dw[i] = sum;
     }
 }
 

@@ -19,51 +19,84 @@ template <> __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(flo
     return __float2bfloat16_rn(v);
 }
 
-// N consecutive elements of type T, aligned to their size: one load or store
-// (32 bytes are one access on sm_100, so that a lane writes whole sectors)
-template <typename T, int N> struct alignas(sizeof(T) * N) Vec { T v[N]; };
+// N consecutive elements of type T as they lie in memory, aligned to their size:
+// one load or store (32 bytes are one access on sm_100, so that a lane writes
+// whole sectors).  Kept as 32-bit words, so that values which wait in registers
+// wait in the type they were read in.
+template <typename T, int N> struct Vec {
+    static constexpr int bytes = (int)sizeof(T) * N;
+    static_assert(bytes == 2 || bytes == 4 || bytes == 8 || bytes == 16 || bytes == 32, "one access");
+    uint32_t u[bytes < 4 ? 1 : bytes / 4];
+};
 
 template <typename T, int N>
 __device__ __forceinline__ Vec<T, N> ldv(const T* p) {
     Vec<T, N> r;
-    if constexpr (sizeof(T) * N == 32) {
-        uint32_t* u = reinterpret_cast<uint32_t*>(&r);
+    if constexpr (r.bytes == 32) {
         asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                     : "=r"(u[0]), "=r"(u[1]), "=r"(u[2]), "=r"(u[3]), "=r"(u[4]), "=r"(u[5]), "=r"(u[6]), "=r"(u[7])
+                     : "=r"(r.u[0]), "=r"(r.u[1]), "=r"(r.u[2]), "=r"(r.u[3]), "=r"(r.u[4]), "=r"(r.u[5]),
+                       "=r"(r.u[6]), "=r"(r.u[7])
                      : "l"(p) : "memory");
+    } else if constexpr (r.bytes == 16) {
+        const uint4 v = *reinterpret_cast<const uint4*>(p);
+        r.u[0] = v.x; r.u[1] = v.y; r.u[2] = v.z; r.u[3] = v.w;
+    } else if constexpr (r.bytes == 8) {
+        const uint2 v = *reinterpret_cast<const uint2*>(p);
+        r.u[0] = v.x; r.u[1] = v.y;
+    } else if constexpr (r.bytes == 4) {
+        r.u[0] = *reinterpret_cast<const uint32_t*>(p);
     } else {
-        static_assert(sizeof(T) * N <= 16, "a load is 1 to 16 or 32 bytes");
-        r = *reinterpret_cast<const Vec<T, N>*>(p);
+        r.u[0] = *reinterpret_cast<const uint16_t*>(p);
     }
     return r;
 }
 template <typename T, int N>
 __device__ __forceinline__ void stv(T* p, const Vec<T, N>& r) {
-    if constexpr (sizeof(T) * N == 32) {
-        const uint32_t* u = reinterpret_cast<const uint32_t*>(&r);
+    if constexpr (r.bytes == 32)
         asm volatile("st.global.v8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};"
-                     ::"r"(u[0]), "r"(u[1]), "r"(u[2]), "r"(u[3]), "r"(u[4]), "r"(u[5]), "r"(u[6]), "r"(u[7]), "l"(p)
+                     ::"r"(r.u[0]), "r"(r.u[1]), "r"(r.u[2]), "r"(r.u[3]), "r"(r.u[4]), "r"(r.u[5]), "r"(r.u[6]),
+                       "r"(r.u[7]), "l"(p)
                      : "memory");
-    } else {
-        static_assert(sizeof(T) * N <= 16, "a store is 1 to 16 or 32 bytes");
-        *reinterpret_cast<Vec<T, N>*>(p) = r;
-    }
+    else if constexpr (r.bytes == 16)
+        *reinterpret_cast<uint4*>(p) = make_uint4(r.u[0], r.u[1], r.u[2], r.u[3]);
+    else if constexpr (r.bytes == 8)
+        *reinterpret_cast<uint2*>(p) = make_uint2(r.u[0], r.u[1]);
+    else if constexpr (r.bytes == 4)
+        *reinterpret_cast<uint32_t*>(p) = r.u[0];
+    else
+        *reinterpret_cast<uint16_t*>(p) = (uint16_t)r.u[0];
 }
 
-// the same as f32 values
+// the same as f32 values, and back (rounded to nearest even)
 template <int N> struct F { float v[N]; };
 template <typename T, int N> __device__ __forceinline__ F<N> widen(const Vec<T, N>& a) {
     F<N> r;
 #pragma unroll
-    for (int i = 0; i < N; ++i) r.v[i] = to_f32(a.v[i]);
+    for (int i = 0; i < N; ++i) {
+        if constexpr (sizeof(T) == 4)
+            r.v[i] = __uint_as_float(a.u[i]);
+        else  // bf16 is the upper half of an f32
+            r.v[i] = __uint_as_float(i & 1 ? a.u[i / 2] & 0xffff0000u : a.u[i / 2] << 16);
+    }
+    return r;
+}
+template <typename T, int N> __device__ __forceinline__ Vec<T, N> narrow(const F<N>& a) {
+    Vec<T, N> r;
+    if constexpr (sizeof(T) == 4) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) r.u[i] = __float_as_uint(a.v[i]);
+    } else if constexpr (N == 1) {
+        r.u[0] = __bfloat16_as_ushort(__float2bfloat16_rn(a.v[0]));
+    } else {
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(a.v[2 * i], a.v[2 * i + 1]);
+            r.u[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
     return r;
 }
 template <typename T, int N> __device__ __forceinline__ F<N> ldf(const T* p) { return widen<T, N>(ldv<T, N>(p)); }
-template <typename T, int N> __device__ __forceinline__ void stf(T* p, const F<N>& a) {
-    Vec<T, N> r;
-#pragma unroll
-    for (int i = 0; i < N; ++i) r.v[i] = from_f32<T>(a.v[i]);
-    stv<T, N>(p, r);
-}
+template <typename T, int N> __device__ __forceinline__ void stf(T* p, const F<N>& a) { stv<T, N>(p, narrow<T, N>(a)); }
 
 }  // namespace coli
