@@ -107,8 +107,8 @@ int coli_moe_fp4_quantize(coli_fp4 fmt, const void* x, coli_dtype xt, int64_t n_
     a.src = src; a.count = count; a.gscale = gscale;
     a.codes = static_cast<uint8_t*>(codes);
     a.scales = static_cast<uint32_t*>(scales);
-    // warps per row: a power of two, as many as have a chunk of 256 columns
-    const int chunks = (K + 255) / 256;
+    // warps per row: a power of two, as many as have a chunk of columns
+    const int chunks = (K + kQuantCols - 1) / kQuantCols;
     int rows_per = 8;
     while (rows_per > 1 && 8 / rows_per < chunks) rows_per /= 2;
     const int warps = 8 / rows_per;

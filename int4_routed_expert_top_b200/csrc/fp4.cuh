@@ -25,8 +25,12 @@
 // take these pieces first, so the wait is short, and it is never for a CTA with
 // a lower index, so CTAs that are scheduled late cannot stop the earlier ones.
 //
+// Every wait is tried by all lanes of its warp: one lane's answer passed on by a
+// shuffle or a vote costs the issuing warps some 300 cycles a stage (the tile
+// loop took 1.6 to 2.5 times as long).
+//
 // CTA roles: warp 0 copies (codes by 2-D TMA with the 128-byte swizzle, the
-// weights' scales by bulk copy), warps 2-3 bring the rows' scales (rows of an
+// weights' scales by bulk copy), four warps bring the rows' scales (rows of an
 // expert start anywhere, a scale tile only at multiples of 128, so those are
 // gathered by plain loads into a tile in shared memory), warp 1 copies scales
 // to TMEM and issues the products, warps 4-7 store.  Accumulators are
@@ -60,38 +64,62 @@ __device__ __forceinline__ int64_t scale_word(int64_t r, int w, int words) {
     return ((r >> 7) * words + w) * 128 + (r & 31) * 4 + ((r >> 5) & 3);
 }
 
-// A lane holds 8 columns of a row, a warp 256 at a time: 16 bytes of bf16 (32
-// of f32) per load, a block's maximum by one or two shuffles.  A CTA's 8 warps
-// share out `rows_per` rows, 8 / rows_per warps each; one chunk per warp, since
-// many small CTAs hide the loads better than a warp's loop over its row does.
-// Bound by HBM (x once, codes, scales and values once).
+// eight f32 to E2M1 (nearest, ties to even, saturating), the first in the lowest
+// nibble
+__device__ __forceinline__ uint32_t e2m1x8(const float* v) {
+    uint32_t r;
+    asm("{\n .reg .b8 b0, b1, b2, b3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 b0, %2, %1;\n cvt.rn.satfinite.e2m1x2.f32 b1, %4, %3;\n"
+        " cvt.rn.satfinite.e2m1x2.f32 b2, %6, %5;\n cvt.rn.satfinite.e2m1x2.f32 b3, %8, %7;\n"
+        " mov.b32 %0, {b0, b1, b2, b3};\n}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+// A lane holds 16 columns of a row (two or four loads of 16 or 32 bytes), a warp
+// 512: a block is one lane (NVFP4) or two, so its maximum takes at most one
+// shuffle.  A CTA's 8 warps share out `rows_per` rows, 8 / rows_per warps each;
+// one chunk of a row per warp, since many small CTAs hide the loads better than
+// a warp's loop over its row does.  Bound by HBM (x once, codes, scales and
+// values once).
+constexpr int kQuantCols = 512;
+
 template <typename T, bool NV>
-__device__ __forceinline__ void fp4_quantize_chunk(const Fp4QuantArgs& a, const T* __restrict__ x,
-                                                   T* __restrict__ values, int64_t r, int64_t from, int c,
-                                                   float g) {
-    const int lane = threadIdx.x & 31;
-    const bool in = c < a.K;
-    F<8> f;
+__global__ void __launch_bounds__(256)
+fp4_quantize_kernel(Fp4QuantArgs a, int rows_per, const T* __restrict__ x, T* __restrict__ values) {
+    const int warps = 8 / rows_per, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t r = (int64_t)blockIdx.x * rows_per + warp / warps;
+    const int c0 = ((int)blockIdx.y * warps + (warp & (warps - 1))) * kQuantCols;
+    const int c = c0 + lane * 16;
+    pdl_trigger();
+    pdl_wait();
+    if (r >= a.rows || c0 >= a.K || (a.count && r >= *a.count)) return;
+    const bool in = c < a.K;  // K is a multiple of 32: all 16 columns or none
+    const int64_t from = a.src ? a.src[r] : r;
+    const float g = NV && a.gscale ? *a.gscale : 1.0f;
+    float v[16];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) f.v[i] = 0.0f;
+    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
     if (in && from >= 0 && from < a.n_src) {
-        if (a.swiglu) {
-            const T* p = x + from * 2 * a.K + c;
-            f = ldf<T, 8>(p);
-            const F<8> u = ldf<T, 8>(p + a.K);
+        const T* p = x + from * (a.swiglu ? 2 * a.K : a.K) + c;
+        const F<8> lo = ldf<T, 8>(p), hi = ldf<T, 8>(p + 8);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) f.v[i] = silu_f(f.v[i]) * u.v[i];
-        } else {
-            f = ldf<T, 8>(x + from * a.K + c);
+        for (int i = 0; i < 8; ++i) { v[i] = lo.v[i]; v[8 + i] = hi.v[i]; }
+        if (a.swiglu) {
+            const F<8> ulo = ldf<T, 8>(p + a.K), uhi = ldf<T, 8>(p + a.K + 8);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                v[i] = silu_f(v[i]) * ulo.v[i];
+                v[8 + i] = silu_f(v[8 + i]) * uhi.v[i];
+            }
         }
     }
-    const float (&v)[8] = f.v;
     // the largest magnitude as bits: infinities and NaN come out on top
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    if (!NV) m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    if (!NV) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     const bool bad = m >= 0x7f800000u;
     uint32_t byte;
     float d, r_d;  // what a code of 1 stands for, and its reciprocal
@@ -107,57 +135,43 @@ __device__ __forceinline__ void fp4_quantize_chunk(const Fp4QuantArgs& a, const 
         d = __uint_as_float(b ? (uint32_t)b << 23 : 0x00400000u);
         r_d = __uint_as_float((uint32_t)(254 - b) << 23);
     }
-    uint32_t code = 0;
-    if (!bad && (!NV || d > 0.0f)) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            code |= (uint32_t)__nv_cvt_float2_to_fp4x2(
-                        make_float2(__fmul_rn(v[2 * i], r_d), __fmul_rn(v[2 * i + 1], r_d)), __NV_E2M1,
-                        cudaRoundNearest) << (8 * i);
-    }
+    for (int i = 0; i < 16; ++i) v[i] = __fmul_rn(v[i], r_d);
+    uint32_t code[2] = {e2m1x8(v), e2m1x8(v + 8)};
+    if (bad || (NV && !(d > 0.0f))) code[0] = code[1] = 0;
+    // four blocks' bytes make a word: a block is 1 (NV) or 2 lanes
+    constexpr int per = NV ? 1 : 2;
     if (!in) byte = 0;
-    // four blocks' bytes make a word: a block is 2 (NV) or 4 lanes
-    constexpr int per = NV ? 2 : 4;
-    const int first = lane & ~(4 * per - 1);
-    uint32_t word = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) word |= __shfl_sync(0xffffffffu, byte, first + i * per) << (8 * i);
-    if (!in) {
-        if (lane == first && c / (32 * per) < a.words) a.scales[scale_word(r, c / (32 * per), a.words)] = word;
-        return;
-    }
-    if (lane == first) a.scales[scale_word(r, c / (32 * per), a.words)] = word;
-    *reinterpret_cast<uint32_t*>(a.codes + (r * a.K + c) / 2) = code;
+    uint32_t word = byte << (8 * (lane / per & 3));
+    word |= __shfl_xor_sync(0xffffffffu, word, per);
+    word |= __shfl_xor_sync(0xffffffffu, word, 2 * per);
+    const int at = c / (64 * per);
+    if ((lane & (4 * per - 1)) == 0 && at < a.words) a.scales[scale_word(r, at, a.words)] = word;
+    if (!in) return;
+    *reinterpret_cast<uint2*>(a.codes + (r * a.K + c) / 2) = make_uint2(code[0], code[1]);
     if (values) {
-        F<8> q;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __half2 h = __half2(__nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(code >> (8 * i)), __NV_E2M1));
-            q.v[2 * i] = __fmul_rn(__low2float(h), d);
-            q.v[2 * i + 1] = __fmul_rn(__high2float(h), d);
-            if (bad) q.v[2 * i] = q.v[2 * i + 1] = __uint_as_float(0x7fc00000u);
+        for (int h = 0; h < 2; ++h) {
+            F<8> q;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const __half2 two = __half2(
+                    __nv_cvt_fp4x2_to_halfraw2((__nv_fp4x2_storage_t)(code[h] >> (8 * i)), __NV_E2M1));
+                q.v[2 * i] = __fmul_rn(__low2float(two), d);
+                q.v[2 * i + 1] = __fmul_rn(__high2float(two), d);
+                if (bad) q.v[2 * i] = q.v[2 * i + 1] = __uint_as_float(0x7fc00000u);
+            }
+            stf<T, 8>(values + r * a.K + c + 8 * h, q);
         }
-        stf<T, 8>(values + r * a.K + c, q);
     }
-}
-
-template <typename T, bool NV>
-__global__ void __launch_bounds__(256)
-fp4_quantize_kernel(Fp4QuantArgs a, int rows_per, const T* __restrict__ x, T* __restrict__ values) {
-    const int warps = 8 / rows_per, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t r = (int64_t)blockIdx.x * rows_per + warp / warps;
-    const int c0 = ((int)blockIdx.y * warps + (warp & (warps - 1))) * 256;
-    pdl_trigger();
-    pdl_wait();
-    if (r >= a.rows || c0 >= a.K || (a.count && r >= *a.count)) return;
-    fp4_quantize_chunk<T, NV>(a, x, values, r, a.src ? a.src[r] : r, c0 + lane * 8,
-                              NV && a.gscale ? *a.gscale : 1.0f);
 }
 
 // ---------------------------------------------------------------------------
 // product
 // ---------------------------------------------------------------------------
-constexpr int kFpThreads = 256;
+// warps 0 copies, 1 products, 2-3 and 8-9 scales of the rows, 4-7 stores
+constexpr int kFpThreads = 320;
+constexpr int kFpScaleWarps = 4;
 constexpr int kFpMaxE = 1024;
 constexpr int kFpMinUnits = 2;     // stages per CTA at least, before fewer CTAs take part
 constexpr int kFpMaxGrid = 160;    // B200 has 148 SMs; the workspace is sized for this many
@@ -203,7 +217,7 @@ struct FpArgs {
 struct FpPlan {
     int32_t begin[kFpMaxE + 1];
     int64_t tile0[kFpMaxE + 1];
-    int64_t warp_sum[8];
+    int64_t warp_sum[kFpThreads / 32];
 };
 
 // Each thread takes four experts; offsets are clamped so that no value of them
@@ -275,8 +289,10 @@ struct FpTile {
     int64_t p0;         // first row
 };
 
+// Not inlined: five roles call it once a tile, and the loops between those calls
+// have to stay in the instruction cache together.
 template <int NT>
-__device__ __forceinline__ FpTile fp_tile(const FpPlan& p, int E, int64_t tile) {
+__device__ __noinline__ FpTile fp_tile(const FpPlan& p, int E, int64_t tile) {
     int lo = 0, hi = E;  // the last expert whose first tile is not after this one
     while (hi - lo > 1) {
         const int m = (lo + hi) / 2;
@@ -339,8 +355,10 @@ __device__ __forceinline__ uint64_t smem_desc_scales(uint32_t addr) {
 
 // 32 rows x 16 bytes of shared memory to 32 lanes x 4 columns of TMEM, repeated
 // in the four lane quarters
-__device__ __forceinline__ void tc_copy_scales(uint32_t dst, uint64_t desc) {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(dst), "l"(desc) : "memory");
+__device__ __forceinline__ void tc_copy_scales_elect(uint32_t dst, uint64_t desc) {
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}" ::"r"(dst), "l"(desc) : "memory");
 }
 
 // instruction descriptor of a block-scaled product of E2M1 operands, both
@@ -352,25 +370,40 @@ __device__ __forceinline__ constexpr uint32_t idesc_fp4(int n) {
 }
 
 template <bool NV>
-__device__ __forceinline__ void tc_mma_fp4(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                           uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+__device__ __forceinline__ void tc_mma_fp4_elect(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                                 uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
     if (NV)
         asm volatile(
-            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n}"
+            "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+            " @e tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n}"
             ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb));
     else
         asm volatile(
-            "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-            " tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n}"
+            "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
+            " @e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n}"
             ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb));
 }
 
-__device__ __forceinline__ uint32_t elect_one() {
-    uint32_t e;
-    asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.b32 %0, 1, 0, p;\n}" : "=r"(e));
-    return e;
-}
+// A role's place in the ring: slot, the phase of its barriers, and whether the
+// slot has been used before.
+struct Ring {
+    int s = 0;
+    uint32_t phase = 0;
+    bool again = false;
+    __device__ __forceinline__ void next(int stages) {
+        if (++s == stages) {
+            s = 0;
+            phase ^= 1;
+            again = true;
+        }
+    }
+    __device__ __forceinline__ Ring back(int stages) const {  // a whole ring earlier
+        Ring r;
+        r.s = s;
+        r.phase = phase ^ 1;
+        return r;
+    }
+};
 
 // Warp-wide wait for a flag of another CTA's store warp, a second at most
 __device__ __forceinline__ bool fp_wait_flag(const uint64_t* flag, int32_t* err) {
@@ -395,12 +428,12 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     __shared__ FpPlan plan;
     __shared__ __align__(8) uint64_t full[C::stages], empty[C::stages], accfull[2], accempty[2];
     __shared__ uint32_t tmem_slot;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
     if (warp == 0) tmem_alloc(&tmem_slot, C::cols);
     if (threadIdx.x == 32) {
         for (int s = 0; s < C::stages; ++s) {
-            mbar_init(&full[s], 3);   // the copies' announcement and two scale warps
+            mbar_init(&full[s], 1 + kFpScaleWarps);  // the copies' announcement, the scale warps
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -416,142 +449,171 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = uniform(tmem_slot);
     const FpRun run(a, plan, gridDim.x);
     FpPieces q(a, run, blockIdx.x);
     bool ok = true;  // cleared by a wait that gave up: then no further waits
 
     if (warp == 0) {
-        // ---------------- copies (whole warp, elected lane issues) ----------------
-        int cnt = 0;
-        while (q.next()) {
+        // ---------------- copies (whole warp, an elected lane issues) ----------------
+        Ring ring;
+        while (uniform((int)q.next())) {
             const FpTile t = fp_tile<NT>(plan, a.E, q.tile);
-            const int64_t wrow = (int64_t)t.e * a.R + (int64_t)t.rt * 128;
-            const int boxes = (t.n + C::box - 1) / C::box;
-            const uint8_t* sfa = a.ws + (wrow >> 7) * a.wwords * 512;
-            for (int k = q.k0; k < q.k1; ++k, ++cnt) {
-                const int s = cnt % C::stages;
-                if (cnt >= C::stages && ok && !mbar_wait_warp(&empty[s], ((cnt / C::stages) - 1) & 1, a.err)) ok = false;
-                uint8_t* st = smem + s * C::stage;
-                const int na = min(C::atoms, a.wwords - k * C::atoms);
-                mbar_expect_tx_elect(&full[s], (uint32_t)(C::a_bytes + boxes * C::box * 128 + na * 512));
-                tma_load_2d_elect(st, &wmap, k * 128, (int)wrow, &full[s]);
-                for (int b = 0; b < boxes; ++b)
-                    tma_load_2d_elect(st + C::a_bytes + b * C::box * 128, &xmap, k * 128,
-                                      (int)t.p0 + b * C::box, &full[s]);
-                bulk_g2s_elect(st + C::a_bytes + C::b_bytes, sfa + (int64_t)k * C::atoms * 512, na * 512, &full[s]);
+            const int wrow = uniform(t.e * a.R + t.rt * 128), p0 = uniform((int)t.p0);
+            const int boxes = uniform((t.n + C::box - 1) / C::box);
+            const int k0 = uniform(q.k0), k1 = uniform(q.k1);
+            const uint8_t* sfa = a.ws + ((int64_t)(wrow >> 7) * a.wwords + k0 * C::atoms) * 512;
+            const uint32_t bytes = (uint32_t)(C::a_bytes + boxes * C::box * 128);
+#pragma unroll 1
+            for (int k = k0; k < k1; ++k) {
+                if (ok && ring.again && !mbar_wait(&empty[ring.s], ring.phase ^ 1, a.err)) ok = false;
+                uint8_t* st = smem + ring.s * C::stage;
+                uint64_t* bar = &full[ring.s];
+                const uint32_t na = (uint32_t)min(C::atoms, a.wwords - k * C::atoms) * 512;
+                mbar_expect_tx_elect(bar, bytes + na);
+                tma_load_2d_elect(st, &wmap, k * 128, wrow, bar);
+#pragma unroll
+                for (int b = 0; b < NT / C::box; ++b)
+                    if (b < boxes)
+                        tma_load_2d_elect(st + C::a_bytes + b * C::box * 128, &xmap, k * 128, p0 + b * C::box, bar);
+                bulk_g2s_elect(st + C::a_bytes + C::b_bytes, sfa, na, bar);
+                sfa += C::atoms * 512;
+                ring.next(C::stages);
             }
         }
         // the last copies have landed before the CTA may end
-        for (int i = max(0, cnt - C::stages); i < cnt; ++i)
-            mbar_wait_warp_sleep(&full[i % C::stages], (i / C::stages) & 1, a.err);
+        Ring last = ring.back(C::stages);
+        for (int i = 0; i < C::stages; ++i, last.next(C::stages))
+            if (ring.again || last.s < ring.s) mbar_wait(&full[last.s], last.phase, a.err, kSleepTries);
     } else if (warp == 1) {
-        // ---------------- products ----------------
-        const uint32_t one = elect_one();
-        const uint32_t sbase = smem_u32(smem);
-        int cnt = 0, piece = 0;
-        for (; q.next(); ++piece) {
+        // ---------------- products (whole warp, an elected lane issues) ----------------
+        Ring ring;
+        const uint32_t sbase = uniform(smem_u32(smem));
+        uint32_t sf = tmem + C::sf0;          // the stage's scales in TMEM: two sets in turn
+        int piece = 0;
+        for (; uniform((int)q.next()); ++piece) {
             const FpTile t = fp_tile<NT>(plan, a.E, q.tile);
-            const uint32_t idesc = idesc_fp4<NV>((t.n + 15) / 16 * 16);
+            const uint32_t idesc = uniform(idesc_fp4<NV>((t.n + 15) / 16 * 16));
+            const int second = C::nb > 1 ? uniform(t.n > 128 ? 1 : 0) : 0;
+            const int k0 = uniform(q.k0), k1 = uniform(q.k1);
             const int buf = piece & 1;
-            if (piece >= 2 && ok && !mbar_wait_warp(&accempty[buf], ((piece >> 1) - 1) & 1, a.err)) ok = false;
+            if (piece >= 2 && ok && !mbar_wait(&accempty[buf], ((piece >> 1) - 1) & 1, a.err)) ok = false;
             tc_fence_after();
             const uint32_t d = tmem + NT * buf;
-            const int nbk = (t.n + 127) / 128;
-            for (int k = q.k0; k < q.k1; ++k, ++cnt) {
-                const int s = cnt % C::stages;
-                if (ok && !mbar_wait_warp(&full[s], (cnt / C::stages) & 1, a.err)) ok = false;
+            uint32_t more = 0;                // 0: the tile's first product clears the accumulator
+#pragma unroll 1
+            for (int k = k0; k < k1; ++k) {
+                if (ok && !mbar_wait(&full[ring.s], ring.phase, a.err)) ok = false;
                 tc_fence_after();
-                if (one) {
-                    const uint32_t st = sbase + s * C::stage;
-                    const uint32_t sf = tmem + C::sf0 + (cnt & 1) * C::sf_cols;
-                    const uint32_t sfa = st + C::a_bytes + C::b_bytes, sfb = sfa + C::sfa_bytes;
-                    const int cols = min(256, a.K - 256 * k);
-                    const int na = (cols + 256 / C::atoms - 1) / (256 / C::atoms);
+                // the scale warps' plain stores, before the tensor unit's copy reads them: fenced
+                // here, where nothing else is in flight, and not by those warps, whose fence
+                // would wait for their loads
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                const uint32_t st = sbase + ring.s * C::stage;
+                const uint64_t sfa = smem_desc_scales(st + C::a_bytes + C::b_bytes);
+                const uint64_t sfb = sfa + (C::sfa_bytes >> 4);
+                const uint64_t ad = smem_desc_sw128_at(st), bd = ad + (C::a_bytes >> 4);
+                const int cols = a.K - 256 * k;
 #pragma unroll
-                    for (int i = 0; i < C::atoms; ++i) {
-                        if (i >= na) break;
-                        tc_copy_scales(sf + 4 * i, smem_desc_scales(sfa + 512 * i));
-#pragma unroll
-                        for (int b = 0; b < C::nb; ++b)
-                            if (b < nbk)
-                                tc_copy_scales(sf + 4 * C::atoms + 4 * (C::nb * i + b),
-                                               smem_desc_scales(sfb + 512 * (C::nb * i + b)));
-                    }
-                    const uint64_t ad = smem_desc_sw128(smem + s * C::stage);
-                    const uint64_t bd = smem_desc_sw128(smem + s * C::stage + C::a_bytes);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        if (64 * j >= cols) break;
-                        const int at = NV ? j : j >> 1;          // scale tile
-                        const uint32_t id = NV ? 0u : 2u * (j & 1);  // first byte of its words
-                        tc_mma_fp4<NV>(d, ad + 2 * j, bd + 2 * j, idesc | id << 29 | id << 4, sf + 4 * at,
-                                       sf + 4 * C::atoms + 4 * C::nb * at, (k > q.k0 || j > 0) ? 1u : 0u);
-                    }
-                    tc_commit(&empty[s]);
+                for (int i = 0; i < C::atoms; ++i) {
+                    if (i * (256 / C::atoms) >= cols) break;
+                    tc_copy_scales_elect(sf + 4 * i, sfa + 32 * i);
+                    tc_copy_scales_elect(sf + 4 * C::atoms + 4 * C::nb * i, sfb + 32 * C::nb * i);
+                    if (second)
+                        tc_copy_scales_elect(sf + 4 * C::atoms + 4 * C::nb * i + 4, sfb + 32 * C::nb * i + 32);
                 }
-                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if (64 * j >= cols) break;
+                    const int at = NV ? j : j >> 1;              // scale tile
+                    const uint32_t id = NV ? 0u : 2u * (j & 1);  // first byte of its words
+                    tc_mma_fp4_elect<NV>(d, ad + 2 * j, bd + 2 * j, idesc | id << 29 | id << 4, sf + 4 * at,
+                                         sf + 4 * C::atoms + 4 * C::nb * at, more);
+                    more = 1;
+                }
+                tc_commit_elect(&empty[ring.s]);
+                sf = 2 * (tmem + C::sf0) + C::sf_cols - sf;
+                ring.next(C::stages);
             }
-            if (one) tc_commit(&accfull[buf]);
-            __syncwarp();
+            tc_commit_elect(&accfull[buf]);
         }
-    } else if (warp < 4) {
-        // ---------------- scales of the rows: atoms of one parity ----------------
-        // The loads of a stage are issued `ahead` stages before it is stored.
-        constexpr int mine = C::atoms / 2;
-        constexpr int words = NT / 32;        // per lane and atom
-        constexpr int ahead = NT > 64 ? 4 : 8;
-        const int par = warp - 2;
-        uint32_t w[ahead][mine][words];
-        FpTile t;
-        const int64_t total = q.stages();
-        const auto load = [&](uint32_t (&to)[mine][words]) {  // the next stage's words, if there is one
-            if (q.k0 == q.k1) {
-                if (!q.next()) return;
-                t = fp_tile<NT>(plan, a.E, q.tile);
+    } else if (warp < 4 || warp >= 8) {
+        // ---------------- scales of the rows ----------------
+        // A stage has atoms * NT / 32 runs of 32 rows' words; warp f takes runs f, f + 4, ..: a
+        // lane loads its row's word and stores it where the scale tile has it.  The loads of a
+        // stage are issued `ahead` stages before it is stored.
+        constexpr int words = NT / 32;
+        constexpr int items = C::atoms * words;
+        constexpr int mine = (items + kFpScaleWarps - 1) / kFpScaleWarps;
+        constexpr int ahead = 4;
+        const int f = warp < 4 ? warp - 2 : warp - 6;
+        uint32_t w[ahead][mine];
+        const uint32_t* from[mine];  // of the next stage to load, NULL for rows past the tile's
+        uint32_t to[mine];           // byte of the stage
+#pragma unroll
+        for (int i = 0; i < mine; ++i) {
+            const int it = f + kFpScaleWarps * i, atom = it / words, j = it - atom * words;
+            to[i] = C::a_bytes + C::b_bytes + C::sfa_bytes + 512 * (C::nb * atom + j / 4) + 16 * lane + 4 * (j & 3);
+            from[i] = nullptr;
+        }
+        const int64_t total = uniform(q.stages());
+        int k = 0, k1 = 0;
+        const auto load = [&](uint32_t (&dst)[mine]) {  // the next stage's words, if there is one
+            if (k == k1) {
+                if (!uniform((int)q.next())) return;
+                const FpTile t = fp_tile<NT>(plan, a.E, q.tile);
+                k = uniform(q.k0);
+                k1 = uniform(q.k1);
+#pragma unroll
+                for (int i = 0; i < mine; ++i) {
+                    const int it = f + kFpScaleWarps * i, atom = it / words, j = it - atom * words;
+                    const int64_t r = t.p0 + 32 * j + lane;
+                    from[i] = it < items && 32 * j < t.n && r < a.P
+                                  ? a.xs + scale_word(r, k * C::atoms + atom, a.xwords) : nullptr;
+                }
             }
+            const int left = a.xwords - k * C::atoms;  // tiles that the row still has
 #pragma unroll
             for (int i = 0; i < mine; ++i) {
-                const int ch = q.k0 * C::atoms + 2 * i + par;
-#pragma unroll
-                for (int j = 0; j < words; ++j) {
-                    const int64_t r = t.p0 + 32 * j + lane;
-                    to[i][j] = 0;
-                    if (ch < a.xwords && 32 * j < t.n && r < a.P) to[i][j] = __ldg(a.xs + scale_word(r, ch, a.xwords));
+                dst[i] = 0;
+                if (from[i]) {
+                    if (left >= C::atoms || (f + kFpScaleWarps * i) / words < left) dst[i] = __ldg(from[i]);
+                    from[i] += C::atoms * 128;
                 }
             }
-            ++q.k0;
+            ++k;
         };
-#pragma unroll
-        for (int d = 0; d < ahead; ++d) load(w[d]);
-        for (int64_t base = 0; base < total; base += ahead) {
+        Ring ring;
+        const uint32_t sbase = uniform(smem_u32(smem));
+#pragma unroll 1
+        for (int64_t base = -ahead; base < total; base += ahead) {
 #pragma unroll
             for (int d = 0; d < ahead; ++d) {
-                const int cnt = (int)base + d;
-                if (cnt >= total) break;
-                const int s = cnt % C::stages;
-                if (cnt >= C::stages && ok && !mbar_wait_warp(&empty[s], ((cnt / C::stages) - 1) & 1, a.err)) ok = false;
-                uint8_t* sfb = smem + s * C::stage + C::a_bytes + C::b_bytes + C::sfa_bytes;
+                if (base < 0) {
+                    load(w[d]);
+                    continue;
+                }
+                if (base + d >= total) break;
+                if (ok && ring.again && !mbar_wait(&empty[ring.s], ring.phase ^ 1, a.err)) ok = false;
+                const uint32_t st = sbase + ring.s * C::stage;
 #pragma unroll
                 for (int i = 0; i < mine; ++i)
-#pragma unroll
-                    for (int j = 0; j < words; ++j)
-                        *reinterpret_cast<uint32_t*>(sfb + 512 * (C::nb * (2 * i + par) + j / 4) + 16 * lane + 4 * (j & 3)) =
-                            w[d][i][j];
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    if (f + kFpScaleWarps * i < items)
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + to[i]), "r"(w[d][i]) : "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&full[s]);
+                if (lane == 0) mbar_arrive(&full[ring.s]);
+                ring.next(C::stages);
                 load(w[d]);
             }
         }
     } else {
         // ---------------- stores: weight rows 32 quarter + lane of the tile ----------------
         const int quarter = warp & 3;
-        for (int piece = 0; q.next(); ++piece) {
+        for (int piece = 0; uniform((int)q.next()); ++piece) {
             const FpTile t = fp_tile<NT>(plan, a.E, q.tile);
-            const int buf = piece & 1;
+            const int buf = piece & 1, n = uniform(t.n);
             const int row = t.rt * 128 + 32 * quarter + lane;
-            const bool begins = q.k0 == 0;
+            const bool begins = uniform((int)(q.k0 == 0));
             const float al = begins && a.alpha ? a.alpha[t.e] : 1.0f;
             float* part = a.partial + 32 * quarter + lane;
             // the CTAs after this one with pieces of the tile: up to the first whose run
@@ -559,31 +621,35 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             int64_t last = blockIdx.x + 1;
             if (begins && q.k1 < a.KS)
                 while (run.lo(last) < (q.tile + 1 - run.tile0) * a.KS) ++last;
-            if (ok && !mbar_wait_warp(&accfull[buf], (piece >> 1) & 1, a.err)) ok = false;
+            if (ok && !mbar_wait(&accfull[buf], (piece >> 1) & 1, a.err)) ok = false;
             tc_fence_after();
             for (int64_t c = blockIdx.x + 1; c < last; ++c)
                 if (ok && !fp_wait_flag(a.flags + 4 * c + quarter, a.err)) ok = false;
             const uint32_t d = tmem + ((uint32_t)(32 * quarter) << 16) + NT * buf;
-            for (int c0 = 0; c0 < t.n; c0 += 16) {
+            YT* yp = y + t.p0 * a.R + row;        // this lane's row of y's columns
+            float* pp = part + (int64_t)blockIdx.x * (128 * NT);
+#pragma unroll 1
+            for (int c0 = 0; c0 < n; c0 += 16, yp += 16 * (int64_t)a.R, pp += 16 * 128) {
                 uint32_t v[16];
                 tmem_ld_32x32b_x16(d + c0, v);
                 tmem_wait_ld();
+                const int m = n - c0;             // columns of this group, if fewer than 16
                 if (!begins) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        if (c0 + i < t.n) part[(int64_t)blockIdx.x * (128 * NT) + (c0 + i) * 128] = __uint_as_float(v[i]);
+                        if (i < m) pp[i * 128] = __uint_as_float(v[i]);
                     continue;
                 }
                 for (int64_t c = blockIdx.x + 1; c < last; ++c)
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
-                        if (c0 + i < t.n)
+                        if (i < m)
                             v[i] = __float_as_uint(__uint_as_float(v[i]) + __ldcg(part + c * (128 * NT) + (c0 + i) * 128));
                 if (row < a.R) {
+                    YT* to = yp;
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (c0 + i < t.n)
-                            y[(t.p0 + c0 + i) * a.R + row] = from_f32<YT>(__uint_as_float(v[i]) * al);
+                    for (int i = 0; i < 16; ++i, to += a.R)
+                        if (i < m) *to = from_f32<YT>(__uint_as_float(v[i]) * al);
                 }
             }
             if (!begins) {

@@ -96,6 +96,16 @@ __device__ __forceinline__ bool mbar_wait_warp(uint64_t* bar, uint32_t parity, i
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
+// A value that is the same in every lane, in a form that the compiler knows to be:
+// operands and branches made from such values stay in uniform registers and
+// warp-uniform control flow, without which every async-copy and tensor-core
+// instruction below costs some 80 cycles to issue.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+__device__ __forceinline__ int64_t uniform(int64_t v) {
+    return (int64_t)__shfl_sync(0xffffffffu, (long long)v, 0);
+}
+
 // global -> shared bulk copy, completion counted in bytes on `bar`.  Both
 // addresses 16-byte aligned, size a multiple of 16.
 __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes,

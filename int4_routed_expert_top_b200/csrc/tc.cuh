@@ -71,8 +71,7 @@ __device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, i
 
 // shared-memory descriptor of a K-major operand in the 128-byte swizzle layout:
 // rows of 64 fp16 (128 B), 8-row groups 1024 B apart
-__device__ __forceinline__ uint64_t smem_desc_sw128(const void* p) {
-    const uint64_t addr = smem_u32(p);
+__device__ __forceinline__ uint64_t smem_desc_sw128_at(uint32_t addr) {
     uint64_t d = 0;
     d |= (addr >> 4) & 0x3FFFull;            // start address
     d |= (uint64_t)1 << 16;                  // leading byte offset (unused for this layout)
@@ -81,5 +80,6 @@ __device__ __forceinline__ uint64_t smem_desc_sw128(const void* p) {
     d |= (uint64_t)2 << 61;                  // swizzle 128 B
     return d;
 }
+__device__ __forceinline__ uint64_t smem_desc_sw128(const void* p) { return smem_desc_sw128_at(smem_u32(p)); }
 
 }  // namespace coli
