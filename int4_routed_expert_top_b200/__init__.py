@@ -420,16 +420,21 @@ def coli_moe_forward_noalloc(layer, x, T, y, stream=None):
 # the sizes given, so that a wrong shape raises here instead of reading past a
 # buffer on the device.
 # ---------------------------------------------------------------------------
-_torch = None
+_torch = _INT32 = _FLOAT32 = _BFLOAT16 = _UINT8 = None
+
+
+def _load_torch():
+    global _torch, _INT32, _FLOAT32, _BFLOAT16, _UINT8
+    import torch
+    torch.cuda.init()
+    _INT32, _FLOAT32, _BFLOAT16, _UINT8 = torch.int32, torch.float32, torch.bfloat16, torch.uint8
+    _torch = torch
 
 
 def _device():
     """Index of the current CUDA device."""
-    global _torch
     if _torch is None:
-        import torch
-        _torch = torch
-        _torch.cuda.init()
+        _load_torch()
     return _torch._C._cuda_getDevice()
 
 
@@ -445,37 +450,25 @@ def _buf(name, a, dtype, count, dev):
     dev (None passes)."""
     if a is None:
         return None
-    if a.dtype is dtype and a.is_cuda and a.get_device() == dev and a.is_contiguous() and a.numel() >= count:
+    if a.dtype is dtype and a.get_device() == dev and a.is_contiguous() and a.numel() >= count:
         return a.data_ptr()
     if a.dtype != dtype:
         raise TypeError(f"{name}: {a.dtype}, expected {dtype}")
-    if not a.is_cuda or a.get_device() != dev:
+    if a.get_device() != dev:
         raise ValueError(f"{name}: on {a.device}, expected the current CUDA device {dev}")
     raise ValueError(f"{name}: {tuple(a.shape)} (contiguous: {a.is_contiguous()}), expected {count} contiguous elements")
 
 
-def _raw(name, a, count, dev):
-    return _buf(name, a, _torch.uint8, count, dev)
-
-
-def _i32(name, a, count, dev):
-    return _buf(name, a, _torch.int32, count, dev)
-
-
-def _f32(name, a, count, dev):
-    return _buf(name, a, _torch.float32, count, dev)
-
-
 def _code_of(dtype):
-    if dtype is _torch.bfloat16:
+    if dtype is _BFLOAT16:
         return COLI_BF16
-    if dtype is _torch.float32:
+    if dtype is _FLOAT32:
         return COLI_F32
     raise TypeError(f"rows must be float32 or bfloat16, got {dtype}")
 
 
 def _workspace(ws, dev):
-    return (None, 0) if ws is None else (_raw("ws", ws, 0, dev), ws.numel())
+    return (None, 0) if ws is None else (_buf("ws", ws, _UINT8, 0, dev), ws.numel())
 
 
 def coli_moe_sort_workspace_size(T: int, k: int, E: int) -> int:
@@ -488,30 +481,30 @@ def coli_moe_sort(idx, T, k, E, offsets, pair_tok, pair_slot, inv, ws, w=None, s
     """pair_tok and pair_slot may be None; ws: uint8 of coli_moe_sort_workspace_size bytes."""
     d, n = _device(), T * k
     p, size = _workspace(ws, d)
-    _ok(lib.coli_moe_sort(_i32("idx", idx, n, d), _f32("w", w, n, d), T, k, E,
-                          _i32("offsets", offsets, E + 1, d), _i32("pair_tok", pair_tok, n, d),
-                          _i32("pair_slot", pair_slot, n, d), _i32("inv", inv, n, d), p, size,
+    _ok(lib.coli_moe_sort(_buf("idx", idx, _INT32, n, d), _buf("w", w, _FLOAT32, n, d), T, k, E,
+                          _buf("offsets", offsets, _INT32, E + 1, d), _buf("pair_tok", pair_tok, _INT32, n, d),
+                          _buf("pair_slot", pair_slot, _INT32, n, d), _buf("inv", inv, _INT32, n, d), p, size,
                           _queue(stream, d)))
 
 
 def coli_moe_dispatch(x, T, H, k, inv, xs, stream=None):
     d = _device()
     _ok(lib.coli_moe_dispatch(_buf("x", x, x.dtype, T * H, d), _code_of(x.dtype), T, H, k,
-                              _i32("inv", inv, T * k, d), _buf("xs", xs, x.dtype, T * k * H, d),
+                              _buf("inv", inv, _INT32, T * k, d), _buf("xs", xs, x.dtype, T * k * H, d),
                               _queue(stream, d)))
 
 
 def coli_moe_dispatch_backward(dxs, T, H, k, inv, dx, stream=None):
     d = _device()
     _ok(lib.coli_moe_dispatch_backward(_buf("dxs", dxs, dxs.dtype, T * k * H, d),
-                                       _code_of(dxs.dtype), T, H, k, _i32("inv", inv, T * k, d),
+                                       _code_of(dxs.dtype), T, H, k, _buf("inv", inv, _INT32, T * k, d),
                                        _buf("dx", dx, dxs.dtype, T * H, d), _queue(stream, d)))
 
 
 def coli_moe_combine(o, T, H, k, inv, w, y, residual=None, stream=None):
     d = _device()
     _ok(lib.coli_moe_combine(_buf("o", o, o.dtype, T * k * H, d), _code_of(o.dtype), T, H, k,
-                             _i32("inv", inv, T * k, d), _f32("w", w, T * k, d),
+                             _buf("inv", inv, _INT32, T * k, d), _buf("w", w, _FLOAT32, T * k, d),
                              _buf("residual", residual, y.dtype, T * H, d),
                              _buf("y", y, y.dtype, T * H, d), _code_of(y.dtype),
                              _queue(stream, d)))
@@ -525,17 +518,17 @@ def coli_moe_combine_backward(dy, o, T, H, k, inv, w, d_o, dw, stream=None):
     d = _device()
     _ok(lib.coli_moe_combine_backward(_buf("dy", dy, dy.dtype, T * H, d), _code_of(dy.dtype),
                                       _buf("o", o, like.dtype, T * k * H, d),
-                                      _code_of(like.dtype), T, H, k, _i32("inv", inv, T * k, d),
-                                      _f32("w", w, T * k, d),
+                                      _code_of(like.dtype), T, H, k, _buf("inv", inv, _INT32, T * k, d),
+                                      _buf("w", w, _FLOAT32, T * k, d),
                                       _buf("d_o", d_o, like.dtype, T * k * H, d),
-                                      _f32("dw", dw, T * k, d), _queue(stream, d)))
+                                      _buf("dw", dw, _FLOAT32, T * k, d), _queue(stream, d)))
 
 
 def _norm_type(code):
     if code == COLI_F32:
-        return _torch.float32
+        return _FLOAT32
     if code == COLI_BF16:
-        return _torch.bfloat16
+        return _BFLOAT16
     raise ValueError(f"NormDesc: bad type {code}")
 
 
@@ -550,10 +543,10 @@ def coli_moe_block_norm(desc, x, o, T, x_out, n_out, gate=None, rstd_post=None, 
     d, n = _device(), T * desc.H
     xt, bt = _norm_type(desc.xt), _norm_type(desc.bt)
     _ok(lib.coli_moe_block_norm(desc, _buf("x", x, xt, n, d), _buf("o", o, bt, n, d),
-                                _f32("gate", gate, _gate_size(desc, T), d), T,
+                                _buf("gate", gate, _FLOAT32, _gate_size(desc, T), d), T,
                                 _buf("x_out", x_out, xt, n, d), _buf("n_out", n_out, bt, n, d),
-                                _f32("rstd_post", rstd_post, T, d),
-                                _f32("rstd_pre", rstd_pre, T, d), _queue(stream, d)))
+                                _buf("rstd_post", rstd_post, _FLOAT32, T, d),
+                                _buf("rstd_pre", rstd_pre, _FLOAT32, T, d), _queue(stream, d)))
 
 
 def coli_moe_block_norm_backward_workspace_size(desc, T: int) -> int:
@@ -569,11 +562,11 @@ def coli_moe_block_norm_backward(desc, x_out, o, T, dx_out, dn, dx, d_o, ws, gat
     xt, bt = _norm_type(desc.xt), _norm_type(desc.bt)
     p, size = _workspace(ws, d)
     _ok(lib.coli_moe_block_norm_backward(
-        desc, _buf("x_out", x_out, xt, n, d), _buf("o", o, bt, n, d), _f32("gate", gate, ng, d), T,
-        _f32("rstd_post", rstd_post, T, d), _f32("rstd_pre", rstd_pre, T, d),
+        desc, _buf("x_out", x_out, xt, n, d), _buf("o", o, bt, n, d), _buf("gate", gate, _FLOAT32, ng, d), T,
+        _buf("rstd_post", rstd_post, _FLOAT32, T, d), _buf("rstd_pre", rstd_pre, _FLOAT32, T, d),
         _buf("dx_out", dx_out, xt, n, d), _buf("dn", dn, bt, n, d), _buf("dx", dx, xt, n, d),
-        _buf("d_o", d_o, bt, n, d), _f32("dpost_gain", dpost_gain, desc.H, d),
-        _f32("dgate", dgate, ng, d), _f32("dpre_gain", dpre_gain, desc.H, d), p, size,
+        _buf("d_o", d_o, bt, n, d), _buf("dpost_gain", dpost_gain, _FLOAT32, desc.H, d),
+        _buf("dgate", dgate, _FLOAT32, ng, d), _buf("dpre_gain", dpre_gain, _FLOAT32, desc.H, d), p, size,
         _queue(stream, d)))
 
 
@@ -598,9 +591,9 @@ def coli_moe_fp4_quantize(fmt, x, rows, K, codes, scales, act=COLI_ACT_NONE, src
     nc, ns = _fp4_sizes(fmt, rows, K)
     n_src = x.numel() // max(1, 2 * K if act == COLI_ACT_SWIGLU else K)
     _ok(lib.coli_moe_fp4_quantize(fmt, _buf("x", x, x.dtype, 0, d), _code_of(x.dtype), n_src, rows,
-                                  K, act, _i32("src", src, rows, d), _i32("count", count, 1, d),
-                                  _f32("gscale", gscale, 1, d), _raw("codes", codes, nc, d),
-                                  _raw("scales", scales, ns, d),
+                                  K, act, _buf("src", src, _INT32, rows, d), _buf("count", count, _INT32, 1, d),
+                                  _buf("gscale", gscale, _FLOAT32, 1, d), _buf("codes", codes, _UINT8, nc, d),
+                                  _buf("scales", scales, _UINT8, ns, d),
                                   _buf("values", values, x.dtype, rows * K, d),
                                   _queue(stream, d)))
 
@@ -617,11 +610,11 @@ def coli_moe_fp4_product(fmt, x_codes, x_scales, P, K, w_codes, w_scales, E, R, 
     xc, xs = _fp4_sizes(fmt, P, K)
     wc, wsc = _fp4_sizes(fmt, E * R, K)
     p, n = _workspace(ws, d)
-    _ok(lib.coli_moe_fp4_product(fmt, _raw("x_codes", x_codes, xc, d),
-                                 _raw("x_scales", x_scales, xs, d), P, K,
-                                 _raw("w_codes", w_codes, wc, d),
-                                 _raw("w_scales", w_scales, wsc, d), E, R,
-                                 _i32("offsets", offsets, E + 1, d), _f32("alpha", alpha, E, d),
+    _ok(lib.coli_moe_fp4_product(fmt, _buf("x_codes", x_codes, _UINT8, xc, d),
+                                 _buf("x_scales", x_scales, _UINT8, xs, d), P, K,
+                                 _buf("w_codes", w_codes, _UINT8, wc, d),
+                                 _buf("w_scales", w_scales, _UINT8, wsc, d), E, R,
+                                 _buf("offsets", offsets, _INT32, E + 1, d), _buf("alpha", alpha, _FLOAT32, E, d),
                                  _buf("y", y, y.dtype, P * R, d), _code_of(y.dtype), p, n,
                                  _queue(stream, d)))
 
@@ -629,6 +622,6 @@ def coli_moe_fp4_product(fmt, x_codes, x_scales, P, K, w_codes, w_scales, E, R, 
 def coli_moe_fp4_product_status(ws, stream=None) -> int:
     """Error flags of the last product that used ws (raises on a timeout)."""
     flags, d = _I32(0), _device()
-    _ok(lib.coli_moe_fp4_product_status(_raw("ws", ws, 4, d), ctypes.byref(flags),
+    _ok(lib.coli_moe_fp4_product_status(_buf("ws", ws, _UINT8, 4, d), ctypes.byref(flags),
                                         _queue(stream, d)))
     return flags.value

@@ -144,23 +144,58 @@ struct NormForward {
     }
 };
 
-// CTAs of the backward pass: two per SM, so that one's loads cover the other's
-// sums over the row; clusters of four leave 74 partial rows
-constexpr int kNormBackwardCtas = 296;
-constexpr int kNormCluster = 4;
+// The backward pass: with many tokens, CTAs whose rows come through a ring (their
+// sums over tokens fill the registers: 8192 columns at 512 threads); else two CTAs
+// per SM, so that one's loads cover the other's sums over the row.  Clusters of two add the sums over tokens before they leave an SM
+// (clusters of four leave SMs without a CTA where a GPC's number of them is no
+// multiple of four: the ring's 37 did not fit at once and took twice as long).
+constexpr int kNormSms = 148, kNormCtas = 2 * kNormSms;
+constexpr int kNormRingMaxH = 8192;
+constexpr int kNormRingBytes = 224 * 1024;   // of an SM
+constexpr int kNormCluster = 2;
 int norm_backward_cluster(int grid) { return grid >= kNormCluster ? kNormCluster : 1; }
-int norm_backward_grid(int T) {
-    const int grid = std::min(T, kNormBackwardCtas);
+int norm_backward_grid(int T, int ctas) {
+    const int grid = std::min(T, ctas);
     return grid / norm_backward_cluster(grid) * norm_backward_cluster(grid);
 }
+// CTAs of the ring form: as many per SM as have two stages with every input, at
+// most six, and two rows or more for each; 0 where that leaves none
+int norm_ring_ctas(const coli_norm_desc& d, int T) {
+    const int need = 3 * d.H * 4 + 2 * 2 * d.H * (type_size(d.xt) + type_size(d.bt));
+    const int per_sm = std::min({6, kNormRingBytes / need, T / (2 * kNormSms)});
+    return d.H <= kNormRingMaxH && d.H % 8 == 0 ? per_sm * kNormSms : 0;
+}
 
-template <typename XT, typename BT, int V, int N>
+// the ring of a call: no stages where it does not apply
+NormRing norm_ring(const coli_norm_desc& d, int ctas, bool wide, bool x_out, bool dx_out, bool o, bool dn) {
+    NormRing r = {0, 0, {-1, -1, -1, -1}, {-1, -1, -1}, 0};
+    if (!wide || ctas < 1) return r;
+    const bool vec[3] = {dn && d.pre_gain, o && d.post_norm && d.post_gain, o && d.gate_kind == COLI_GATE_CHANNEL};
+    for (int i = 0; i < 3; ++i) {
+        if (!vec[i]) continue;
+        r.gain[i] = r.first;
+        r.first += d.H * 4;
+    }
+    const bool has[4] = {x_out, dx_out, o, dn};
+    for (int i = 0; i < 4; ++i) {
+        if (!has[i]) continue;
+        r.off[i] = r.stage;
+        r.stage += d.H * type_size(i < 2 ? d.xt : d.bt);
+    }
+    r.stages = std::min(kNormMaxStages, (kNormRingBytes / (ctas / kNormSms) - 1024 - r.first) / r.stage);
+    // room for the sums at the end as well
+    if (r.stages < 2 || kNormSums * d.H * 4 > r.first + r.stages * r.stage) r.stages = 0;
+    return r;
+}
+
+template <typename XT, typename BT, int V, int N, bool RING>
 struct NormBackward {
-    static int launch(const NormShape& s, const NormArgs& a, const NormSums& keep, const void* x_out, const void* o,
-                      const float* rstd_post, const float* rstd_pre, const void* dx_out, const void* dn,
-                      void* dx, void* d_o, float* dgate, float* partial, int grid, cudaStream_t st) {
-        const auto kern = block_norm_backward_kernel<XT, BT, V, N>;
-        const int smem = keep.n * a.H * 4;
+    static int launch(const NormShape& s, const NormArgs& a, const NormSums& keep, const NormRing& ring,
+                      const void* x_out, const void* o, const float* rstd_post, const float* rstd_pre,
+                      const void* dx_out, const void* dn, void* dx, void* d_o, float* dgate, float* partial, int grid,
+                      cudaStream_t st) {
+        const auto kern = block_norm_backward_kernel<XT, BT, V, N, RING>;
+        const int smem = RING ? ring.first + ring.stages * ring.stage : keep.n * a.H * 4;
         int rc = set_smem((const void*)kern, smem);
         if (rc) return rc;
         cudaLaunchConfig_t cfg = {};
@@ -176,12 +211,27 @@ struct NormBackward {
         attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
         cfg.attrs = attr;
         cfg.numAttrs = 2;
-        const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, keep, (const XT*)x_out, (const BT*)o, rstd_post, rstd_pre,
-                                                 (const XT*)dx_out, (const BT*)dn, (XT*)dx, (BT*)d_o, dgate, partial);
+        const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, keep, ring, (const XT*)x_out, (const BT*)o, rstd_post,
+                                                 rstd_pre, (const XT*)dx_out, (const BT*)dn, (XT*)dx, (BT*)d_o, dgate,
+                                                 partial);
         if (e != cudaSuccess) return fail(COLI_E_CUDA, "block norm backward: %s", cudaGetErrorString(e));
         return check_launch("block norm backward");
     }
 };
+template <typename XT, typename BT, int V, int N> using NormBackwardPlain = NormBackward<XT, BT, V, N, false>;
+
+// ring rows: one or two vectors of eight per thread
+template <typename XT, typename BT, typename... A>
+int norm_ring_launch(const NormShape& s, A... args) {
+    if (s.N == 1) return NormBackward<XT, BT, 8, 1, true>::launch(s, args...);
+    return NormBackward<XT, BT, 8, 2, true>::launch(s, args...);
+}
+template <typename... A>
+int norm_ring_dispatch(const coli_norm_desc& d, const NormShape& s, A... args) {
+    if (d.bt == COLI_F32) return norm_ring_launch<float, float>(s, args...);
+    if (d.xt == COLI_F32) return norm_ring_launch<float, __nv_bfloat16>(s, args...);
+    return norm_ring_launch<__nv_bfloat16, __nv_bfloat16>(s, args...);
+}
 
 }  // namespace
 
@@ -298,7 +348,7 @@ int coli_moe_block_norm_backward_workspace_size(const coli_norm_desc* desc, int3
     int rc = norm_ok("block_norm_backward_workspace_size", desc, T);
     if (rc) return rc;
     if (!bytes) return fail(COLI_E_INVAL, "block_norm_backward_workspace_size: NULL pointer");
-    const int grid = norm_backward_grid(T);
+    const int grid = norm_backward_grid(T, std::max(kNormCtas, norm_ring_ctas(*desc, T)));  // of either form
     *bytes = (size_t)(grid / norm_backward_cluster(grid)) * kNormSums * desc->H * 4;
     return COLI_OK;
 }
@@ -330,16 +380,29 @@ int coli_moe_block_norm_backward(const coli_norm_desc* desc, const void* x_out, 
     if (keep.n && (!ws || ws_bytes < need || !aligned(ws, 16)))
         return fail(COLI_E_WORKSPACE, "block_norm_backward: workspace of %zu bytes, %zu needed", ws ? ws_bytes : 0,
                     need);
-    const int grid = norm_backward_grid(T);
     float* partial = static_cast<float*>(ws);
+    int grid = 0;
     if (T > 0) {
         const int xa = 8 * type_size(desc->xt), ba = 8 * type_size(desc->bt);
         const bool wide = desc->H % 8 == 0 && aligned(x_out, xa) && aligned(dx_out, xa) && aligned(dx, xa) &&
                           aligned(o, ba) && aligned(dn, ba) && aligned(d_o, ba) && aligned(desc->post_gain, 32) &&
                           aligned(desc->pre_gain, 32) && aligned(gate, 32) && aligned(dgate, 32);
         const NormArgs a = norm_args(*desc, gate, T);
-        rc = norm_dispatch<NormBackward>(*desc, norm_shape(desc->H, T, wide, true), a, keep, x_out, o, rstd_post,
-                                         rstd_pre, dx_out, dn, dx, d_o, dgate, partial, grid, S(stream));
+        const int ctas = norm_ring_ctas(*desc, T);
+        const NormRing ring = norm_ring(*desc, ctas, wide, dn != nullptr, dx_out != nullptr, o != nullptr, dn != nullptr);
+        grid = norm_backward_grid(T, ring.stages > 0 ? ctas : kNormCtas);
+        if (ring.stages > 0) {
+            NormShape s;
+            s.V = 8;
+            s.N = desc->H / 8 <= 768 ? 1 : 2;  // more warps hide more of each other's waits
+            s.threads = ((desc->H / 8 + s.N - 1) / s.N + 31) / 32 * 32;
+            rc = norm_ring_dispatch(*desc, s, a, keep, ring, x_out, o, rstd_post, rstd_pre, dx_out, dn, dx, d_o, dgate,
+                                    partial, grid, S(stream));
+        } else {
+            rc = norm_dispatch<NormBackwardPlain>(*desc, norm_shape(desc->H, T, wide, true), a, keep, ring, x_out, o,
+                                                  rstd_post, rstd_pre, dx_out, dn, dx, d_o, dgate, partial, grid,
+                                                  S(stream));
+        }
         if (rc) return rc;
     }
     if (!keep.n) return COLI_OK;

@@ -191,13 +191,13 @@ def check_backward(c, dxo=True, dn=True):
 
 @pytest.mark.parametrize("xt,bt", TYPES)
 @pytest.mark.parametrize("gate", list(KIND))
-@pytest.mark.parametrize("T,H", SHAPES + [(1000, 64)])
+@pytest.mark.parametrize("T,H", SHAPES + [(1000, 64), (296, 8), (301, 2048), (2000, 1024), (450, 6144), (297, 8192)])
 def test_backward(T, H, gate, xt, bt):
     for post, gains in ((True, True), (False, False)):
         check_backward(Case(T, H, xt, bt, gate, post, gains))
 
 
-@pytest.mark.parametrize("T,H", [(5, 96), (2, 6144)])
+@pytest.mark.parametrize("T,H", [(5, 96), (2, 6144), (400, 1024)])
 def test_backward_with_one_gradient(T, H):
     for gate, (dxo, dn) in itertools.product(("none", "token"), ((True, False), (False, True))):
         check_backward(Case(T, H, F, B, gate), dxo, dn)
