@@ -107,18 +107,19 @@ int coli_moe_fp4_quantize(coli_fp4 fmt, const void* x, coli_dtype xt, int64_t n_
     a.src = src; a.count = count; a.gscale = gscale;
     a.codes = static_cast<uint8_t*>(codes);
     a.scales = static_cast<uint32_t*>(scales);
-    // warps per row: a power of two, as many as have a chunk of columns
+    // a warp per chunk of a row, several rows where they are short
     const int chunks = (K + kQuantCols - 1) / kQuantCols;
-    int rows_per = 8;
-    while (rows_per > 1 && 8 / rows_per < chunks) rows_per /= 2;
-    const int warps = 8 / rows_per;
-    const dim3 grid((unsigned)((rows + rows_per - 1) / rows_per), (chunks + warps - 1) / warps);
+    const int parts = (chunks + kQuantWarps - 1) / kQuantWarps, warps = (chunks + parts - 1) / parts;
+    const int rows_per = std::max(1, 8 / warps);
+    const dim3 grid((unsigned)((rows + rows_per - 1) / rows_per), parts);
+    const int threads = 32 * warps * rows_per;
     if (xt == COLI_F32)
         return launch_pdl(fmt == COLI_NVFP4 ? fp4_quantize_kernel<float, true> : fp4_quantize_kernel<float, false>, grid,
-                          256, 0, S(stream), "fp4 quantize", a, rows_per, (const float*)x, (float*)values);
+                          threads, 0, S(stream), "fp4 quantize", a, warps, rows_per, (const float*)x, (float*)values);
     return launch_pdl(fmt == COLI_NVFP4 ? fp4_quantize_kernel<__nv_bfloat16, true>
                                         : fp4_quantize_kernel<__nv_bfloat16, false>,
-                      grid, 256, 0, S(stream), "fp4 quantize", a, rows_per, (const __nv_bfloat16*)x, (__nv_bfloat16*)values);
+                      grid, threads, 0, S(stream), "fp4 quantize", a, warps, rows_per, (const __nv_bfloat16*)x,
+                      (__nv_bfloat16*)values);
 }
 
 int coli_moe_fp4_product_workspace_size(coli_fp4 fmt, int64_t P, int32_t K, int32_t E, int32_t R, size_t* bytes) {

@@ -77,20 +77,27 @@ __device__ __forceinline__ uint32_t e2m1x8(const float* v) {
     return r;
 }
 
+// the largest magnitude of three, NaN if one is
+__device__ __forceinline__ float max3_abs(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // A lane holds 16 columns of a row (two or four loads of 16 or 32 bytes), a warp
 // 512: a block is one lane (NVFP4) or two, so its maximum takes at most one
-// shuffle.  A CTA's 8 warps share out `rows_per` rows, 8 / rows_per warps each;
-// one chunk of a row per warp, since many small CTAs hide the loads better than
-// a warp's loop over its row does.  Bound by HBM (x once, codes, scales and
+// shuffle.  Every warp of a CTA has one chunk of one of its rows: that hides the
+// loads better than a warp's loop over its row does.  Bound by HBM (x once, codes, scales and
 // values once).
 constexpr int kQuantCols = 512;
+constexpr int kQuantWarps = 16;  // of a CTA, at most
 
 template <typename T, bool NV>
-__global__ void __launch_bounds__(256)
-fp4_quantize_kernel(Fp4QuantArgs a, int rows_per, const T* __restrict__ x, T* __restrict__ values) {
-    const int warps = 8 / rows_per, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t r = (int64_t)blockIdx.x * rows_per + warp / warps;
-    const int c0 = ((int)blockIdx.y * warps + (warp & (warps - 1))) * kQuantCols;
+__global__ void __launch_bounds__(32 * kQuantWarps)
+fp4_quantize_kernel(Fp4QuantArgs a, int warps, int rows_per, const T* __restrict__ x, T* __restrict__ values) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mine = warp / warps;
+    const int64_t r = (int64_t)blockIdx.x * rows_per + mine;
+    const int c0 = ((int)blockIdx.y * warps + warp - mine * warps) * kQuantCols;
     const int c = c0 + lane * 16;
     pdl_trigger();
     pdl_wait();
@@ -115,10 +122,11 @@ fp4_quantize_kernel(Fp4QuantArgs a, int rows_per, const T* __restrict__ x, T* __
             }
         }
     }
-    // the largest magnitude as bits: infinities and NaN come out on top
-    uint32_t m = 0;
+    // the largest magnitude; infinities and NaN come out on top, as bits too
+    float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) m = max(m, __float_as_uint(v[i]) & 0x7fffffffu);
+    for (int i = 0; i < 16; i += 2) top = max3_abs(top, v[i], v[i + 1]);
+    uint32_t m = __float_as_uint(top);
     if (!NV) m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
     const bool bad = m >= 0x7f800000u;
     uint32_t byte;
@@ -136,7 +144,10 @@ fp4_quantize_kernel(Fp4QuantArgs a, int rows_per, const T* __restrict__ x, T* __
         r_d = __uint_as_float((uint32_t)(254 - b) << 23);
     }
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = __fmul_rn(v[i], r_d);
+    for (int i = 0; i < 16; i += 2) {
+        const float2 q = f2unpack(f2mul(f2pack(v[i], v[i + 1]), f2pack(r_d, r_d)));
+        v[i] = q.x; v[i + 1] = q.y;
+    }
     uint32_t code[2] = {e2m1x8(v), e2m1x8(v + 8)};
     if (bad || (NV && !(d > 0.0f))) code[0] = code[1] = 0;
     // four blocks' bytes make a word: a block is 1 (NV) or 2 lanes
