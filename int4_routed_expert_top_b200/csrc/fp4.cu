@@ -31,10 +31,10 @@ int sm_count() {
     return sms;
 }
 
-// Rows of an expert per tile: 32 streams the weights with the deepest ring, 192
-// makes the most of each weight byte.
-constexpr int kFpSmallNT = 32, kFpLargeNT = 192;
-int tile_rows(int64_t P, int E) { return P > (int64_t)48 * E ? kFpLargeNT : kFpSmallNT; }
+// Rows of an expert per tile: 32 streams the weights with the deepest ring, 224 (a
+// pair of CTAs) makes the most of each byte in shared memory.
+constexpr int kFpSmallNT = 32, kFpLargeNT = 224;
+bool pairs_apply(int64_t P, int E) { return P > (int64_t)48 * E; }
 
 // bytes [rows][K/2], boxes of 128 bytes x box_rows, 128-byte swizzle
 int encode_codes_map(CUtensorMap* m, const void* base, int64_t rows, int K, int box_rows) {
@@ -51,26 +51,41 @@ int encode_codes_map(CUtensorMap* m, const void* base, int64_t rows, int K, int 
     return COLI_OK;
 }
 
-template <int NT, bool NV, typename YT>
+template <int NT, bool NV, bool PAIR, typename YT>
 int launch_product(const FpArgs& a, const void* x_codes, const void* w_codes, void* y, cudaStream_t st) {
-    using C = FpShape<NT, NV>;
+    using C = FpShape<NT, NV, PAIR>;
+    const auto kern = fp4_product_kernel<NT, NV, PAIR, YT>;
     CUtensorMap wmap, xmap;
     int rc;
     if ((rc = encode_codes_map(&wmap, w_codes, (int64_t)a.E * a.R, a.K, 128))) return rc;
     if ((rc = encode_codes_map(&xmap, x_codes, a.P, a.K, C::box))) return rc;
-    if ((rc = set_smem((const void*)fp4_product_kernel<NT, NV, YT>, C::smem))) return rc;
-    return launch_pdl(fp4_product_kernel<NT, NV, YT>, dim3(std::min(sm_count(), kFpMaxGrid)), kFpThreads, C::smem, st,
-                      "fp4 product", wmap, xmap, a, (YT*)y);
+    if ((rc = set_smem((const void*)kern, C::smem))) return rc;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(std::min(sm_count(), kFpMaxGrid) / C::ctas * C::ctas);
+    cfg.blockDim = dim3(kFpThreads);
+    cfg.dynamicSmemBytes = C::smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = C::ctas;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = PAIR ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, wmap, xmap, a, (YT*)y);
+    if (e != cudaSuccess) return fail(COLI_E_CUDA, "fp4 product: %s", cudaGetErrorString(e));
+    return check_launch("fp4 product");
 }
 
-template <int NT>
+template <int NT, bool PAIR>
 int launch_product_t(coli_fp4 fmt, coli_dtype yt, const FpArgs& a, const void* x_codes, const void* w_codes, void* y,
                      cudaStream_t st) {
     if (fmt == COLI_NVFP4)
-        return yt == COLI_F32 ? launch_product<NT, true, float>(a, x_codes, w_codes, y, st)
-                              : launch_product<NT, true, __nv_bfloat16>(a, x_codes, w_codes, y, st);
-    return yt == COLI_F32 ? launch_product<NT, false, float>(a, x_codes, w_codes, y, st)
-                          : launch_product<NT, false, __nv_bfloat16>(a, x_codes, w_codes, y, st);
+        return yt == COLI_F32 ? launch_product<NT, true, PAIR, float>(a, x_codes, w_codes, y, st)
+                              : launch_product<NT, true, PAIR, __nv_bfloat16>(a, x_codes, w_codes, y, st);
+    return yt == COLI_F32 ? launch_product<NT, false, PAIR, float>(a, x_codes, w_codes, y, st)
+                          : launch_product<NT, false, PAIR, __nv_bfloat16>(a, x_codes, w_codes, y, st);
 }
 
 }  // namespace
@@ -128,7 +143,7 @@ int coli_moe_fp4_product_workspace_size(coli_fp4 fmt, int64_t P, int32_t K, int3
     if (!bytes) return fail(COLI_E_INVAL, "fp4_product_workspace_size: NULL pointer");
     if (E < 1 || E > kFpMaxE || R < 1 || (E > 1 && R % 128) || (int64_t)E * R > INT32_MAX)
         return fail(COLI_E_INVAL, "fp4_product: bad sizes E=%d R=%d", E, R);
-    *bytes = kFpHeadBytes + (size_t)kFpMaxGrid * 128 * tile_rows(P, E) * 4;
+    *bytes = kFpHeadBytes + (size_t)kFpMaxGrid * 128 * (pairs_apply(P, E) ? kFpLargeNT : kFpSmallNT) * 4;
     return COLI_OK;
 }
 
@@ -157,9 +172,8 @@ int coli_moe_fp4_product(coli_fp4 fmt, const void* x_codes, const void* x_scales
     a.err = static_cast<int32_t*>(ws);
     a.flags = reinterpret_cast<uint64_t*>(static_cast<char*>(ws) + kFpFlagBytes);
     a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kFpHeadBytes);
-    if (tile_rows(P, E) == kFpLargeNT)
-        return launch_product_t<kFpLargeNT>(fmt, yt, a, x_codes, w_codes, y, S(stream));
-    return launch_product_t<kFpSmallNT>(fmt, yt, a, x_codes, w_codes, y, S(stream));
+    if (pairs_apply(P, E)) return launch_product_t<kFpLargeNT, true>(fmt, yt, a, x_codes, w_codes, y, S(stream));
+    return launch_product_t<kFpSmallNT, false>(fmt, yt, a, x_codes, w_codes, y, S(stream));
 }
 
 int coli_moe_fp4_product_status(const void* ws, int32_t* flags, coli_stream_t stream) {

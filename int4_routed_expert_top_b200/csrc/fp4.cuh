@@ -29,6 +29,13 @@
 // shuffle or a vote costs the issuing warps some 300 cycles a stage (the tile
 // loop took 1.6 to 2.5 times as long).
 //
+// At few rows per expert a CTA works by itself on 128 weight rows and up to 32 of
+// the expert's.  At many, two CTAs of a cluster share a tile of 256 weight rows and
+// up to 224 rows (tcgen05 cta_group::2): each holds 128 of the weight rows and half
+// of the others in its shared memory and the accumulators of its weight rows, and
+// CTA 0 issues the products for both.  A stage is then 33 KB per SM instead of the
+// 43 KB of a 128 x 192 tile for 1.17 times the work: PAIR_TIME.
+//
 // CTA roles: warp 0 copies (codes by 2-D TMA with the 128-byte swizzle, the
 // weights' scales by bulk copy), four warps bring the rows' scales (rows of an
 // expert start anywhere, a scale tile only at multiples of 128, so those are
@@ -192,23 +199,30 @@ constexpr int kFpHeadBytes = kFpFlagBytes + kFpMaxGrid * 4 * 8;
 // a raised flag: a value that unset memory does not hold (0 after every call)
 constexpr uint64_t kFpRaised = 0x9d3ac1f5e8276b41ull;
 
-template <int NT, bool NV>
+// NT: rows of a tile at most; PAIR: two CTAs to a tile, M = 256 weight rows
+template <int NT, bool NV, bool PAIR>
 struct FpShape {
-    static constexpr int box = NT < 64 ? NT : 64;            // rows per TMA box of X
+    static constexpr int M = PAIR ? 256 : 128;
+    static constexpr int ctas = PAIR ? 2 : 1;
+    static constexpr int rows = NT / ctas;                   // of X in a CTA's shared memory
+    static constexpr int box = PAIR ? rows / 2 : rows;       // rows per TMA box of X
+    static constexpr int step = 16 * ctas;                   // N is a multiple of it
     static constexpr int atoms = NV ? 4 : 2;                 // 512-byte scale tiles per 256 columns
     static constexpr int nb = (NT + 127) / 128;              // of the rows, per atom
     static constexpr int a_bytes = 128 * 128;
-    static constexpr int b_bytes = NT * 128;
+    static constexpr int b_bytes = rows * 128;
     static constexpr int sfa_bytes = atoms * 512;
     static constexpr int sfb_bytes = atoms * nb * 512;
     static constexpr int stage = (a_bytes + b_bytes + sfa_bytes + sfb_bytes + 1023) / 1024 * 1024;
-    static constexpr int stages = 196608 / stage;
+    static constexpr int stages = 200 * 1024 / stage;
     static constexpr int smem = stages * stage + 1024;
     static constexpr int sf_cols = atoms * 4 * (1 + nb);     // TMEM columns of one stage's scales
     static constexpr int sf0 = 2 * NT;                       // after two accumulators
-    static constexpr int cols_used = sf0 + 2 * sf_cols;
+    static constexpr int sf_sets = sf0 + 2 * sf_cols <= 512 ? 2 : 1;
+    static constexpr int cols_used = sf0 + sf_sets * sf_cols;
     static constexpr int cols = cols_used <= 128 ? 128 : cols_used <= 256 ? 256 : 512;
-    static_assert(NT % box == 0 && NT % 16 == 0 && cols_used <= 512, "TMEM holds 512 columns");
+    static_assert(NT % step == 0 && NT % 32 == 0 && rows % box == 0 && box % 8 == 0, "whole swizzle atoms");
+    static_assert(cols_used <= 512, "TMEM holds 512 columns");
 };
 
 struct FpArgs {
@@ -233,10 +247,10 @@ struct FpPlan {
 
 // Each thread takes four experts; offsets are clamped so that no value of them
 // leads out of the buffers.
-template <int NT>
+template <int NT, int M>
 __device__ __forceinline__ void fp_plan(const FpArgs& a, FpPlan& p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int RT = (a.R + 127) / 128;
+    const int RT = (a.R + M - 1) / M;
     if (!a.offsets) {
         if (threadIdx.x == 0) {
             p.begin[0] = 0;
@@ -285,7 +299,7 @@ __device__ __forceinline__ void fp_plan(const FpArgs& a, FpPlan& p) {
 // [lo(c), lo(c + 1)) of the tiles from tile0 on.
 struct FpRun {
     int64_t G, waves, tile0, U;
-    __device__ __forceinline__ FpRun(const FpArgs& a, const FpPlan& p, int grid) {
+    __device__ __forceinline__ FpRun(const FpArgs& a, const FpPlan& p, int grid) {  // grid: CTAs, or pairs
         const int64_t tiles = p.tile0[a.E];
         G = min((int64_t)grid, max((int64_t)1, tiles * a.KS / kFpMinUnits));
         waves = tiles / G;
@@ -365,35 +379,40 @@ __device__ __forceinline__ uint64_t smem_desc_scales(uint32_t addr) {
 }
 
 // 32 rows x 16 bytes of shared memory to 32 lanes x 4 columns of TMEM, repeated
-// in the four lane quarters
+// in the four lane quarters (in both CTAs of a pair, each from its own)
+template <bool PAIR>
 __device__ __forceinline__ void tc_copy_scales_elect(uint32_t dst, uint64_t desc) {
-    asm volatile(
-        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-        " @e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}" ::"r"(dst), "l"(desc) : "memory");
+    if (PAIR)
+        asm volatile(
+            "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+            " @e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n}" ::"r"(dst), "l"(desc) : "memory");
+    else
+        asm volatile(
+            "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+            " @e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}" ::"r"(dst), "l"(desc) : "memory");
 }
 
 // instruction descriptor of a block-scaled product of E2M1 operands, both
-// K-major, M = 128: types 1 (E2M1), N / 8, scale type (1 E8M0, 0 E4M3), M / 128;
+// K-major: types 1 (E2M1), N / 8, scale type (1 E8M0, 0 E4M3), M / 128;
 // the bytes of a scale word that apply are added per product
-template <bool NV>
+template <bool NV, int M>
 __device__ __forceinline__ constexpr uint32_t idesc_fp4(int n) {
-    return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((NV ? 0u : 1u) << 23) | (1u << 27);
+    return (1u << 7) | (1u << 10) | ((uint32_t)(n >> 3) << 17) | ((NV ? 0u : 1u) << 23) | ((uint32_t)(M >> 7) << 27);
 }
 
-template <bool NV>
+#define COLI_MMA_FP4(GROUP, KIND)                                                                              \
+    asm volatile("{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"             \
+                 " @e tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%5], [%6], p;\n}"    \
+                 ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb))
+template <bool NV, bool PAIR>
 __device__ __forceinline__ void tc_mma_fp4_elect(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                                  uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
-    if (NV)
-        asm volatile(
-            "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-            " @e tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%5], [%6], p;\n}"
-            ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb));
-    else
-        asm volatile(
-            "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-            " @e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%5], [%6], p;\n}"
-            ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb));
+    if constexpr (PAIR && NV) COLI_MMA_FP4("2", "mxf4nvf4.block_scale.scale_vec::4X");
+    else if constexpr (PAIR) COLI_MMA_FP4("2", "mxf4.block_scale.scale_vec::2X");
+    else if constexpr (NV) COLI_MMA_FP4("1", "mxf4nvf4.block_scale.scale_vec::4X");
+    else COLI_MMA_FP4("1", "mxf4.block_scale.scale_vec::2X");
 }
+#undef COLI_MMA_FP4
 
 // A role's place in the ring: slot, the phase of its barriers, and whether the
 // slot has been used before.
@@ -429,40 +448,49 @@ __device__ __forceinline__ bool fp_wait_flag(const uint64_t* flag, int32_t* err)
     return __shfl_sync(0xffffffffu, ok, 0) != 0;
 }
 
-template <int NT, bool NV, typename YT>
+template <int NT, bool NV, bool PAIR, typename YT>
 __global__ void __launch_bounds__(kFpThreads, 1)
 fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                    FpArgs a, YT* y) {
-    using C = FpShape<NT, NV>;
+    using C = FpShape<NT, NV, PAIR>;
     extern __shared__ uint8_t fp_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(fp_raw) + 1023) & ~uintptr_t(1023));
     __shared__ FpPlan plan;
     __shared__ __align__(8) uint64_t full[C::stages], empty[C::stages], accfull[2], accempty[2];
+    __shared__ __align__(8) uint64_t peer[C::stages];   // of CTA 0 of a pair: CTA 1's stage is full
     __shared__ uint32_t tmem_slot;
     const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
-    if (warp == 0) tmem_alloc(&tmem_slot, C::cols);
+    // of the pair's work, this CTA's part
+    const int rank = PAIR ? (int)cluster_rank() : 0, unit = (int)blockIdx.x / C::ctas;
+
+    if (warp == 0) {
+        if (PAIR) tmem_alloc_pair(&tmem_slot, C::cols);
+        else tmem_alloc(&tmem_slot, C::cols);
+    }
     if (threadIdx.x == 32) {
         for (int s = 0; s < C::stages; ++s) {
+            mbar_init(&peer[s], 1);
             mbar_init(&full[s], 1 + kFpScaleWarps);  // the copies' announcement, the scale warps
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&accfull[b], 1);
-            mbar_init(&accempty[b], 4);
+            mbar_init(&accempty[b], 4 * C::ctas);
         }
         fence_mbar_init();
     }
     pdl_trigger();
     pdl_wait();
     if (blockIdx.x == 0 && threadIdx.x == 64) *a.err = 0;
-    fp_plan<NT>(a, plan);
+    fp_plan<NT, C::M>(a, plan);
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();  // the other CTA's barriers are set up
     tc_fence_after();
     const uint32_t tmem = uniform(tmem_slot);
-    const FpRun run(a, plan, gridDim.x);
-    FpPieces q(a, run, blockIdx.x);
+    const FpRun run(a, plan, gridDim.x / C::ctas);
+    FpPieces q(a, run, unit);
     bool ok = true;  // cleared by a wait that gave up: then no further waits
 
     if (warp == 0) {
@@ -470,10 +498,17 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         Ring ring;
         while (uniform((int)q.next())) {
             const FpTile t = fp_tile<NT>(plan, a.E, q.tile);
-            const int wrow = uniform(t.e * a.R + t.rt * 128), p0 = uniform((int)t.p0);
-            const int boxes = uniform((t.n + C::box - 1) / C::box);
+            // this CTA's share of the rows: half of N, itself a multiple of 16
+            const int half = (t.n + C::step - 1) / C::step * 16;
+            const int first = PAIR ? rank * half : 0, count = min(half, t.n - first);
+            const int p0 = uniform((int)t.p0 + first);
+            const int boxes = uniform(PAIR ? max(0, (count + C::box - 1) / C::box) : 1);
+            const int wrow = uniform(t.e * a.R + t.rt * C::M + rank * 128);
             const int k0 = uniform(q.k0), k1 = uniform(q.k1);
-            const uint8_t* sfa = a.ws + ((int64_t)(wrow >> 7) * a.wwords + k0 * C::atoms) * 512;
+            // past the expert's last weight row (the second half of a tile may be) the products are
+            // not stored: any scales do
+            const int block = uniform(t.rt * C::M + rank * 128 < a.R ? wrow >> 7 : (wrow >> 7) - 1);
+            const uint8_t* sfa = a.ws + ((int64_t)block * a.wwords + k0 * C::atoms) * 512;
             const uint32_t bytes = (uint32_t)(C::a_bytes + boxes * C::box * 128);
 #pragma unroll 1
             for (int k = k0; k < k1; ++k) {
@@ -484,7 +519,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 mbar_expect_tx_elect(bar, bytes + na);
                 tma_load_2d_elect(st, &wmap, k * 128, wrow, bar);
 #pragma unroll
-                for (int b = 0; b < NT / C::box; ++b)
+                for (int b = 0; b < C::rows / C::box; ++b)
                     if (b < boxes)
                         tma_load_2d_elect(st + C::a_bytes + b * C::box * 128, &xmap, k * 128, p0 + b * C::box, bar);
                 bulk_g2s_elect(st + C::a_bytes + C::b_bytes, sfa, na, bar);
@@ -496,25 +531,38 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         Ring last = ring.back(C::stages);
         for (int i = 0; i < C::stages; ++i, last.next(C::stages))
             if (ring.again || last.s < ring.s) mbar_wait(&full[last.s], last.phase, a.err, kSleepTries);
+    } else if (PAIR && warp == 1 && rank == 1) {
+        // ---------------- CTA 1 of a pair tells CTA 0 of its full stages ----------------
+        const int64_t total = uniform(q.stages());
+        Ring ring;
+#pragma unroll 1
+        for (int64_t i = 0; i < total; ++i) {
+            if (ok && !mbar_wait(&full[ring.s], ring.phase, a.err)) ok = false;
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            if (lane == 0) mbar_arrive_remote(&peer[ring.s], 0);
+            __syncwarp();
+            ring.next(C::stages);
+        }
     } else if (warp == 1) {
         // ---------------- products (whole warp, an elected lane issues) ----------------
         Ring ring;
         const uint32_t sbase = uniform(smem_u32(smem));
-        uint32_t sf = tmem + C::sf0;          // the stage's scales in TMEM: two sets in turn
+        uint32_t sf = tmem + C::sf0;          // the stage's scales in TMEM: the sets in turn
         int piece = 0;
         for (; uniform((int)q.next()); ++piece) {
             const FpTile t = fp_tile<NT>(plan, a.E, q.tile);
-            const uint32_t idesc = uniform(idesc_fp4<NV>((t.n + 15) / 16 * 16));
+            const uint32_t idesc = uniform(idesc_fp4<NV, C::M>((t.n + C::step - 1) / C::step * C::step));
             const int second = C::nb > 1 ? uniform(t.n > 128 ? 1 : 0) : 0;
             const int k0 = uniform(q.k0), k1 = uniform(q.k1);
             const int buf = piece & 1;
-            if (piece >= 2 && ok && !mbar_wait(&accempty[buf], ((piece >> 1) - 1) & 1, a.err)) ok = false;
+            if (piece >= 2 && ok && !mbar_wait_cluster(&accempty[buf], ((piece >> 1) - 1) & 1, a.err)) ok = false;
             tc_fence_after();
             const uint32_t d = tmem + NT * buf;
             uint32_t more = 0;                // 0: the tile's first product clears the accumulator
 #pragma unroll 1
             for (int k = k0; k < k1; ++k) {
                 if (ok && !mbar_wait(&full[ring.s], ring.phase, a.err)) ok = false;
+                if (PAIR && ok && !mbar_wait_cluster(&peer[ring.s], ring.phase, a.err)) ok = false;
                 tc_fence_after();
                 // the scale warps' plain stores, before the tensor unit's copy reads them: fenced
                 // here, where nothing else is in flight, and not by those warps, whose fence
@@ -528,25 +576,27 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
 #pragma unroll
                 for (int i = 0; i < C::atoms; ++i) {
                     if (i * (256 / C::atoms) >= cols) break;
-                    tc_copy_scales_elect(sf + 4 * i, sfa + 32 * i);
-                    tc_copy_scales_elect(sf + 4 * C::atoms + 4 * C::nb * i, sfb + 32 * C::nb * i);
+                    tc_copy_scales_elect<PAIR>(sf + 4 * i, sfa + 32 * i);
+                    tc_copy_scales_elect<PAIR>(sf + 4 * C::atoms + 4 * C::nb * i, sfb + 32 * C::nb * i);
                     if (second)
-                        tc_copy_scales_elect(sf + 4 * C::atoms + 4 * C::nb * i + 4, sfb + 32 * C::nb * i + 32);
+                        tc_copy_scales_elect<PAIR>(sf + 4 * C::atoms + 4 * C::nb * i + 4, sfb + 32 * C::nb * i + 32);
                 }
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     if (64 * j >= cols) break;
                     const int at = NV ? j : j >> 1;              // scale tile
                     const uint32_t id = NV ? 0u : 2u * (j & 1);  // first byte of its words
-                    tc_mma_fp4_elect<NV>(d, ad + 2 * j, bd + 2 * j, idesc | id << 29 | id << 4, sf + 4 * at,
-                                         sf + 4 * C::atoms + 4 * C::nb * at, more);
+                    tc_mma_fp4_elect<NV, PAIR>(d, ad + 2 * j, bd + 2 * j, idesc | id << 29 | id << 4, sf + 4 * at,
+                                               sf + 4 * C::atoms + 4 * C::nb * at, more);
                     more = 1;
                 }
-                tc_commit_elect(&empty[ring.s]);
-                sf = 2 * (tmem + C::sf0) + C::sf_cols - sf;
+                if (PAIR) tc_commit_pair_elect(&empty[ring.s]);
+                else tc_commit_elect(&empty[ring.s]);
+                if (C::sf_sets == 2) sf = 2 * (tmem + C::sf0) + C::sf_cols - sf;
                 ring.next(C::stages);
             }
-            tc_commit_elect(&accfull[buf]);
+            if (PAIR) tc_commit_pair_elect(&accfull[buf]);
+            else tc_commit_elect(&accfull[buf]);
         }
     } else if (warp < 4 || warp >= 8) {
         // ---------------- scales of the rows ----------------
@@ -559,13 +609,15 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         constexpr int ahead = 4;
         const int f = warp < 4 ? warp - 2 : warp - 6;
         uint32_t w[ahead][mine];
-        const uint32_t* from[mine];  // of the next stage to load, NULL for rows past the tile's
+        uint32_t from[mine];         // word to load next (all of X's scales are under 2^32 words)
         uint32_t to[mine];           // byte of the stage
+        int atom[mine];
 #pragma unroll
         for (int i = 0; i < mine; ++i) {
-            const int it = f + kFpScaleWarps * i, atom = it / words, j = it - atom * words;
-            to[i] = C::a_bytes + C::b_bytes + C::sfa_bytes + 512 * (C::nb * atom + j / 4) + 16 * lane + 4 * (j & 3);
-            from[i] = nullptr;
+            const int it = min(f + kFpScaleWarps * i, items - 1), j = it % words;
+            atom[i] = it / words;
+            to[i] = C::a_bytes + C::b_bytes + C::sfa_bytes + 512 * (C::nb * atom[i] + j / 4) + 16 * lane + 4 * (j & 3);
+            from[i] = 0;
         }
         const int64_t total = uniform(q.stages());
         int k = 0, k1 = 0;
@@ -575,23 +627,22 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 const FpTile t = fp_tile<NT>(plan, a.E, q.tile);
                 k = uniform(q.k0);
                 k1 = uniform(q.k1);
+                // rows past the tile's are not stored: any row's scales do for them
 #pragma unroll
                 for (int i = 0; i < mine; ++i) {
-                    const int it = f + kFpScaleWarps * i, atom = it / words, j = it - atom * words;
-                    const int64_t r = t.p0 + 32 * j + lane;
-                    from[i] = it < items && 32 * j < t.n && r < a.P
-                                  ? a.xs + scale_word(r, k * C::atoms + atom, a.xwords) : nullptr;
+                    const int j = min(f + kFpScaleWarps * i, items - 1) % words;
+                    from[i] = (uint32_t)scale_word(min(t.p0 + 32 * j + lane, a.P - 1), k * C::atoms + atom[i], a.xwords);
                 }
             }
-            const int left = a.xwords - k * C::atoms;  // tiles that the row still has
+            if (a.xwords - k * C::atoms >= C::atoms) {
 #pragma unroll
-            for (int i = 0; i < mine; ++i) {
-                dst[i] = 0;
-                if (from[i]) {
-                    if (left >= C::atoms || (f + kFpScaleWarps * i) / words < left) dst[i] = __ldg(from[i]);
-                    from[i] += C::atoms * 128;
-                }
+                for (int i = 0; i < mine; ++i) dst[i] = __ldg(a.xs + from[i]);
+            } else {  // the row's last scale tiles
+#pragma unroll
+                for (int i = 0; i < mine; ++i) dst[i] = atom[i] < a.xwords - k * C::atoms ? __ldg(a.xs + from[i]) : 0;
             }
+#pragma unroll
+            for (int i = 0; i < mine; ++i) from[i] += C::atoms * 128;
             ++k;
         };
         Ring ring;
@@ -609,8 +660,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 const uint32_t st = sbase + ring.s * C::stage;
 #pragma unroll
                 for (int i = 0; i < mine; ++i)
-                    if (f + kFpScaleWarps * i < items)
-                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + to[i]), "r"(w[d][i]) : "memory");
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + to[i]), "r"(w[d][i]) : "memory");
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&full[ring.s]);
                 ring.next(C::stages);
@@ -623,19 +673,20 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         for (int piece = 0; uniform((int)q.next()); ++piece) {
             const FpTile t = fp_tile<NT>(plan, a.E, q.tile);
             const int buf = piece & 1, n = uniform(t.n);
-            const int row = t.rt * 128 + 32 * quarter + lane;
+            const int row = t.rt * C::M + 128 * rank + 32 * quarter + lane;
             const bool begins = uniform((int)(q.k0 == 0));
             const float al = begins && a.alpha ? a.alpha[t.e] : 1.0f;
             float* part = a.partial + 32 * quarter + lane;
-            // the CTAs after this one with pieces of the tile: up to the first whose run
-            // starts at its end or later
-            int64_t last = blockIdx.x + 1;
+            // the CTAs (or pairs) after this one with pieces of the tile: up to the first whose
+            // run starts at its end or later; of a pair, the CTA with the same weight rows
+            const auto slot = [&](int64_t c) { return c * C::ctas + rank; };
+            int64_t last = unit + 1;
             if (begins && q.k1 < a.KS)
                 while (run.lo(last) < (q.tile + 1 - run.tile0) * a.KS) ++last;
             if (ok && !mbar_wait(&accfull[buf], (piece >> 1) & 1, a.err)) ok = false;
             tc_fence_after();
-            for (int64_t c = blockIdx.x + 1; c < last; ++c)
-                if (ok && !fp_wait_flag(a.flags + 4 * c + quarter, a.err)) ok = false;
+            for (int64_t c = unit + 1; c < last; ++c)
+                if (ok && !fp_wait_flag(a.flags + 4 * slot(c) + quarter, a.err)) ok = false;
             const uint32_t d = tmem + ((uint32_t)(32 * quarter) << 16) + NT * buf;
             YT* yp = y + t.p0 * a.R + row;        // this lane's row of y's columns
             float* pp = part + (int64_t)blockIdx.x * (128 * NT);
@@ -651,11 +702,11 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                         if (i < m) pp[i * 128] = __uint_as_float(v[i]);
                     continue;
                 }
-                for (int64_t c = blockIdx.x + 1; c < last; ++c)
+                for (int64_t c = unit + 1; c < last; ++c)
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         if (i < m)
-                            v[i] = __float_as_uint(__uint_as_float(v[i]) + __ldcg(part + c * (128 * NT) + (c0 + i) * 128));
+                            v[i] = __float_as_uint(__uint_as_float(v[i]) + __ldcg(part + slot(c) * (128 * NT) + (c0 + i) * 128));
                 if (row < a.R) {
                     YT* to = yp;
 #pragma unroll
@@ -672,18 +723,25 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 }
             } else {
                 __syncwarp();
-                for (int64_t c = blockIdx.x + 1; c < last; ++c)
-                    if (lane == 0) a.flags[4 * c + quarter] = 0;  // read once: down again for the next call
+                for (int64_t c = unit + 1; c < last; ++c)
+                    if (lane == 0) a.flags[4 * slot(c) + quarter] = 0;  // read once: down again for the next call
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&accempty[buf]);
+            if (lane == 0) {
+                if (PAIR) mbar_arrive_cluster(&accempty[buf], 0);
+                else mbar_arrive(&accempty[buf]);
+            }
         }
     }
     tc_fence_before();
     __syncthreads();
+    if (PAIR) cluster_sync();  // neither CTA leaves while the other may reach into it
     tc_fence_after();
-    if (warp == 0) tmem_dealloc(tmem, C::cols);
+    if (warp == 0) {
+        if (PAIR) tmem_dealloc_pair(tmem, C::cols);
+        else tmem_dealloc(tmem, C::cols);
+    }
 }
 
 }  // namespace coli

@@ -169,6 +169,61 @@ __device__ __forceinline__ void tma_load_2d_elect(void* dst, const CUtensorMap* 
         : "memory");
 }
 
+// CTAs of a cluster: rank, size, a barrier of all their threads, and a float of
+// another CTA's shared memory (at p's place in it)
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n barrier.cluster.wait.aligned;" ::: "memory");
+}
+__device__ __forceinline__ float ld_cluster(const float* p, uint32_t rank) {
+    uint32_t addr = (uint32_t)__cvta_generic_to_shared(p);
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+
+// One arrival at the barrier in the same place of CTA `rank`, releasing this
+// thread's writes to the cluster; and the wait that acquires them.
+__device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank) {
+    uint32_t addr = smem_u32(bar);
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(addr), "r"(rank));
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// The arrival alone, ordered after what this thread has seen of its own CTA's
+// shared memory (and after its proxy fence): for data that stays in that memory
+// and is read there, by the tensor unit of this SM.  The release above takes some
+// 1500 cycles under load, as it waits for everything the SM has in flight.
+__device__ __forceinline__ void mbar_arrive_remote(uint64_t* bar, uint32_t rank) {
+    uint32_t addr = smem_u32(bar);
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(addr), "r"(rank));
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, int32_t* err,
+                                                  uint32_t tries = kWaitTries) {
+    for (uint32_t i = 0; i < tries; ++i) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+            " selp.b32 %0, 1, 0, p;\n}"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity)
+            : "memory");
+        if (ok) return true;
+    }
+    if (err) atomicOr(err, kErrWaitTimeout);
+    return false;
+}
+
 // barrier among the first `threads` threads of the CTA (named barrier 1)
 __device__ __forceinline__ void named_sync(int threads) {
     asm volatile("bar.sync 1, %0;" ::"r"(threads) : "memory");

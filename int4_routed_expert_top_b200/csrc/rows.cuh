@@ -7,8 +7,10 @@
 // lanes of equal expert with match.any, and keeps its own counts per expert in
 // shared memory; a pick's row is the count of its expert in everything before
 // it.  Up to kSortOneCta picks one CTA does it all (one launch, the case of
-// decode); above, at most kSortMaxChunks CTAs count their chunk of the picks
-// first and a second launch places them.
+// decode: 2.7 us at 8 picks; 4096 picks would take it 11.3 us, the two launches
+// take 7.4 us for 8192); above, at most kSortMaxChunks CTAs count their chunk of
+// the picks first and a second launch places them (65536 picks: 14.9 us; with
+// 128 chunks, whose counts every CTA adds up, 21.8 us).
 //
 // The copies and sums are bound by HBM (each row of xs / o once): a thread owns
 // 16 bytes of columns and walks the token's picks.
@@ -20,8 +22,8 @@ namespace coli {
 
 constexpr int kSortThreads = 512;
 constexpr int kSortWarps = kSortThreads / 32;
-constexpr int kSortOneCta = 4096;     // picks
-constexpr int kSortMaxChunks = 128;
+constexpr int kSortOneCta = 1024;     // picks
+constexpr int kSortMaxChunks = 64;
 
 // expert of pick i, E for one that is not computed
 __device__ __forceinline__ int pick_expert(const int32_t* idx, const float* w, int64_t i, int E) {
@@ -103,9 +105,9 @@ __device__ __forceinline__ void sort_place(const int32_t* idx, const float* w, i
         __syncwarp();
         if (in) inv[i] = p;
         if (p >= 0) {
-            const int t = (int)(i / k);
+            const int t = (int)((uint32_t)i / (uint32_t)k);  // T * k <= 2^30
             if (pair_tok) pair_tok[p] = t;
-            if (pair_slot) pair_slot[p] = (int)(i - (int64_t)t * k);
+            if (pair_slot) pair_slot[p] = (int)i - t * k;
         }
     }
 }

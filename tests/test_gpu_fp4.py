@@ -169,8 +169,8 @@ def test_product_one_group(fmt, R, K, n):
 
 
 @pytest.mark.parametrize("fmt", list(FMT))
-@pytest.mark.parametrize("R,K,n", [(128, 256, 49), (128, 512, 128), (256, 288, 129), (100, 1024, 192), (384, 2048, 193),
-                                   (1000, 96, 500), (256, 6144, 400)])
+@pytest.mark.parametrize("R,K,n", [(128, 256, 49), (128, 512, 128), (256, 288, 129), (100, 1024, 192), (384, 2048, 193), (512, 512, 224), (640, 768, 225),
+                                   (1000, 96, 500), (256, 6144, 400), (128, 128, 449)])
 def test_product_one_group_many_rows(fmt, R, K, n):
     for yt in (F, B):
         check_product(fmt, 1, R, K, [n], yt)

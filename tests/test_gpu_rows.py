@@ -43,8 +43,8 @@ def run_sort(idx, E, w=None):
 
 @pytest.mark.parametrize("T,k,E,drop", [
     (1, 1, 1, 0.0), (1, 8, 256, 0.0), (1, 8, 256, 1.0), (3, 8, 256, 0.2), (33, 2, 5, 0.3), (100, 32, 64, 0.1),
-    (511, 8, 1024, 0.5), (512, 8, 3, 0.0),        # 4088 and 4096 picks: one launch
-    (4097, 1, 7, 0.1), (700, 9, 1024, 0.2),       # two launches
+    (127, 8, 1024, 0.5), (128, 8, 3, 0.0),        # 1016 and 1024 picks: one launch
+    (1025, 1, 7, 0.1), (511, 8, 1024, 0.5), (700, 9, 1024, 0.2),   # two launches
     (8192, 8, 256, 0.0), (16411, 8, 32, 0.9), (40000, 7, 1, 0.5)])
 def test_sort(T, k, E, drop):
     idx = picks(T, k, E, drop, T + k)
