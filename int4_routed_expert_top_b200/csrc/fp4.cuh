@@ -414,6 +414,75 @@ __device__ __forceinline__ void tc_mma_fp4_elect(uint32_t d, uint64_t adesc, uin
 }
 #undef COLI_MMA_FP4
 
+// A whole stage in one piece of code that one elected lane runs: the scale tiles
+// to TMEM (A's at sf, then B's, NB of them per scale tile of K), four products and
+// the arrival at `empty`.  Issued one by one, each with its own election and
+// address arithmetic, the eleven to seventeen instructions take 510 cycles, more
+// than the 448 that a 256 x 224 stage keeps the tensor unit busy.
+#define COLI_CP(G, P, DST, SRC)                                                                                  \
+    " add.u32 t, %6, " #DST ";\n add.u64 x, %" SRC ";\n"                                                        \
+    " @" P " tcgen05.cp.cta_group::" G ".32x128b.warpx4 [t], x;\n"
+#define COLI_STAGE_MMA(G, KIND, J, M, ID, SFA, SFB)                                                               \
+    " add.u64 x, %1, " #J ";\n add.u64 z, %2, " #J ";\n add.u32 i, %3, " #ID ";\n add.u32 t, %6, " #SFA ";\n"    \
+    " add.u32 u, %6, " #SFB ";\n @e tcgen05.mma.cta_group::" G ".kind::" KIND " [%0], x, z, i, [t], [u], " M ";\n"
+#define COLI_STAGE_BEGIN                                                                                          \
+    "{\n .reg .pred e, f, m, n;\n .reg .b64 x, z;\n .reg .b32 t, u, i;\n elect.sync _|e, 0xffffffff;\n"          \
+    " setp.ne.b32 m, %7, 0;\n setp.ne.and.b32 f, %8, 0, e;\n setp.eq.b32 n, 0, 0;\n"
+#define COLI_STAGE_OPERANDS                                                                                       \
+    ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "l"(sfa), "l"(sfb), "r"(sf), "r"(more), "r"(second), "r"(empty),      \
+        "h"((uint16_t)3)                                                                                          \
+        : "memory"
+#define COLI_COMMIT_1 " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%9];\n}"
+#define COLI_COMMIT_2                                                                                             \
+    " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%9], %10;\n}"
+// ID of a product that takes the upper two bytes of its scale words: 2 << 29 | 2 << 4
+#define COLI_MX "mxf4.block_scale.scale_vec::2X"
+#define COLI_NV "mxf4nvf4.block_scale.scale_vec::4X"
+template <bool NV, bool PAIR>
+__device__ __forceinline__ void fp4_stage(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint64_t sfa,
+                                          uint64_t sfb, uint32_t sf, uint32_t more, uint32_t second, uint32_t empty) {
+    if constexpr (PAIR && NV)
+        asm volatile(COLI_STAGE_BEGIN
+                     COLI_CP("2", "e", 0, "4, 0") COLI_CP("2", "e", 16, "5, 0") COLI_CP("2", "f", 20, "5, 32")
+                     COLI_CP("2", "e", 4, "4, 32") COLI_CP("2", "e", 24, "5, 64") COLI_CP("2", "f", 28, "5, 96")
+                     COLI_CP("2", "e", 8, "4, 64") COLI_CP("2", "e", 32, "5, 128") COLI_CP("2", "f", 36, "5, 160")
+                     COLI_CP("2", "e", 12, "4, 96") COLI_CP("2", "e", 40, "5, 192") COLI_CP("2", "f", 44, "5, 224")
+                     COLI_STAGE_MMA("2", COLI_NV, 0, "m", 0, 0, 16) COLI_STAGE_MMA("2", COLI_NV, 2, "n", 0, 4, 24)
+                     COLI_STAGE_MMA("2", COLI_NV, 4, "n", 0, 8, 32) COLI_STAGE_MMA("2", COLI_NV, 6, "n", 0, 12, 40)
+                     COLI_COMMIT_2 COLI_STAGE_OPERANDS);
+    else if constexpr (PAIR)
+        asm volatile(COLI_STAGE_BEGIN
+                     COLI_CP("2", "e", 0, "4, 0") COLI_CP("2", "e", 8, "5, 0") COLI_CP("2", "f", 12, "5, 32")
+                     COLI_CP("2", "e", 4, "4, 32") COLI_CP("2", "e", 16, "5, 64") COLI_CP("2", "f", 20, "5, 96")
+                     COLI_STAGE_MMA("2", COLI_MX, 0, "m", 0, 0, 8) COLI_STAGE_MMA("2", COLI_MX, 2, "n", 0x40000020, 0, 8)
+                     COLI_STAGE_MMA("2", COLI_MX, 4, "n", 0, 4, 16) COLI_STAGE_MMA("2", COLI_MX, 6, "n", 0x40000020, 4, 16)
+                     COLI_COMMIT_2 COLI_STAGE_OPERANDS);
+    else if constexpr (NV)
+        asm volatile(COLI_STAGE_BEGIN
+                     COLI_CP("1", "e", 0, "4, 0") COLI_CP("1", "e", 16, "5, 0")
+                     COLI_CP("1", "e", 4, "4, 32") COLI_CP("1", "e", 20, "5, 32")
+                     COLI_CP("1", "e", 8, "4, 64") COLI_CP("1", "e", 24, "5, 64")
+                     COLI_CP("1", "e", 12, "4, 96") COLI_CP("1", "e", 28, "5, 96")
+                     COLI_STAGE_MMA("1", COLI_NV, 0, "m", 0, 0, 16) COLI_STAGE_MMA("1", COLI_NV, 2, "n", 0, 4, 20)
+                     COLI_STAGE_MMA("1", COLI_NV, 4, "n", 0, 8, 24) COLI_STAGE_MMA("1", COLI_NV, 6, "n", 0, 12, 28)
+                     COLI_COMMIT_1 COLI_STAGE_OPERANDS);
+    else
+        asm volatile(COLI_STAGE_BEGIN
+                     COLI_CP("1", "e", 0, "4, 0") COLI_CP("1", "e", 8, "5, 0")
+                     COLI_CP("1", "e", 4, "4, 32") COLI_CP("1", "e", 12, "5, 32")
+                     COLI_STAGE_MMA("1", COLI_MX, 0, "m", 0, 0, 8) COLI_STAGE_MMA("1", COLI_MX, 2, "n", 0x40000020, 0, 8)
+                     COLI_STAGE_MMA("1", COLI_MX, 4, "n", 0, 4, 12) COLI_STAGE_MMA("1", COLI_MX, 6, "n", 0x40000020, 4, 12)
+                     COLI_COMMIT_1 COLI_STAGE_OPERANDS);
+}
+#undef COLI_CP
+#undef COLI_STAGE_MMA
+#undef COLI_STAGE_BEGIN
+#undef COLI_STAGE_OPERANDS
+#undef COLI_COMMIT_1
+#undef COLI_COMMIT_2
+#undef COLI_MX
+#undef COLI_NV
+
 // A role's place in the ring: slot, the phase of its barriers, and whether the
 // slot has been used before.
 struct Ring {
@@ -457,7 +526,6 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(fp_raw) + 1023) & ~uintptr_t(1023));
     __shared__ FpPlan plan;
     __shared__ __align__(8) uint64_t full[C::stages], empty[C::stages], accfull[2], accempty[2];
-    __shared__ __align__(8) uint64_t peer[C::stages];   // of CTA 0 of a pair: CTA 1's stage is full
     __shared__ uint32_t tmem_slot;
     const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
@@ -470,8 +538,9 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     }
     if (threadIdx.x == 32) {
         for (int s = 0; s < C::stages; ++s) {
-            mbar_init(&peer[s], 1);
-            mbar_init(&full[s], 1 + kFpScaleWarps);  // the copies' announcement, the scale warps
+
+            // the copies' announcement, the scale warps; in CTA 0 of a pair, CTA 1's stage
+            mbar_init(&full[s], 1 + kFpScaleWarps + (PAIR && rank == 0 ? 1 : 0));
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -539,7 +608,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         for (int64_t i = 0; i < total; ++i) {
             if (ok && !mbar_wait(&full[ring.s], ring.phase, a.err)) ok = false;
             asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            if (lane == 0) mbar_arrive_remote(&peer[ring.s], 0);
+            if (lane == 0) mbar_arrive_remote(&full[ring.s], 0);
             __syncwarp();
             ring.next(C::stages);
         }
@@ -547,8 +616,9 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         // ---------------- products (whole warp, an elected lane issues) ----------------
         Ring ring;
         const uint32_t sbase = uniform(smem_u32(smem));
-        uint32_t sf = tmem + C::sf0;          // the stage's scales in TMEM: the sets in turn
+        uint32_t sf = uniform(tmem + C::sf0);  // the stage's scales in TMEM: the sets in turn
         int piece = 0;
+        bool ready = false;                   // the ring's next stage has been seen to be full
         for (; uniform((int)q.next()); ++piece) {
             const FpTile t = fp_tile<NT>(plan, a.E, q.tile);
             const uint32_t idesc = uniform(idesc_fp4<NV, C::M>((t.n + C::step - 1) / C::step * C::step));
@@ -561,8 +631,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             uint32_t more = 0;                // 0: the tile's first product clears the accumulator
 #pragma unroll 1
             for (int k = k0; k < k1; ++k) {
-                if (ok && !mbar_wait(&full[ring.s], ring.phase, a.err)) ok = false;
-                if (PAIR && ok && !mbar_wait_cluster(&peer[ring.s], ring.phase, a.err)) ok = false;
+                if (!ready && ok && !mbar_wait(&full[ring.s], ring.phase, a.err)) ok = false;
                 tc_fence_after();
                 // the scale warps' plain stores, before the tensor unit's copy reads them: fenced
                 // here, where nothing else is in flight, and not by those warps, whose fence
@@ -573,27 +642,34 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 const uint64_t sfb = sfa + (C::sfa_bytes >> 4);
                 const uint64_t ad = smem_desc_sw128_at(st), bd = ad + (C::a_bytes >> 4);
                 const int cols = a.K - 256 * k;
-#pragma unroll
-                for (int i = 0; i < C::atoms; ++i) {
-                    if (i * (256 / C::atoms) >= cols) break;
-                    tc_copy_scales_elect<PAIR>(sf + 4 * i, sfa + 32 * i);
-                    tc_copy_scales_elect<PAIR>(sf + 4 * C::atoms + 4 * C::nb * i, sfb + 32 * C::nb * i);
-                    if (second)
-                        tc_copy_scales_elect<PAIR>(sf + 4 * C::atoms + 4 * C::nb * i + 4, sfb + 32 * C::nb * i + 32);
-                }
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if (64 * j >= cols) break;
-                    const int at = NV ? j : j >> 1;              // scale tile
-                    const uint32_t id = NV ? 0u : 2u * (j & 1);  // first byte of its words
-                    tc_mma_fp4_elect<NV, PAIR>(d, ad + 2 * j, bd + 2 * j, idesc | id << 29 | id << 4, sf + 4 * at,
-                                               sf + 4 * C::atoms + 4 * C::nb * at, more);
-                    more = 1;
-                }
-                if (PAIR) tc_commit_pair_elect(&empty[ring.s]);
-                else tc_commit_elect(&empty[ring.s]);
-                if (C::sf_sets == 2) sf = 2 * (tmem + C::sf0) + C::sf_cols - sf;
+                uint64_t* empty_s = &empty[ring.s];
                 ring.next(C::stages);
+                // asked before this stage is issued, so that the answer is there after it
+                ready = mbar_test(&full[ring.s], ring.phase);
+                if (cols >= 256) {
+                    fp4_stage<NV, PAIR>(d, ad, bd, idesc, sfa, sfb, sf, more, second, smem_u32(empty_s));
+                } else {  // the row's last columns
+#pragma unroll
+                    for (int i = 0; i < C::atoms; ++i) {
+                        if (i * (256 / C::atoms) >= cols) break;
+                        tc_copy_scales_elect<PAIR>(sf + 4 * i, sfa + 32 * i);
+                        tc_copy_scales_elect<PAIR>(sf + 4 * C::atoms + 4 * C::nb * i, sfb + 32 * C::nb * i);
+                        if (second)
+                            tc_copy_scales_elect<PAIR>(sf + 4 * C::atoms + 4 * C::nb * i + 4, sfb + 32 * C::nb * i + 32);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        if (64 * j >= cols) break;
+                        const int at = NV ? j : j >> 1;              // scale tile
+                        const uint32_t id = NV ? 0u : 2u * (j & 1);  // first byte of its words
+                        tc_mma_fp4_elect<NV, PAIR>(d, ad + 2 * j, bd + 2 * j, idesc | id << 29 | id << 4, sf + 4 * at,
+                                                   sf + 4 * C::atoms + 4 * C::nb * at, j > 0 ? 1u : more);
+                    }
+                    if (PAIR) tc_commit_pair_elect(empty_s);
+                    else tc_commit_elect(empty_s);
+                }
+                more = 1;
+                if (C::sf_sets == 2) sf = 2 * (tmem + C::sf0) + C::sf_cols - sf;
             }
             if (PAIR) tc_commit_pair_elect(&accfull[buf]);
             else tc_commit_elect(&accfull[buf]);
@@ -646,6 +722,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             ++k;
         };
         Ring ring;
+        bool free = false;           // the ring's next slot has been seen to be free
         const uint32_t sbase = uniform(smem_u32(smem));
 #pragma unroll 1
         for (int64_t base = -ahead; base < total; base += ahead) {
@@ -656,14 +733,16 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                     continue;
                 }
                 if (base + d >= total) break;
-                if (ok && ring.again && !mbar_wait(&empty[ring.s], ring.phase ^ 1, a.err)) ok = false;
+                if (ok && ring.again && !free && !mbar_wait(&empty[ring.s], ring.phase ^ 1, a.err)) ok = false;
                 const uint32_t st = sbase + ring.s * C::stage;
+                uint64_t* full_s = &full[ring.s];
+                ring.next(C::stages);
+                free = ring.again && mbar_test(&empty[ring.s], ring.phase ^ 1);
 #pragma unroll
                 for (int i = 0; i < mine; ++i)
                     asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + to[i]), "r"(w[d][i]) : "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&full[ring.s]);
-                ring.next(C::stages);
+                if (lane == 0) mbar_arrive(full_s);
                 load(w[d]);
             }
         }
