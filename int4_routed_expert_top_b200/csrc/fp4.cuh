@@ -39,7 +39,7 @@
 // CTA roles: warp 0 copies (codes by 2-D TMA with the 128-byte swizzle, the
 // weights' scales by bulk copy), four warps bring the rows' scales (rows of an
 // expert start anywhere, a scale tile only at multiples of 128, so those are
-// gathered by plain loads into a tile in shared memory), warp 1 copies scales
+// gathered word by word into a tile in shared memory), warp 1 copies scales
 // to TMEM and issues the products, warps 4-7 store.  Accumulators are
 // double-buffered, so a tile's stores overlap the next one's products.
 #pragma once
@@ -539,8 +539,8 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     if (threadIdx.x == 32) {
         for (int s = 0; s < C::stages; ++s) {
 
-            // the copies' announcement, the scale warps; in CTA 0 of a pair, CTA 1's stage
-            mbar_init(&full[s], 1 + kFpScaleWarps + (PAIR && rank == 0 ? 1 : 0));
+            // the copies' announcement, the lanes of the scale warps; in CTA 0 of a pair, CTA 1's stage
+            mbar_init(&full[s], 1 + 32 * kFpScaleWarps + (PAIR && rank == 0 ? 1 : 0));
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -633,9 +633,8 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             for (int k = k0; k < k1; ++k) {
                 if (!ready && ok && !mbar_wait(&full[ring.s], ring.phase, a.err)) ok = false;
                 tc_fence_after();
-                // the scale warps' plain stores, before the tensor unit's copy reads them: fenced
-                // here, where nothing else is in flight, and not by those warps, whose fence
-                // would wait for their loads
+                // the scale warps' copies are writes of the generic proxy, and the tensor unit reads
+                // them: fenced here, where they are known to have landed
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 const uint32_t st = sbase + ring.s * C::stage;
                 const uint64_t sfa = smem_desc_scales(st + C::a_bytes + C::b_bytes);
@@ -677,75 +676,51 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     } else if (warp < 4 || warp >= 8) {
         // ---------------- scales of the rows ----------------
         // A stage has atoms * NT / 32 runs of 32 rows' words; warp f takes runs f, f + 4, ..: a
-        // lane loads its row's word and stores it where the scale tile has it.  The loads of a
-        // stage are issued `ahead` stages before it is stored.
+        // lane copies its row's word to where the scale tile has it.  The copies are asynchronous
+        // and arrive at the barrier by themselves, so a stage's are in flight as long as its TMA
+        // copies are; through registers, loaded some stages ahead, the unrolled code took more
+        // time in the instruction cache than its loads saved.
         constexpr int words = NT / 32;
         constexpr int items = C::atoms * words;
         constexpr int mine = (items + kFpScaleWarps - 1) / kFpScaleWarps;
-        constexpr int ahead = 4;
         const int f = warp < 4 ? warp - 2 : warp - 6;
-        uint32_t w[ahead][mine];
-        uint32_t from[mine];         // word to load next (all of X's scales are under 2^32 words)
+        const uint32_t sbase = uniform(smem_u32(smem));
         uint32_t to[mine];           // byte of the stage
-        int atom[mine];
 #pragma unroll
         for (int i = 0; i < mine; ++i) {
-            const int it = min(f + kFpScaleWarps * i, items - 1), j = it % words;
-            atom[i] = it / words;
-            to[i] = C::a_bytes + C::b_bytes + C::sfa_bytes + 512 * (C::nb * atom[i] + j / 4) + 16 * lane + 4 * (j & 3);
-            from[i] = 0;
+            const int it = min(f + kFpScaleWarps * i, items - 1), atom = it / words, j = it - atom * words;
+            to[i] = sbase + C::a_bytes + C::b_bytes + C::sfa_bytes + 512 * (C::nb * atom + j / 4) + 16 * lane + 4 * (j & 3);
         }
-        const int64_t total = uniform(q.stages());
-        int k = 0, k1 = 0;
-        const auto load = [&](uint32_t (&dst)[mine]) {  // the next stage's words, if there is one
-            if (k == k1) {
-                if (!uniform((int)q.next())) return;
-                const FpTile t = fp_tile<NT>(plan, a.E, q.tile);
-                k = uniform(q.k0);
-                k1 = uniform(q.k1);
-                // rows past the tile's are not stored: any row's scales do for them
-#pragma unroll
-                for (int i = 0; i < mine; ++i) {
-                    const int j = min(f + kFpScaleWarps * i, items - 1) % words;
-                    from[i] = (uint32_t)scale_word(min(t.p0 + 32 * j + lane, a.P - 1), k * C::atoms + atom[i], a.xwords);
-                }
-            }
-            if (a.xwords - k * C::atoms >= C::atoms) {
-#pragma unroll
-                for (int i = 0; i < mine; ++i) dst[i] = __ldg(a.xs + from[i]);
-            } else {  // the row's last scale tiles
-#pragma unroll
-                for (int i = 0; i < mine; ++i) dst[i] = atom[i] < a.xwords - k * C::atoms ? __ldg(a.xs + from[i]) : 0;
-            }
-#pragma unroll
-            for (int i = 0; i < mine; ++i) from[i] += C::atoms * 128;
-            ++k;
-        };
         Ring ring;
         bool free = false;           // the ring's next slot has been seen to be free
-        const uint32_t sbase = uniform(smem_u32(smem));
-#pragma unroll 1
-        for (int64_t base = -ahead; base < total; base += ahead) {
+        while (uniform((int)q.next())) {
+            const FpTile t = fp_tile<NT>(plan, a.E, q.tile);
+            const int k0 = uniform(q.k0), k1 = uniform(q.k1);
+            const uint32_t* from[mine];
 #pragma unroll
-            for (int d = 0; d < ahead; ++d) {
-                if (base < 0) {
-                    load(w[d]);
-                    continue;
-                }
-                if (base + d >= total) break;
+            for (int i = 0; i < mine; ++i) {
+                const int it = min(f + kFpScaleWarps * i, items - 1), atom = it / words, j = it - atom * words;
+                // rows past the tile's are not stored: any row's scales do for them
+                from[i] = a.xs + scale_word(min(t.p0 + 32 * j + lane, a.P - 1), k0 * C::atoms + atom, a.xwords);
+            }
+#pragma unroll 1
+            for (int k = k0; k < k1; ++k) {
                 if (ok && ring.again && !free && !mbar_wait(&empty[ring.s], ring.phase ^ 1, a.err)) ok = false;
-                const uint32_t st = sbase + ring.s * C::stage;
+                const uint32_t at = ring.s * C::stage;
                 uint64_t* full_s = &full[ring.s];
                 ring.next(C::stages);
                 free = ring.again && mbar_test(&empty[ring.s], ring.phase ^ 1);
+                const int left = a.xwords - k * C::atoms;  // scale tiles that the row still has
 #pragma unroll
-                for (int i = 0; i < mine; ++i)
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(st + to[i]), "r"(w[d][i]) : "memory");
-                __syncwarp();
-                if (lane == 0) mbar_arrive(full_s);
-                load(w[d]);
+                for (int i = 0; i < mine; ++i) {
+                    const int atom = min(f + kFpScaleWarps * i, items - 1) / words;
+                    if (atom < left) cp_async4(at + to[i], from[i]);
+                    from[i] += C::atoms * 128;
+                }
+                cp_async_arrive(full_s);
             }
         }
+        cp_async_wait_all();         // the last copies have landed before the CTA may end
     } else {
         // ---------------- stores: weight rows 32 quarter + lane of the tile ----------------
         const int quarter = warp & 3;

@@ -118,6 +118,16 @@ __device__ __forceinline__ int64_t uniform(int64_t v) {
     return (int64_t)__shfl_sync(0xffffffffu, (long long)v, 0);
 }
 
+// global -> shared copy of 4 bytes by this thread, its arrival at `bar` once all
+// its copies so far have landed (one of the barrier's count), and the wait for them
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
 // global -> shared bulk copy, completion counted in bytes on `bar`.  Both
 // addresses 16-byte aligned, size a multiple of 16.
 __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t bytes,
