@@ -62,7 +62,7 @@ int launch_product(const FpArgs& a, const void* x_codes, const void* w_codes, vo
     if ((rc = set_smem((const void*)kern, C::smem))) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(std::min(sm_count(), kFpMaxGrid) / C::ctas * C::ctas);
-    cfg.blockDim = dim3(kFpThreads);
+    cfg.blockDim = dim3(C::threads);
     cfg.dynamicSmemBytes = C::smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];

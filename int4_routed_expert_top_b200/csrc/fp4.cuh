@@ -187,15 +187,16 @@ fp4_quantize_kernel(Fp4QuantArgs a, int warps, int rows_per, const T* __restrict
 // ---------------------------------------------------------------------------
 // product
 // ---------------------------------------------------------------------------
-// warps 0 copies, 1 products, 2-3 and 8-9 scales of the rows, 4-7 stores
-constexpr int kFpThreads = 320;
+// warps 0 copies, 1 products, 2-3 and 8-9 scales of the rows, 4-7 and (for tiles of
+// many rows) 10-13 stores
 constexpr int kFpScaleWarps = 4;
+constexpr int kFpStoreWarps = 8;   // at most
 constexpr int kFpMaxE = 1024;
 constexpr int kFpMinUnits = 2;     // stages per CTA at least, before fewer CTAs take part
 constexpr int kFpMaxGrid = 160;    // B200 has 148 SMs; the workspace is sized for this many
 // the workspace: error flags, a flag per CTA and store warp, then partial sums
 constexpr int kFpFlagBytes = 256;
-constexpr int kFpHeadBytes = kFpFlagBytes + kFpMaxGrid * 4 * 8;
+constexpr int kFpHeadBytes = kFpFlagBytes + kFpMaxGrid * kFpStoreWarps * 8;
 // a raised flag: a value that unset memory does not hold (0 after every call)
 constexpr uint64_t kFpRaised = 0x9d3ac1f5e8276b41ull;
 
@@ -206,6 +207,9 @@ struct FpShape {
     static constexpr int ctas = PAIR ? 2 : 1;
     static constexpr int rows = NT / ctas;                   // of X in a CTA's shared memory
     static constexpr int box = PAIR ? rows / 2 : rows;       // rows per TMA box of X
+    static constexpr int store_warps = NT > 32 ? kFpStoreWarps : 4;
+    static constexpr int groups = store_warps / 4;           // warps to a quarter of the lanes
+    static constexpr int threads = 32 * (6 + store_warps);
     static constexpr int step = 16 * ctas;                   // N is a multiple of it
     static constexpr int atoms = NV ? 4 : 2;                 // 512-byte scale tiles per 256 columns
     static constexpr int nb = (NT + 127) / 128;              // of the rows, per atom
@@ -242,7 +246,7 @@ struct FpArgs {
 struct FpPlan {
     int32_t begin[kFpMaxE + 1];
     int64_t tile0[kFpMaxE + 1];
-    int64_t warp_sum[kFpThreads / 32];
+    int64_t warp_sum[6 + kFpStoreWarps];
 };
 
 // Each thread takes four experts; offsets are clamped so that no value of them
@@ -518,7 +522,7 @@ __device__ __forceinline__ bool fp_wait_flag(const uint64_t* flag, int32_t* err)
 }
 
 template <int NT, bool NV, bool PAIR, typename YT>
-__global__ void __launch_bounds__(kFpThreads, 1)
+__global__ void __launch_bounds__(FpShape<NT, NV, PAIR>::threads, 1)
 fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
                    FpArgs a, YT* y) {
     using C = FpShape<NT, NV, PAIR>;
@@ -545,7 +549,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         }
         for (int b = 0; b < 2; ++b) {
             mbar_init(&accfull[b], 1);
-            mbar_init(&accempty[b], 4 * C::ctas);
+            mbar_init(&accempty[b], C::store_warps * C::ctas);
         }
         fence_mbar_init();
     }
@@ -673,7 +677,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             if (PAIR) tc_commit_pair_elect(&accfull[buf]);
             else tc_commit_elect(&accfull[buf]);
         }
-    } else if (warp < 4 || warp >= 8) {
+    } else if (warp < 4 || (warp >= 8 && warp < 10)) {
         // ---------------- scales of the rows ----------------
         // A stage has atoms * NT / 32 runs of 32 rows' words; warp f takes runs f, f + 4, ..: a
         // lane copies its row's word to where the scale tile has it.  The copies are asynchronous
@@ -723,7 +727,10 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
         cp_async_wait_all();         // the last copies have landed before the CTA may end
     } else {
         // ---------------- stores: weight rows 32 quarter + lane of the tile ----------------
-        const int quarter = warp & 3;
+        // A warp reaches its own quarter of the accumulator's lanes alone.  Tiles of many rows have
+        // two warps to a quarter, each with every second group of 16 columns: with one, a tile's
+        // stores take 4.2 us, as long as ten stages (with two, 3.3 us).
+        const int quarter = warp & 3, half = warp < 8 ? 0 : 1, flag = 2 * quarter + half;
         for (int piece = 0; uniform((int)q.next()); ++piece) {
             const FpTile t = fp_tile<NT>(plan, a.E, q.tile);
             const int buf = piece & 1, n = uniform(t.n);
@@ -740,12 +747,12 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             if (ok && !mbar_wait(&accfull[buf], (piece >> 1) & 1, a.err)) ok = false;
             tc_fence_after();
             for (int64_t c = unit + 1; c < last; ++c)
-                if (ok && !fp_wait_flag(a.flags + 4 * slot(c) + quarter, a.err)) ok = false;
+                if (ok && !fp_wait_flag(a.flags + kFpStoreWarps * slot(c) + flag, a.err)) ok = false;
             const uint32_t d = tmem + ((uint32_t)(32 * quarter) << 16) + NT * buf;
-            YT* yp = y + t.p0 * a.R + row;        // this lane's row of y's columns
-            float* pp = part + (int64_t)blockIdx.x * (128 * NT);
+            YT* yp = y + (t.p0 + 16 * half) * a.R + row;  // this lane's row of y's columns
+            float* pp = part + (int64_t)blockIdx.x * (128 * NT) + 16 * half * 128;
 #pragma unroll 1
-            for (int c0 = 0; c0 < n; c0 += 16, yp += 16 * (int64_t)a.R, pp += 16 * 128) {
+            for (int c0 = 16 * half; c0 < n; c0 += 16 * C::groups, yp += 16 * C::groups * (int64_t)a.R, pp += 16 * C::groups * 128) {
                 uint32_t v[16];
                 tmem_ld_32x32b_x16(d + c0, v);
                 tmem_wait_ld();
@@ -761,24 +768,26 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                     for (int i = 0; i < 16; ++i)
                         if (i < m)
                             v[i] = __float_as_uint(__uint_as_float(v[i]) + __ldcg(part + slot(c) * (128 * NT) + (c0 + i) * 128));
-                if (row < a.R) {
-                    YT* to = yp;
+                if (row >= a.R) continue;
+                if (m >= 16) {
 #pragma unroll
-                    for (int i = 0; i < 16; ++i, to += a.R)
-                        if (i < m) *to = from_f32<YT>(__uint_as_float(v[i]) * al);
+                    for (int i = 0; i < 16; ++i) yp[i * (int64_t)a.R] = from_f32<YT>(__uint_as_float(v[i]) * al);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        if (i < m) yp[i * (int64_t)a.R] = from_f32<YT>(__uint_as_float(v[i]) * al);
                 }
             }
+            __syncwarp();
             if (!begins) {
-                __syncwarp();
                 if (lane == 0) {
                     __threadfence();
-                    asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(a.flags + 4 * blockIdx.x + quarter), "l"(kFpRaised)
-                                 : "memory");
+                    asm volatile("st.release.gpu.global.u64 [%0], %1;"
+                                 ::"l"(a.flags + kFpStoreWarps * (int64_t)blockIdx.x + flag), "l"(kFpRaised) : "memory");
                 }
             } else {
-                __syncwarp();
-                for (int64_t c = unit + 1; c < last; ++c)
-                    if (lane == 0) a.flags[4 * slot(c) + quarter] = 0;  // read once: down again for the next call
+                for (int64_t c = unit + 1; c < last; ++c)  // read once: down again for the next call
+                    if (lane == 0) a.flags[kFpStoreWarps * slot(c) + flag] = 0;
             }
             tc_fence_before();
             __syncwarp();
