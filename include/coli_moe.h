@@ -595,7 +595,8 @@ int coli_moe_fp4_quantize(coli_fp4 fmt, const void* x, coli_dtype xt, int64_t n_
  * E * R < 2^31, K a multiple of 32.  ws: device, 16-byte aligned,
  * coli_moe_fp4_product_workspace_size bytes.  coli_moe_fp4_product_status is
  * coli_moe_status for these calls: it synchronises the stream and reports
- * whether a bounded wait gave up in the last call that used ws. */
+ * whether a bounded wait gave up in the last call that used ws (after which ws
+ * has to be cleared to zeros before its next use). */
 int coli_moe_fp4_product_workspace_size(coli_fp4 fmt, int64_t P, int32_t K, int32_t E, int32_t R,
                                         size_t* bytes);
 int coli_moe_fp4_product(coli_fp4 fmt, const void* x_codes, const void* x_scales, int64_t P,

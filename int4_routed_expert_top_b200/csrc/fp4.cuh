@@ -299,18 +299,21 @@ __device__ __forceinline__ void fp_plan(const FpArgs& a, FpPlan& p) {
     __syncthreads();
 }
 
-// The share of every CTA: tiles c, c + G, .. of the first waves * G, and units
-// [lo(c), lo(c + 1)) of the tiles from tile0 on.
+// The share of every CTA (or pair): tiles c, c + G, .. of the first waves * G, and
+// units [lo(c), lo(c + 1)) of the tiles from tile0 on.  As many of them share those
+// as get kFpMinUnits each, so that no run between two others is empty: whoever
+// begins a tile waits for every CTA up to the tile's end.
 struct FpRun {
-    int64_t G, waves, tile0, U;
+    int64_t G, waves, tile0, U, sharers;
     __device__ __forceinline__ FpRun(const FpArgs& a, const FpPlan& p, int grid) {  // grid: CTAs, or pairs
         const int64_t tiles = p.tile0[a.E];
         G = min((int64_t)grid, max((int64_t)1, tiles * a.KS / kFpMinUnits));
         waves = tiles / G;
         tile0 = waves * G;
         U = (tiles - tile0) * a.KS;
+        sharers = min(G, max((int64_t)1, U / kFpMinUnits));
     }
-    __device__ __forceinline__ int64_t lo(int64_t c) const { return c >= G ? U : U * c / G; }
+    __device__ __forceinline__ int64_t lo(int64_t c) const { return c >= sharers ? U : U * c / sharers; }
 };
 
 struct FpTile {
@@ -508,12 +511,13 @@ struct Ring {
     }
 };
 
-// Warp-wide wait for a flag of another CTA's store warp, a second at most
+// Warp-wide wait for a flag of another CTA's store warp: some ten seconds at most,
+// since that CTA may have to wait for an SM that another stream's kernel holds
 __device__ __forceinline__ bool fp_wait_flag(const uint64_t* flag, int32_t* err) {
     int ok = 1;
     if ((threadIdx.x & 31) == 0) {
         uint64_t v = 0;
-        for (int i = 0; i < (1 << 21) && v != kFpRaised; ++i)
+        for (int i = 0; i < (1 << 25) && v != kFpRaised; ++i)
             asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(flag) : "memory");
         ok = v == kFpRaised;
         if (!ok) atomicOr(err, kErrWaitTimeout);

@@ -186,6 +186,15 @@ def test_product_groups(fmt, R, K, sizes):
         check_product(fmt, len(sizes), R, K, sizes, yt, seed=len(sizes))
 
 
+@pytest.mark.parametrize("tiles,K,n", [(149, 512, 1), (149, 768, 2), (150, 1024, 1), (297, 512, 1), (75, 512, 60),
+                                       (75, 768, 50), (76, 1280, 49), (151, 512, 100), (222, 768, 64)])
+def test_product_few_tiles_left_over(tiles, K, n):
+    """A little more than whole waves of tiles (148 CTAs, or 74 pairs of them): the rest has
+    fewer stages than there are CTAs, so that some get none."""
+    rows = 128 if n <= 48 else 256
+    check_product("mx", 1, rows * tiles, K, [n])
+
+
 @pytest.mark.parametrize("fmt", list(FMT))
 def test_product_wide_scales_and_no_alpha(fmt):
     check_product(fmt, 3, 256, 512, [4, 70, 9], wide=True, alpha=False)
