@@ -4,6 +4,8 @@
 // norm.cuh on the caller's stream.
 #include <algorithm>
 #include <cmath>
+#include <initializer_list>
+#include <utility>
 
 #include "coli_moe.h"
 #include "common.cuh"
@@ -40,25 +42,35 @@ int64_t sort_chunk(int64_t P) {
     return ((P + kSortMaxChunks - 1) / kSortMaxChunks + group - 1) / group * group;
 }
 
-template <typename V>
+template <typename V, int N>
 int launch_dispatch(const void* x, int T, int nvec, int k, const int32_t* inv, void* xs, cudaStream_t st) {
-    const int per = (nvec + 255) / 256;
-    return launch_pdl(dispatch_kernel<V>, dim3((unsigned)T * per), 256, 0, st, "dispatch", (const V*)x,
+    const int per = (nvec + 256 * N - 1) / (256 * N);
+    return launch_pdl(dispatch_kernel<V, N>, dim3((unsigned)T * per), 256, 0, st, "dispatch", (const V*)x,
                       (int64_t)T * k, nvec, per, k, inv, (V*)xs);
+}
+
+// How many neighbouring elements an access may take: `most`, 2 or 1, by the row
+// length and every pointer's alignment (sizes: of the elements behind them).
+template <int most>
+int chunk_of(int H, std::initializer_list<std::pair<const void*, int>> buffers) {
+    for (int w : {most, 2}) {
+        bool ok = H % w == 0;
+        for (const auto& b : buffers) ok = ok && aligned(b.first, w * b.second);
+        if (ok) return w;
+    }
+    return 1;
 }
 
 template <typename OT, typename YT>
 int launch_rows_sum(const void* o, int T, int H, int k, const int32_t* inv, const float* w,
                     const void* residual, void* y, cudaStream_t st) {
-    // 16 bytes of o per thread where rows and pointers allow it
-    constexpr int N = 16 / sizeof(OT);
-    constexpr int ya = N * sizeof(YT);
-    const bool wide = H % N == 0 && aligned(o, 16) && aligned(residual, ya) && aligned(y, ya);
-    const int cols = 32 * (wide ? N : 1);
-    const int64_t items = (int64_t)T * ((H + cols - 1) / cols);
-    const auto kern = wide ? rows_sum_kernel<OT, YT, N> : rows_sum_kernel<OT, YT, 1>;
-    // as many CTAs as the SMs hold at three each, and no more than there are warps of work
-    const int grid = (int)std::min<int64_t>((items + 7) / 8, 3 * 148);
+    constexpr int N = 16 / sizeof(OT);  // columns of a lane: 16 bytes of o
+    const int W = chunk_of<N>(H, {{o, (int)sizeof(OT)}, {residual, (int)sizeof(YT)}, {y, (int)sizeof(YT)}});
+    const int64_t items = (int64_t)T * ((H + 32 * N - 1) / (32 * N));
+    const auto kern = W == N ? rows_sum_kernel<OT, YT, N, N>
+                             : W == 2 ? rows_sum_kernel<OT, YT, N, 2> : rows_sum_kernel<OT, YT, N, 1>;
+    // as many CTAs as the SMs hold, and no more than there are warps of work
+    const int grid = (int)std::min<int64_t>((items + 7) / 8, (W == N ? 3 : 2) * 148);
     return launch_pdl(kern, dim3(grid), 256, 0, st, "combine", (const OT*)o, (int64_t)T * k, T, H, k, inv, w,
                       (const YT*)residual, (YT*)y);
 }
@@ -67,11 +79,11 @@ template <typename YT, typename OT>
 int launch_rows_sum_backward(const void* dy, const void* o, int T, int H, int k, const int32_t* inv,
                              const float* w, void* d_o, float* dw, cudaStream_t st) {
     constexpr int N = 16 / sizeof(OT);
-    constexpr int ya = N * sizeof(YT);
-    const bool wide = H % N == 0 && aligned(o, 16) && aligned(d_o, 16) && aligned(dy, ya);
-    const auto kern = wide ? rows_sum_backward_kernel<YT, OT, N> : rows_sum_backward_kernel<YT, OT, 1>;
-    return launch_pdl(kern, dim3((unsigned)(((int64_t)T * k + 7) / 8)), 256, 0, st, "combine backward", (const YT*)dy, (const OT*)o,
-                      (int64_t)T * k, H, k, inv, w, (OT*)d_o, dw);
+    const int W = chunk_of<N>(H, {{o, (int)sizeof(OT)}, {d_o, (int)sizeof(OT)}, {dy, (int)sizeof(YT)}});
+    const auto kern = W == N ? rows_sum_backward_kernel<YT, OT, N, N>
+                             : W == 2 ? rows_sum_backward_kernel<YT, OT, N, 2> : rows_sum_backward_kernel<YT, OT, N, 1>;
+    return launch_pdl(kern, dim3((unsigned)(((int64_t)T * k + 7) / 8)), 256, 0, st, "combine backward",
+                      (const YT*)dy, (const OT*)o, (int64_t)T * k, H, k, inv, w, (OT*)d_o, dw);
 }
 
 int norm_ok(const char* what, const coli_norm_desc* d, int T) {
@@ -98,17 +110,15 @@ NormArgs norm_args(const coli_norm_desc& d, const float* gate, int T) {
     return a;
 }
 
-// elements per vector, vectors per thread and threads of a row
-struct NormShape { int V, N, threads; };
+// neighbours of an access, vectors of eight per thread and threads of a row
+struct NormShape { int W, N, threads; };
 // Many tokens: about 256 threads a row, so that an SM holds several rows.  Few
 // (less than two rows per SM): one vector a thread (the time of one row is what counts).
-NormShape norm_shape(int H, int T, bool wide, bool backward) {
+NormShape norm_shape(int H, int T, int W, bool backward) {
     NormShape s;
-    s.V = wide ? 8 : 1;
-    const int vecs = H / s.V;
-    if (!wide)
-        s.N = vecs <= 16 * 512 ? 16 : 32;
-    else if (vecs <= 256 || (!backward && T < 2 * 148 && vecs <= 1024))
+    s.W = W;
+    const int vecs = (H + 7) / 8;
+    if (vecs <= 256 || (!backward && T < 2 * 148 && vecs <= 1024))
         s.N = 1;
     else
         s.N = vecs <= 2 * 256 ? 2 : vecs <= 3 * 512 ? 3 : 4;
@@ -117,16 +127,18 @@ NormShape norm_shape(int H, int T, bool wide, bool backward) {
 }
 
 // calls the kernel with its type and shape parameters as template arguments
+template <template <typename, typename, int, int> class K, typename XT, typename BT, int W, typename... A>
+int norm_launch_w(const NormShape& s, A... args) {
+    if (s.N == 1) return K<XT, BT, W, 1>::launch(s, args...);
+    if (s.N == 2) return K<XT, BT, W, 2>::launch(s, args...);
+    if (s.N == 3) return K<XT, BT, W, 3>::launch(s, args...);
+    return K<XT, BT, W, 4>::launch(s, args...);
+}
 template <template <typename, typename, int, int> class K, typename XT, typename BT, typename... A>
 int norm_launch(const NormShape& s, A... args) {
-    if (s.V == 8) {
-        if (s.N == 1) return K<XT, BT, 8, 1>::launch(s, args...);
-        if (s.N == 2) return K<XT, BT, 8, 2>::launch(s, args...);
-        if (s.N == 3) return K<XT, BT, 8, 3>::launch(s, args...);
-        return K<XT, BT, 8, 4>::launch(s, args...);
-    }
-    if (s.N == 16) return K<XT, BT, 1, 16>::launch(s, args...);
-    return K<XT, BT, 1, 32>::launch(s, args...);
+    if (s.W == 8) return norm_launch_w<K, XT, BT, 8>(s, args...);
+    if (s.W == 2) return norm_launch_w<K, XT, BT, 2>(s, args...);
+    return norm_launch_w<K, XT, BT, 1>(s, args...);
 }
 template <template <typename, typename, int, int> class K, typename... A>
 int norm_dispatch(const coli_norm_desc& d, const NormShape& s, A... args) {
@@ -135,11 +147,11 @@ int norm_dispatch(const coli_norm_desc& d, const NormShape& s, A... args) {
     return norm_launch<K, __nv_bfloat16, __nv_bfloat16>(s, args...);
 }
 
-template <typename XT, typename BT, int V, int N>
+template <typename XT, typename BT, int W, int N>
 struct NormForward {
     static int launch(const NormShape& s, const NormArgs& a, const void* x, const void* o, void* x_out,
                       void* n_out, float* rstd_post, float* rstd_pre, cudaStream_t st) {
-        return launch_pdl(block_norm_kernel<XT, BT, V, N>, dim3(a.T), s.threads, 0, st, "block norm", a,
+        return launch_pdl(block_norm_kernel<XT, BT, W, N>, dim3(a.T), s.threads, 0, st, "block norm", a,
                           (const XT*)x, (const BT*)o, (XT*)x_out, (BT*)n_out, rstd_post, rstd_pre);
     }
 };
@@ -149,11 +161,17 @@ struct NormForward {
 // per SM, so that one's loads cover the other's sums over the row.  Clusters of two add the sums over tokens before they leave an SM
 // (clusters of four leave SMs without a CTA where a GPC's number of them is no
 // multiple of four: the ring's 37 did not fit at once and took twice as long).
-constexpr int kNormSms = 148, kNormCtas = 2 * kNormSms;
+constexpr int kNormSms = 148;
 constexpr int kNormRingMaxH = 8192;
 constexpr int kNormRingBytes = 224 * 1024;   // of an SM
 constexpr int kNormCluster = 2;
 int norm_backward_cluster(int grid) { return grid >= kNormCluster ? kNormCluster : 1; }
+// CTAs of the plain form: two per SM, more where rows are short (1024 threads, at
+// most 16 CTAs, and their sums in 200 KB of shared memory)
+int norm_plain_ctas(const coli_norm_desc& d, int T) {
+    const int threads = norm_shape(d.H, T, 1, true).threads;
+    return kNormSms * std::max(1, std::min({16, std::max(2, 1024 / threads), 200 * 1024 / (kNormSums * d.H * 4)}));
+}
 int norm_backward_grid(int T, int ctas) {
     const int grid = std::min(T, ctas);
     return grid / norm_backward_cluster(grid) * norm_backward_cluster(grid);
@@ -188,13 +206,13 @@ NormRing norm_ring(const coli_norm_desc& d, int ctas, bool wide, bool x_out, boo
     return r;
 }
 
-template <typename XT, typename BT, int V, int N, bool RING>
+template <typename XT, typename BT, int W, int N, bool RING>
 struct NormBackward {
     static int launch(const NormShape& s, const NormArgs& a, const NormSums& keep, const NormRing& ring,
                       const void* x_out, const void* o, const float* rstd_post, const float* rstd_pre,
                       const void* dx_out, const void* dn, void* dx, void* d_o, float* dgate, float* partial, int grid,
                       cudaStream_t st) {
-        const auto kern = block_norm_backward_kernel<XT, BT, V, N, RING>;
+        const auto kern = block_norm_backward_kernel<XT, BT, W, N, RING>;
         const int smem = RING ? ring.first + ring.stages * ring.stage : keep.n * a.H * 4;
         int rc = set_smem((const void*)kern, smem);
         if (rc) return rc;
@@ -218,7 +236,7 @@ struct NormBackward {
         return check_launch("block norm backward");
     }
 };
-template <typename XT, typename BT, int V, int N> using NormBackwardPlain = NormBackward<XT, BT, V, N, false>;
+template <typename XT, typename BT, int W, int N> using NormBackwardPlain = NormBackward<XT, BT, W, N, false>;
 
 // ring rows: one or two vectors of eight per thread
 template <typename XT, typename BT, typename... A>
@@ -285,9 +303,10 @@ int coli_moe_dispatch(const void* x, coli_dtype xt, int32_t T, int32_t H, int32_
     if (!x || !inv || !xs) return fail(COLI_E_INVAL, "dispatch: NULL pointer");
     const int64_t bytes = (int64_t)H * type_size(xt);
     if (bytes % 16 == 0 && aligned(x, 16) && aligned(xs, 16))
-        return launch_dispatch<uint4>(x, T, (int)(bytes / 16), k, inv, xs, S(stream));
-    if (xt == COLI_F32) return launch_dispatch<uint32_t>(x, T, H, k, inv, xs, S(stream));
-    return launch_dispatch<uint16_t>(x, T, H, k, inv, xs, S(stream));
+        return launch_dispatch<uint4, 1>(x, T, (int)(bytes / 16), k, inv, xs, S(stream));
+    if (bytes % 4 == 0 && aligned(x, 4) && aligned(xs, 4))
+        return launch_dispatch<uint32_t, 4>(x, T, (int)(bytes / 4), k, inv, xs, S(stream));
+    return launch_dispatch<uint16_t, 8>(x, T, (int)(bytes / 2), k, inv, xs, S(stream));
 }
 
 int coli_moe_dispatch_backward(const void* dxs, coli_dtype xt, int32_t T, int32_t H, int32_t k,
@@ -335,12 +354,11 @@ int coli_moe_block_norm(const coli_norm_desc* desc, const void* x, const void* o
     if (!x || (o && !x_out) || (!o && !n_out)) return fail(COLI_E_INVAL, "block_norm: NULL pointer");
     if (o && (desc->gate_kind != COLI_GATE_NONE) != (gate != nullptr))
         return fail(COLI_E_INVAL, "block_norm: gate and gate_kind disagree");
-    const int xa = 8 * type_size(desc->xt), ba = 8 * type_size(desc->bt);
-    const bool wide = desc->H % 8 == 0 && aligned(x, xa) && aligned(x_out, xa) && aligned(o, ba) &&
-                      aligned(n_out, ba) && aligned(desc->post_gain, 32) && aligned(desc->pre_gain, 32) &&
-                      aligned(gate, 32);
+    const int xs = type_size(desc->xt), bs = type_size(desc->bt);
+    const int W = chunk_of<8>(desc->H, {{x, xs}, {x_out, xs}, {o, bs}, {n_out, bs}, {desc->post_gain, 4},
+                                        {desc->pre_gain, 4}, {gate, 4}});
     const NormArgs a = norm_args(*desc, gate, T);
-    return norm_dispatch<NormForward>(*desc, norm_shape(desc->H, T, wide, false), a, x, o, x_out, n_out, rstd_post, rstd_pre,
+    return norm_dispatch<NormForward>(*desc, norm_shape(desc->H, T, W, false), a, x, o, x_out, n_out, rstd_post, rstd_pre,
                                       S(stream));
 }
 
@@ -348,7 +366,7 @@ int coli_moe_block_norm_backward_workspace_size(const coli_norm_desc* desc, int3
     int rc = norm_ok("block_norm_backward_workspace_size", desc, T);
     if (rc) return rc;
     if (!bytes) return fail(COLI_E_INVAL, "block_norm_backward_workspace_size: NULL pointer");
-    const int grid = norm_backward_grid(T, std::max(kNormCtas, norm_ring_ctas(*desc, T)));  // of either form
+    const int grid = norm_backward_grid(T, std::max(norm_plain_ctas(*desc, T), norm_ring_ctas(*desc, T)));  // of either form
     *bytes = (size_t)(grid / norm_backward_cluster(grid)) * kNormSums * desc->H * 4;
     return COLI_OK;
 }
@@ -383,32 +401,34 @@ int coli_moe_block_norm_backward(const coli_norm_desc* desc, const void* x_out, 
     float* partial = static_cast<float*>(ws);
     int grid = 0;
     if (T > 0) {
-        const int xa = 8 * type_size(desc->xt), ba = 8 * type_size(desc->bt);
-        const bool wide = desc->H % 8 == 0 && aligned(x_out, xa) && aligned(dx_out, xa) && aligned(dx, xa) &&
-                          aligned(o, ba) && aligned(dn, ba) && aligned(d_o, ba) && aligned(desc->post_gain, 32) &&
-                          aligned(desc->pre_gain, 32) && aligned(gate, 32) && aligned(dgate, 32);
+        const int xs = type_size(desc->xt), bs = type_size(desc->bt);
+        const int W = chunk_of<8>(desc->H, {{x_out, xs}, {dx_out, xs}, {dx, xs}, {o, bs}, {dn, bs}, {d_o, bs},
+                                            {desc->post_gain, 4}, {desc->pre_gain, 4}, {gate, 4}, {dgate, 4}});
         const NormArgs a = norm_args(*desc, gate, T);
         const int ctas = norm_ring_ctas(*desc, T);
-        const NormRing ring = norm_ring(*desc, ctas, wide, dn != nullptr, dx_out != nullptr, o != nullptr, dn != nullptr);
-        grid = norm_backward_grid(T, ring.stages > 0 ? ctas : kNormCtas);
+        const NormRing ring = norm_ring(*desc, ctas, W == 8, dn != nullptr, dx_out != nullptr, o != nullptr, dn != nullptr);
+        grid = norm_backward_grid(T, ring.stages > 0 ? ctas : norm_plain_ctas(*desc, T));
         if (ring.stages > 0) {
             NormShape s;
-            s.V = 8;
+            s.W = 8;
             s.N = desc->H / 8 <= 768 ? 1 : 2;  // more warps hide more of each other's waits
             s.threads = ((desc->H / 8 + s.N - 1) / s.N + 31) / 32 * 32;
             rc = norm_ring_dispatch(*desc, s, a, keep, ring, x_out, o, rstd_post, rstd_pre, dx_out, dn, dx, d_o, dgate,
                                     partial, grid, S(stream));
         } else {
-            rc = norm_dispatch<NormBackwardPlain>(*desc, norm_shape(desc->H, T, wide, true), a, keep, ring, x_out, o,
+            rc = norm_dispatch<NormBackwardPlain>(*desc, norm_shape(desc->H, T, W, true), a, keep, ring, x_out, o,
                                                   rstd_post, rstd_pre, dx_out, dn, dx, d_o, dgate, partial, grid,
                                                   S(stream));
         }
         if (rc) return rc;
     }
     if (!keep.n) return COLI_OK;
-    return launch_pdl(norm_reduce_kernel, dim3((desc->H + 31) / 32, kNormSums), 256, 0, S(stream), "block norm sums",
-                      (const float*)partial, grid / norm_backward_cluster(grid), (int)desc->H, keep, dpost_gain, dgate,
-                      dpre_gain);
+    // few partial rows: small CTAs, many of them at once; many (short rows): more runs
+    const int rows = grid / norm_backward_cluster(grid);
+    const auto reduce = rows <= 128 ? norm_reduce_kernel<8> : norm_reduce_kernel<32>;
+    return launch_pdl(reduce, dim3((desc->H + 31) / 32, kNormSums), 32 * (rows <= 128 ? 8 : 32), 0, S(stream),
+                      "block norm sums", (const float*)partial, rows, (int)desc->H, keep, dpost_gain,
+                      channel ? dgate : nullptr, dpre_gain);
 }
 
 }  // extern "C"

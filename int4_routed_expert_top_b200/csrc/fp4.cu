@@ -122,18 +122,20 @@ int coli_moe_fp4_quantize(coli_fp4 fmt, const void* x, coli_dtype xt, int64_t n_
     a.src = src; a.count = count; a.gscale = gscale;
     a.codes = static_cast<uint8_t*>(codes);
     a.scales = static_cast<uint32_t*>(scales);
-    // a warp per chunk of a row, several rows where they are short
+    // a warp per chunk of a row, several rows to a CTA or a warp where they are short
+    const int lanes = K > 256 ? 32 : K > 128 ? 16 : 8;
     const int chunks = (K + kQuantCols - 1) / kQuantCols;
     const int parts = (chunks + kQuantWarps - 1) / kQuantWarps, warps = (chunks + parts - 1) / parts;
     const int rows_per = std::max(1, 8 / warps);
-    const dim3 grid((unsigned)((rows + rows_per - 1) / rows_per), parts);
+    const int cta_rows = rows_per * (32 / lanes);
+    const dim3 grid((unsigned)((rows + cta_rows - 1) / cta_rows), parts);
     const int threads = 32 * warps * rows_per;
     if (xt == COLI_F32)
         return launch_pdl(fmt == COLI_NVFP4 ? fp4_quantize_kernel<float, true> : fp4_quantize_kernel<float, false>, grid,
-                          threads, 0, S(stream), "fp4 quantize", a, warps, rows_per, (const float*)x, (float*)values);
+                          threads, 0, S(stream), "fp4 quantize", a, warps, rows_per, lanes, (const float*)x, (float*)values);
     return launch_pdl(fmt == COLI_NVFP4 ? fp4_quantize_kernel<__nv_bfloat16, true>
                                         : fp4_quantize_kernel<__nv_bfloat16, false>,
-                      grid, threads, 0, S(stream), "fp4 quantize", a, warps, rows_per, (const __nv_bfloat16*)x,
+                      grid, threads, 0, S(stream), "fp4 quantize", a, warps, rows_per, lanes, (const __nv_bfloat16*)x,
                       (__nv_bfloat16*)values);
 }
 

@@ -94,23 +94,27 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 // A lane holds 16 columns of a row (two or four loads of 16 or 32 bytes), a warp
 // 512: a block is one lane (NVFP4) or two, so its maximum takes at most one
 // shuffle.  Every warp of a CTA has one chunk of one of its rows: that hides the
-// loads better than a warp's loop over its row does.  Bound by HBM (x once, codes, scales and
+// loads better than a warp's loop over its row does.  Rows of 256 columns or
+// fewer share a warp (`lanes` to a row: 8, 16 or 32; a scale word is 4 or 8).  Bound by HBM (x once, codes, scales and
 // values once).
 constexpr int kQuantCols = 512;
 constexpr int kQuantWarps = 16;  // of a CTA, at most
 
 template <typename T, bool NV>
 __global__ void __launch_bounds__(32 * kQuantWarps)
-fp4_quantize_kernel(Fp4QuantArgs a, int warps, int rows_per, const T* __restrict__ x, T* __restrict__ values) {
+fp4_quantize_kernel(Fp4QuantArgs a, int warps, int rows_per, int lanes, const T* __restrict__ x,
+                    T* __restrict__ values) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mine = warp / warps;
-    const int64_t r = (int64_t)blockIdx.x * rows_per + mine;
+    // rows_per rows of a warp each (or of `warps` warps), or 32 / lanes rows to a warp
+    const int64_t r = ((int64_t)blockIdx.x * rows_per + mine) * (32 / lanes) + lane / lanes;
     const int c0 = ((int)blockIdx.y * warps + warp - mine * warps) * kQuantCols;
-    const int c = c0 + lane * 16;
+    const int c = c0 + (lane & (lanes - 1)) * 16;
     pdl_trigger();
     pdl_wait();
-    if (r >= a.rows || c0 >= a.K || (a.count && r >= *a.count)) return;
-    const bool in = c < a.K;  // K is a multiple of 32: all 16 columns or none
-    const int64_t from = a.src ? a.src[r] : r;
+    const int64_t rows = a.count ? min(a.rows, (int64_t)*a.count) : a.rows;
+    if (c0 >= a.K || r - lane / lanes >= rows) return;        // the whole warp
+    const bool live = r < rows, in = live && c < a.K;  // K is a multiple of 32: all 16 columns or none
+    const int64_t from = !live ? 0 : a.src ? a.src[r] : r;
     const float g = NV && a.gscale ? *a.gscale : 1.0f;
     float v[16];
 #pragma unroll
@@ -164,7 +168,7 @@ fp4_quantize_kernel(Fp4QuantArgs a, int warps, int rows_per, const T* __restrict
     word |= __shfl_xor_sync(0xffffffffu, word, per);
     word |= __shfl_xor_sync(0xffffffffu, word, 2 * per);
     const int at = c / (64 * per);
-    if ((lane & (4 * per - 1)) == 0 && at < a.words) a.scales[scale_word(r, at, a.words)] = word;
+    if (live && (lane & (4 * per - 1)) == 0 && at < a.words) a.scales[scale_word(r, at, a.words)] = word;
     if (!in) return;
     *reinterpret_cast<uint2*>(a.codes + (r * a.K + c) / 2) = make_uint2(code[0], code[1]);
     if (values) {
@@ -192,7 +196,6 @@ fp4_quantize_kernel(Fp4QuantArgs a, int warps, int rows_per, const T* __restrict
 constexpr int kFpScaleWarps = 4;
 constexpr int kFpStoreWarps = 8;   // at most
 constexpr int kFpMaxE = 1024;
-constexpr int kFpMinUnits = 2;     // stages per CTA at least, before fewer CTAs take part
 constexpr int kFpMaxGrid = 160;    // B200 has 148 SMs; the workspace is sized for this many
 // the workspace: error flags, a flag per CTA and store warp, then partial sums
 constexpr int kFpFlagBytes = 256;
@@ -207,6 +210,9 @@ struct FpShape {
     static constexpr int ctas = PAIR ? 2 : 1;
     static constexpr int rows = NT / ctas;                   // of X in a CTA's shared memory
     static constexpr int box = PAIR ? rows / 2 : rows;       // rows per TMA box of X
+    // stages that a cut tile's pieces have at least: fewer cost less time than joining them
+    // (one tile of 24 stages: MIN_UNITS)
+    static constexpr int min_units = PAIR ? 8 : 4;
     static constexpr int store_warps = NT > 32 ? kFpStoreWarps : 4;
     static constexpr int groups = store_warps / 4;           // warps to a quarter of the lanes
     static constexpr int threads = 32 * (6 + store_warps);
@@ -300,18 +306,20 @@ __device__ __forceinline__ void fp_plan(const FpArgs& a, FpPlan& p) {
 }
 
 // The share of every CTA (or pair): tiles c, c + G, .. of the first waves * G, and
-// units [lo(c), lo(c + 1)) of the tiles from tile0 on.  As many of them share those
-// as get kFpMinUnits each, so that no run between two others is empty: whoever
-// begins a tile waits for every CTA up to the tile's end.
+// units [lo(c), lo(c + 1)) of the tiles from tile0 on.  As many CTAs share those as
+// get min_units each, or one tile each where that is more, so that no run between
+// two others is empty: whoever begins a tile waits for every CTA up to the tile's
+// end.
 struct FpRun {
     int64_t G, waves, tile0, U, sharers;
-    __device__ __forceinline__ FpRun(const FpArgs& a, const FpPlan& p, int grid) {  // grid: CTAs, or pairs
+    __device__ __forceinline__ FpRun(const FpArgs& a, const FpPlan& p, int grid, int min_units) {  // grid: CTAs, or pairs
         const int64_t tiles = p.tile0[a.E];
-        G = min((int64_t)grid, max((int64_t)1, tiles * a.KS / kFpMinUnits));
+        G = min((int64_t)grid, max(tiles, tiles * a.KS / min_units));
+        G = max(G, (int64_t)1);
         waves = tiles / G;
         tile0 = waves * G;
         U = (tiles - tile0) * a.KS;
-        sharers = min(G, max((int64_t)1, U / kFpMinUnits));
+        sharers = max(min(G, max(tiles - tile0, U / min_units)), (int64_t)1);
     }
     __device__ __forceinline__ int64_t lo(int64_t c) const { return c >= sharers ? U : U * c / sharers; }
 };
@@ -511,18 +519,21 @@ struct Ring {
     }
 };
 
-// Warp-wide wait for a flag of another CTA's store warp: some ten seconds at most,
-// since that CTA may have to wait for an SM that another stream's kernel holds
-__device__ __forceinline__ bool fp_wait_flag(const uint64_t* flag, int32_t* err) {
-    int ok = 1;
-    if ((threadIdx.x & 31) == 0) {
+// Warp-wide wait for the flags of `parts` CTAs' store warps, `step` flags apart, a
+// lane each: some ten seconds at most, since those CTAs may have to wait for an SM
+// that another stream's kernel holds
+__device__ __forceinline__ bool fp_wait_flags(const uint64_t* flags, int64_t step, int64_t parts, int32_t* err) {
+    bool ok = true;
+    for (int64_t c = threadIdx.x & 31; c < parts; c += 32) {
         uint64_t v = 0;
         for (int i = 0; i < (1 << 25) && v != kFpRaised; ++i)
-            asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(flag) : "memory");
-        ok = v == kFpRaised;
-        if (!ok) atomicOr(err, kErrWaitTimeout);
+            asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(flags + c * step) : "memory");
+        if (v != kFpRaised) {
+            atomicOr(err, kErrWaitTimeout);
+            ok = false;
+        }
     }
-    return __shfl_sync(0xffffffffu, ok, 0) != 0;
+    return __all_sync(0xffffffffu, ok);
 }
 
 template <int NT, bool NV, bool PAIR, typename YT>
@@ -566,7 +577,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     if (PAIR) cluster_sync();  // the other CTA's barriers are set up
     tc_fence_after();
     const uint32_t tmem = uniform(tmem_slot);
-    const FpRun run(a, plan, gridDim.x / C::ctas);
+    const FpRun run(a, plan, gridDim.x / C::ctas, C::min_units);
     FpPieces q(a, run, unit);
     bool ok = true;  // cleared by a wait that gave up: then no further waits
 
@@ -741,22 +752,23 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             const int row = t.rt * C::M + 128 * rank + 32 * quarter + lane;
             const bool begins = uniform((int)(q.k0 == 0));
             const float al = begins && a.alpha ? a.alpha[t.e] : 1.0f;
-            float* part = a.partial + 32 * quarter + lane;
             // the CTAs (or pairs) after this one with pieces of the tile: up to the first whose
             // run starts at its end or later; of a pair, the CTA with the same weight rows
-            const auto slot = [&](int64_t c) { return c * C::ctas + rank; };
-            int64_t last = unit + 1;
+            int64_t parts = 0;
             if (begins && q.k1 < a.KS)
-                while (run.lo(last) < (q.tile + 1 - run.tile0) * a.KS) ++last;
+                while (run.lo(unit + 1 + parts) < (q.tile + 1 - run.tile0) * a.KS) ++parts;
+            parts = uniform(parts);
+            const int64_t other = (int64_t)blockIdx.x + C::ctas;  // the first of them
+            uint64_t* flags = a.flags + kFpStoreWarps * other + flag;
+            const float* theirs = a.partial + other * (128 * NT) + 16 * half * 128 + 32 * quarter + lane;
             if (ok && !mbar_wait(&accfull[buf], (piece >> 1) & 1, a.err)) ok = false;
             tc_fence_after();
-            for (int64_t c = unit + 1; c < last; ++c)
-                if (ok && !fp_wait_flag(a.flags + kFpStoreWarps * slot(c) + flag, a.err)) ok = false;
+            if (parts && ok && !fp_wait_flags(flags, kFpStoreWarps * C::ctas, parts, a.err)) ok = false;
             const uint32_t d = tmem + ((uint32_t)(32 * quarter) << 16) + NT * buf;
             YT* yp = y + (t.p0 + 16 * half) * a.R + row;  // this lane's row of y's columns
-            float* pp = part + (int64_t)blockIdx.x * (128 * NT) + 16 * half * 128;
+            float* pp = a.partial + (int64_t)blockIdx.x * (128 * NT) + 16 * half * 128 + 32 * quarter + lane;
 #pragma unroll 1
-            for (int c0 = 16 * half; c0 < n; c0 += 16 * C::groups, yp += 16 * C::groups * (int64_t)a.R, pp += 16 * C::groups * 128) {
+            for (int c0 = 16 * half; c0 < n; c0 += 16 * C::groups) {
                 uint32_t v[16];
                 tmem_ld_32x32b_x16(d + c0, v);
                 tmem_wait_ld();
@@ -765,34 +777,45 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
 #pragma unroll
                     for (int i = 0; i < 16; ++i)
                         if (i < m) pp[i * 128] = __uint_as_float(v[i]);
-                    continue;
                 }
-                for (int64_t c = unit + 1; c < last; ++c)
+                // pieces in the order of their columns, the loads of some at a time in flight
+                constexpr int at_once = PAIR ? 2 : 4;
+#pragma unroll 1
+                for (int64_t c = 0; c < parts; c += at_once) {
+                    float p[at_once][16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (i < m)
-                            v[i] = __float_as_uint(__uint_as_float(v[i]) + __ldcg(part + slot(c) * (128 * NT) + (c0 + i) * 128));
-                if (row >= a.R) continue;
-                if (m >= 16) {
+                    for (int u = 0; u < at_once; ++u)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) yp[i * (int64_t)a.R] = from_f32<YT>(__uint_as_float(v[i]) * al);
-                } else {
+                        for (int i = 0; i < 16; ++i)
+                            if (c + u < parts && i < m) p[u][i] = __ldcg(theirs + (c + u) * (C::ctas * 128 * NT) + i * 128);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        if (i < m) yp[i * (int64_t)a.R] = from_f32<YT>(__uint_as_float(v[i]) * al);
+                    for (int u = 0; u < at_once; ++u)
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (c + u < parts && i < m) v[i] = __float_as_uint(__uint_as_float(v[i]) + p[u][i]);
                 }
+                if (begins && row < a.R) {
+                    if (m >= 16) {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) yp[i * (int64_t)a.R] = from_f32<YT>(__uint_as_float(v[i]) * al);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; ++i)
+                            if (i < m) yp[i * (int64_t)a.R] = from_f32<YT>(__uint_as_float(v[i]) * al);
+                    }
+                }
+                yp += 16 * C::groups * (int64_t)a.R;
+                pp += 16 * C::groups * 128;
+                theirs += 16 * C::groups * 128;
             }
             __syncwarp();
-            if (!begins) {
-                if (lane == 0) {
-                    __threadfence();
-                    asm volatile("st.release.gpu.global.u64 [%0], %1;"
-                                 ::"l"(a.flags + kFpStoreWarps * (int64_t)blockIdx.x + flag), "l"(kFpRaised) : "memory");
-                }
-            } else {
-                for (int64_t c = unit + 1; c < last; ++c)  // read once: down again for the next call
-                    if (lane == 0) a.flags[kFpStoreWarps * slot(c) + flag] = 0;
+            if (!begins && lane == 0) {
+                __threadfence();
+                asm volatile("st.release.gpu.global.u64 [%0], %1;"
+                             ::"l"(a.flags + kFpStoreWarps * (int64_t)blockIdx.x + flag), "l"(kFpRaised) : "memory");
             }
+            for (int64_t c = lane; c < parts; c += 32)  // read once: down again for the next call
+                flags[c * (kFpStoreWarps * C::ctas)] = 0;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {

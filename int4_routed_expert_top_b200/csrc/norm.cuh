@@ -7,8 +7,8 @@
 // and keeps it in registers, in the types it was read in, between the two sums
 // over the row, so nothing is read twice; 64 registers a thread let an SM hold
 // several rows (over 100 KB of loads) while others wait at their sums.  Rows are
-// cut into vectors of eight elements (single elements where H or a pointer
-// allows no more), N of them per thread; few tokens take N = 1, which spreads a
+// cut into vectors of eight elements (chunks of W = 2 or 1 neighbours where H or a
+// pointer allows no more, see Cols), N of them per thread; few tokens take N = 1, which spreads a
 // row over more threads and asks for the gains before the first sum.
 //
 // Backward, with xh = x' r_x, oh = o r_o, v = pre_gain dn, <.> the mean over H:
@@ -44,28 +44,41 @@ struct NormArgs {
     const float* gate;
 };
 
-template <int V>
-__device__ __forceinline__ F<V> ones() {
-    F<V> r;
+template <int N>
+__device__ __forceinline__ F<N> ones() {
+    F<N> r;
 #pragma unroll
-    for (int j = 0; j < V; ++j) r.v[j] = 1.0f;
+    for (int j = 0; j < N; ++j) r.v[j] = 1.0f;
     return r;
 }
-template <int V>
-__device__ __forceinline__ F<V> gain_at(const float* g, int c) {
-    return g ? ldf<float, V>(g + c) : ones<V>();
+// this thread's part of vector i of a row: first column, and what lies between its chunks
+template <int W> struct Part {
+    int c, stride;
+    __device__ __forceinline__ Part(int c0, int step, int i) : c(c0 + i * step), stride(step / 8 * W) {}
+};
+template <typename T, int W>
+__device__ __forceinline__ Cols<T, 8, W> ld_part(const T* row, const Part<W>& p, int H) {
+    return ldc<T, 8, W>(row, p.c, p.stride, H);
+}
+template <typename T, int W>
+__device__ __forceinline__ void st_part(T* row, const Part<W>& p, int H, const F<8>& f) {
+    stc<T, 8, W>(row, p.c, p.stride, H, narrow_cols<T, 8, W>(f));
+}
+template <int W>
+__device__ __forceinline__ F<8> gain_at(const float* g, const Part<W>& p, int H) {
+    return g ? widen<float, 8, W>(ld_part<float, W>(g, p, H)) : ones<8>();
 }
 
-// gate of token t, columns c .. c + V - 1
-template <int V>
-__device__ __forceinline__ F<V> gate_at(const NormArgs& a, int64_t t, int c) {
-    if (a.gate_kind == 1) return ldf<float, V>(a.gate + c);
-    if (a.gate_kind == 3) return ldf<float, V>(a.gate + t * a.H + c);
-    F<V> r = ones<V>();
+// gate of token t at this part
+template <int W>
+__device__ __forceinline__ F<8> gate_at(const NormArgs& a, int64_t t, const Part<W>& p) {
+    if (a.gate_kind == 1) return gain_at<W>(a.gate, p, a.H);
+    if (a.gate_kind == 3) return gain_at<W>(a.gate + t * a.H, p, a.H);
+    F<8> r = ones<8>();
     if (a.gate_kind == 2) {
         const float g = a.gate[t];
 #pragma unroll
-        for (int j = 0; j < V; ++j) r.v[j] = g;
+        for (int j = 0; j < 8; ++j) r.v[j] = g;
     }
     return r;
 }
@@ -87,32 +100,32 @@ __device__ __forceinline__ void cta_sum(float (&s)[K], float* part) {
 
 constexpr int norm_max_threads(int N) { return N == 1 ? 1024 : 512; }
 
-template <typename XT, typename BT, int V, int N>
-__global__ void __launch_bounds__(norm_max_threads(N), N == 2 || N == 3 ? 2 : 1)
+template <typename XT, typename BT, int W, int N>
+__global__ void __launch_bounds__(norm_max_threads(N), W == 8 && (N == 2 || N == 3) ? 2 : 1)
 block_norm_kernel(NormArgs a, const XT* x, const BT* o, XT* x_out, BT* n_out, float* rstd_post,
                   float* rstd_pre) {
     __shared__ float part[2][32];
     const int64_t t = blockIdx.x;
     const int64_t row = t * a.H;
-    const int step = (int)blockDim.x * V, c0 = (int)threadIdx.x * V;
+    const int step = (int)blockDim.x * 8, c0 = (int)threadIdx.x * W;
     pdl_trigger();
     pdl_wait();
-    Vec<XT, V> xv[N];
-    Vec<BT, V> ov[N];
+    Cols<XT, 8, W> xv[N];
+    Cols<BT, 8, W> ov[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int c = c0 + i * step;
-        if (c >= a.H) continue;
-        if (o) ov[i] = ldv<BT, V>(o + row + c);
-        xv[i] = ldv<XT, V>(x + row + c);
+        const Part<W> p(c0, step, i);
+        if (o) ov[i] = ld_part<BT, W>(o + row, p, a.H);
+        xv[i] = ld_part<XT, W>(x + row, p, a.H);
     }
-    F<V> early_post, early_gate, early_pre;  // N == 1: asked for before the sums
-    if (N == 1 && c0 < a.H) {
+    F<8> early_post, early_gate, early_pre;  // N == 1: asked for before the sums
+    if (N == 1) {
+        const Part<W> p(c0, step, 0);
         if (o) {
-            early_gate = gate_at<V>(a, t, c0);
-            if (a.post_norm) early_post = gain_at<V>(a.post_gain, c0);
+            early_gate = gate_at<W>(a, t, p);
+            if (a.post_norm) early_post = gain_at<W>(a.post_gain, p, a.H);
         }
-        if (n_out) early_pre = gain_at<V>(a.pre_gain, c0);
+        if (n_out) early_pre = gain_at<W>(a.pre_gain, p, a.H);
     }
     float s[1] = {0.0f};
     if (o) {
@@ -120,10 +133,9 @@ block_norm_kernel(NormArgs a, const XT* x, const BT* o, XT* x_out, BT* n_out, fl
         if (a.post_norm) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                if (c0 + i * step >= a.H) continue;
-                const F<V> f = widen<BT, V>(ov[i]);
+                const F<8> f = widen<BT, 8, W>(ov[i]);
 #pragma unroll
-                for (int j = 0; j < V; ++j) s[0] = fmaf(f.v[j], f.v[j], s[0]);
+                for (int j = 0; j < 8; ++j) s[0] = fmaf(f.v[j], f.v[j], s[0]);
             }
             cta_sum(s, part[0]);
             r = 1.0f / sqrtf(s[0] / (float)a.H + a.eps);
@@ -131,68 +143,72 @@ block_norm_kernel(NormArgs a, const XT* x, const BT* o, XT* x_out, BT* n_out, fl
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int c = c0 + i * step;
-            if (c >= a.H) continue;
-            const F<V> g = N == 1 ? early_gate : gate_at<V>(a, t, c);
-            F<V> f = widen<BT, V>(ov[i]);
+            const Part<W> p(c0, step, i);
+            const F<8> g = N == 1 ? early_gate : gate_at<W>(a, t, p);
+            F<8> f = widen<BT, 8, W>(ov[i]);
             if (a.post_norm) {
-                const F<V> pg = N == 1 ? early_post : gain_at<V>(a.post_gain, c);
+                const F<8> pg = N == 1 ? early_post : gain_at<W>(a.post_gain, p, a.H);
 #pragma unroll
-                for (int j = 0; j < V; ++j) f.v[j] = f.v[j] * r * pg.v[j];
+                for (int j = 0; j < 8; ++j) f.v[j] = f.v[j] * r * pg.v[j];
             }
-            const F<V> xf = widen<XT, V>(xv[i]);
+            const F<8> xf = widen<XT, 8, W>(xv[i]);
 #pragma unroll
-            for (int j = 0; j < V; ++j) f.v[j] = fmaf(a.alpha * g.v[j], f.v[j], xf.v[j]);
-            xv[i] = narrow<XT, V>(f);  // the stored value, which the norm below reads
-            stv<XT, V>(x_out + row + c, xv[i]);
+            for (int j = 0; j < 8; ++j) f.v[j] = fmaf(a.alpha * g.v[j], f.v[j], xf.v[j]);
+            xv[i] = narrow_cols<XT, 8, W>(f);  // the stored value, which the norm below reads
+            stc<XT, 8, W>(x_out + row, p.c, p.stride, a.H, xv[i]);
         }
     }
     if (!n_out) return;
     s[0] = 0.0f;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        if (c0 + i * step >= a.H) continue;
-        const F<V> f = widen<XT, V>(xv[i]);
+        const Part<W> p(c0, step, i);
+        const F<8> f = widen<XT, 8, W>(xv[i]);
 #pragma unroll
-        for (int j = 0; j < V; ++j) s[0] = fmaf(f.v[j], f.v[j], s[0]);
+        for (int j = 0; j < 8; ++j)
+            if (p.c + j / W * p.stride < a.H) s[0] = fmaf(f.v[j], f.v[j], s[0]);
     }
     cta_sum(s, part[1]);
     const float r = 1.0f / sqrtf(s[0] / (float)a.H + a.eps);
     if (rstd_pre && threadIdx.x == 0) rstd_pre[t] = r;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int c = c0 + i * step;
-        if (c >= a.H) continue;
-        const F<V> pg = N == 1 ? early_pre : gain_at<V>(a.pre_gain, c);
-        F<V> f = widen<XT, V>(xv[i]);
+        const Part<W> p(c0, step, i);
+        const F<8> pg = N == 1 ? early_pre : gain_at<W>(a.pre_gain, p, a.H);
+        F<8> f = widen<XT, 8, W>(xv[i]);
 #pragma unroll
-        for (int j = 0; j < V; ++j) f.v[j] = f.v[j] * r * pg.v[j];
-        stf<BT, V>(n_out + row + c, f);
+        for (int j = 0; j < 8; ++j) f.v[j] = f.v[j] * r * pg.v[j];
+        st_part<BT, W>(n_out + row, p, a.H, f);
     }
 }
 
-// Sums of this CTA in shared memory, kept so that a warp's 16-byte accesses meet
-// no bank twice: for vectors of eight, the first four elements of all vectors,
-// then the last four.
-template <int V>
+// Sums of this CTA in shared memory, kept so that a warp's accesses meet no bank
+// twice: for vectors of eight neighbours, the first four elements of all vectors, then
+// the last four; else in the order of their columns.
+template <int W>
 __device__ __forceinline__ int sum_at(int c, int H) {  // column c of one sum
-    return V == 8 ? (((c >> 2) & 1) * (H >> 3) + (c >> 3)) * 4 + (c & 3) : c;
+    return W == 8 ? (((c >> 2) & 1) * (H >> 3) + (c >> 3)) * 4 + (c & 3) : c;
 }
-template <int V>
-__device__ __forceinline__ void sum_add(float* sums, int c, int H, const F<V>& f, const F<V>& g) {
-    if constexpr (V == 8) {
+template <int W>
+__device__ __forceinline__ void sum_add(float* sums, const Part<W>& p, int H, const F<8>& f, const F<8>& g) {
+    if constexpr (W == 8) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            float4* p = reinterpret_cast<float4*>(sums + sum_at<V>(c + 4 * h, H));
-            float4 v = *p;
+            if (p.c >= H) break;
+            float4* at = reinterpret_cast<float4*>(sums + sum_at<W>(p.c + 4 * h, H));
+            float4 v = *at;
             v.x = fmaf(f.v[4 * h], g.v[4 * h], v.x);
             v.y = fmaf(f.v[4 * h + 1], g.v[4 * h + 1], v.y);
             v.z = fmaf(f.v[4 * h + 2], g.v[4 * h + 2], v.z);
             v.w = fmaf(f.v[4 * h + 3], g.v[4 * h + 3], v.w);
-            *p = v;
+            *at = v;
         }
     } else {
-        sums[c] = fmaf(f.v[0], g.v[0], sums[c]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int c = p.c + j / W * p.stride + j % W;
+            if (c < H) sums[c] = fmaf(f.v[j], g.v[j], sums[c]);
+        }
     }
 }
 
@@ -215,11 +231,10 @@ struct NormRing {
 };
 constexpr int kNormMaxStages = 4;
 
-// N elements of a row in shared memory (V = 8) as they lie there
-template <typename T, int V>
-__device__ __forceinline__ Vec<T, V> lds_row(const uint8_t* row, int c) {
-    Vec<T, V> r;
-    static_assert(r.bytes >= 16, "vectors of eight");
+// eight elements of a row in shared memory as they lie there
+template <typename T>
+__device__ __forceinline__ Vec<T, 8> lds_row(const uint8_t* row, int c) {
+    Vec<T, 8> r;
 #pragma unroll
     for (int i = 0; i < r.bytes / 16; ++i) {
         const uint4 v = *reinterpret_cast<const uint4*>(row + c * (int)sizeof(T) + 16 * i);
@@ -228,15 +243,14 @@ __device__ __forceinline__ Vec<T, V> lds_row(const uint8_t* row, int c) {
     return r;
 }
 
-// V elements from column c of a vector kept in sum_at's order, 1 where there is none
-template <int V>
-__device__ __forceinline__ F<V> lds_gain(const uint8_t* smem, int off, int c, int H) {
-    F<V> r = ones<V>();
+// eight elements from column c of a vector kept in sum_at's order, 1 where there is none
+__device__ __forceinline__ F<8> lds_gain(const uint8_t* smem, int off, int c, int H) {
+    F<8> r = ones<8>();
     if (off >= 0) {
         const float* p = reinterpret_cast<const float*>(smem + off);
 #pragma unroll
-        for (int h = 0; h < V / 4; ++h) {
-            const float4 v = *reinterpret_cast<const float4*>(p + sum_at<V>(c + 4 * h, H));
+        for (int h = 0; h < 2; ++h) {
+            const float4 v = *reinterpret_cast<const float4*>(p + sum_at<8>(c + 4 * h, H));
             r.v[4 * h] = v.x; r.v[4 * h + 1] = v.y; r.v[4 * h + 2] = v.z; r.v[4 * h + 3] = v.w;
         }
     }
@@ -244,7 +258,7 @@ __device__ __forceinline__ F<V> lds_gain(const uint8_t* smem, int off, int c, in
 }
 
 // partial [clusters][sums.n][H]
-template <typename XT, typename BT, int V, int N, bool RING>
+template <typename XT, typename BT, int W, int N, bool RING>
 __global__ void __launch_bounds__(RING && N == 1 ? 768 : 512)
 block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x_out, const BT* o,
                            const float* rstd_post, const float* rstd_pre, const XT* dx_out, const BT* dn, XT* dx,
@@ -252,21 +266,23 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
     extern __shared__ __align__(128) uint8_t nb_smem[];   // the ring, or the sums; at the end the sums
     __shared__ float part[2][64];
     __shared__ __align__(8) uint64_t full[kNormMaxStages];
+    __shared__ float rstds[kNormMaxStages][2];
     float* sums = reinterpret_cast<float*>(nb_smem);
-    const int step = (int)blockDim.x * V, c0 = (int)threadIdx.x * V;
+    static_assert(!RING || W == 8, "rows of the ring are read in vectors of eight");
+    const int step = (int)blockDim.x * 8, c0 = (int)threadIdx.x * W;
     float* s_of[kNormSums];
 #pragma unroll
     for (int i = 0; i < kNormSums; ++i) s_of[i] = keep.at[i] >= 0 ? sums + keep.at[i] * a.H : nullptr;
-    F<V> acc[RING ? kNormSums : 1][RING ? N : 1];
+    F<8> acc[RING ? kNormSums : 1][RING ? N : 1];
     if (RING) {
 #pragma unroll
         for (int k = 0; k < kNormSums; ++k)
 #pragma unroll
             for (int i = 0; i < N; ++i)
 #pragma unroll
-                for (int j = 0; j < V; ++j) acc[RING ? k : 0][RING ? i : 0].v[j] = 0.0f;
+                for (int j = 0; j < 8; ++j) acc[RING ? k : 0][RING ? i : 0].v[j] = 0.0f;
         if (threadIdx.x == 0) {
-            for (int i = 0; i < ring.stages; ++i) mbar_init(&full[i], 1);
+            for (int i = 0; i < ring.stages; ++i) mbar_init(&full[i], 2);  // the rows, the two rstd
             fence_mbar_init();
         }
     } else {
@@ -274,14 +290,14 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
     }
     __syncthreads();
     // sum k += f * h
-    const auto add = [&](int k, int i, int c, const F<V>& f, const F<V>& h) {
+    const auto add = [&](int k, int i, const Part<W>& p, const F<8>& f, const F<8>& h) {
         if (!s_of[k]) return;
         if (RING) {
-            F<V>& s = acc[RING ? k : 0][RING ? i : 0];
+            F<8>& s = acc[RING ? k : 0][RING ? i : 0];
 #pragma unroll
-            for (int j = 0; j < V; ++j) s.v[j] = fmaf(f.v[j], h.v[j], s.v[j]);
+            for (int j = 0; j < 8; ++j) s.v[j] = fmaf(f.v[j], h.v[j], s.v[j]);
         } else {
-            sum_add<V>(s_of[k], c, a.H, f, h);
+            sum_add<W>(s_of[k], p, a.H, f, h);
         }
     };
     const float inv_h = 1.0f / (float)a.H;
@@ -296,15 +312,12 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
         if (ring.off[1] >= 0) bulk_g2s(st + ring.off[1], dx_out + t * a.H, xb, &full[at]);
         if (ring.off[2] >= 0) bulk_g2s(st + ring.off[2], o + t * a.H, bb, &full[at]);
         if (ring.off[3] >= 0) bulk_g2s(st + ring.off[3], dn + t * a.H, bb, &full[at]);
+        if (dn) cp_async4(smem_u32(&rstds[at][0]), rstd_pre + t);
+        if (o && a.post_norm) cp_async4(smem_u32(&rstds[at][1]), rstd_post + t);
+        cp_async_arrive(&full[at]);
     };
     pdl_trigger();
     pdl_wait();
-    float rx = 0.0f, ro = 1.0f;  // of the next row
-    const auto rstd = [&](int64_t t) {
-        if (t >= a.T) return;
-        if (dn) rx = rstd_pre[t];
-        if (o && a.post_norm) ro = rstd_post[t];
-    };
     if (RING) {
         if (threadIdx.x == 0)
             for (int i = 0; i < ring.stages; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
@@ -313,67 +326,67 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
         for (int k = 0; k < 3; ++k)
             if (ring.gain[k] >= 0)
                 for (int c = threadIdx.x; c < a.H; c += blockDim.x)
-                    reinterpret_cast<float*>(nb_smem + ring.gain[k])[sum_at<V>(c, a.H)] = from[k][c];
+                    reinterpret_cast<float*>(nb_smem + ring.gain[k])[sum_at<W>(c, a.H)] = from[k][c];
         __syncthreads();
     }
-    rstd(blockIdx.x);
     int at = 0;
     uint32_t phase = 0;
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
         const int64_t row = t * a.H;
-        F<V> d[N];
-        Vec<XT, V> xv[N];
-        Vec<BT, V> ov[N], gv[N];
+        F<8> d[N];
+        Cols<XT, 8, W> xv[N];
+        Cols<BT, 8, W> ov[N], gv[N];
         float s1[1] = {0.0f};
-        const float rx_t = rx, ro_t = ro;
-        rstd(t + gridDim.x);
+        float rx_t = 0.0f, ro_t = 1.0f;
         const uint8_t* st = nb_smem + ring.first + at * ring.stage;
         // a copy that never lands (a wait of seconds) makes the row NaN
         bool landed = true;
         if (RING) landed = mbar_wait(&full[at], phase, nullptr);
+        if (dn) rx_t = RING ? rstds[at][0] : rstd_pre[t];
+        if (o && a.post_norm) ro_t = RING ? rstds[at][1] : rstd_post[t];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int c = c0 + i * step;
-            if (c >= a.H) continue;
+            const Part<W> p(c0, step, i);
+            if (p.c >= a.H) continue;
             if constexpr (RING) {
                 if (dn) {
-                    xv[i] = lds_row<XT, V>(st + ring.off[0], c);
-                    gv[i] = lds_row<BT, V>(st + ring.off[3], c);
+                    xv[i].q[0] = lds_row<XT>(st + ring.off[0], p.c);
+                    gv[i].q[0] = lds_row<BT>(st + ring.off[3], p.c);
                 }
-                if (dx_out) d[i] = widen<XT, V>(lds_row<XT, V>(st + ring.off[1], c));
-                if (o) ov[i] = lds_row<BT, V>(st + ring.off[2], c);
+                if (dx_out) d[i] = widen<XT, 8>(lds_row<XT>(st + ring.off[1], p.c));
+                if (o) ov[i].q[0] = lds_row<BT>(st + ring.off[2], p.c);
             } else {
                 if (dn) {
-                    xv[i] = ldv<XT, V>(x_out + row + c);
-                    gv[i] = ldv<BT, V>(dn + row + c);
+                    xv[i] = ld_part<XT, W>(x_out + row, p, a.H);
+                    gv[i] = ld_part<BT, W>(dn + row, p, a.H);
                 }
-                if (dx_out) d[i] = ldf<XT, V>(dx_out + row + c);
-                if (o) ov[i] = ldv<BT, V>(o + row + c);
+                if (dx_out) d[i] = widen<XT, 8, W>(ld_part<XT, W>(dx_out + row, p, a.H));
+                if (o) ov[i] = ld_part<BT, W>(o + row, p, a.H);
             }
             if (!dx_out) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) d[i].v[j] = 0.0f;
+                for (int j = 0; j < 8; ++j) d[i].v[j] = 0.0f;
             }
             if (!landed) d[i].v[0] = __uint_as_float(0x7fc00000u);
         }
         if (dn) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int c = c0 + i * step;
-                if (c >= a.H) continue;
-                F<V> pg;
-                if constexpr (RING) pg = lds_gain<V>(nb_smem, ring.gain[0], c, a.H);
-                else pg = gain_at<V>(a.pre_gain, c);
-                const F<V> xf = widen<XT, V>(xv[i]), gf = widen<BT, V>(gv[i]);
-                F<V> xh;
+                const Part<W> p(c0, step, i);
+                if (p.c >= a.H) continue;
+                F<8> pg;
+                if constexpr (RING) pg = lds_gain(nb_smem, ring.gain[0], p.c, a.H);
+                else pg = gain_at<W>(a.pre_gain, p, a.H);
+                const F<8> xf = widen<XT, 8, W>(xv[i]), gf = widen<BT, 8, W>(gv[i]);
+                F<8> xh;
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
+                for (int j = 0; j < 8; ++j) {
                     xh.v[j] = xf.v[j] * rx_t;
                     const float v = gf.v[j] * pg.v[j];
                     s1[0] = fmaf(v, xh.v[j], s1[0]);
                     d[i].v[j] = fmaf(rx_t, v, d[i].v[j]);
                 }
-                add(2, i, c, gf, xh);
+                add(2, i, p, gf, xh);
             }
             cta_sum(s1, part[0]);
         } else if (RING) {
@@ -392,45 +405,45 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 if (c0 + i * step >= a.H) continue;
-                const F<V> xf = widen<XT, V>(xv[i]);
+                const F<8> xf = widen<XT, 8, W>(xv[i]);
 #pragma unroll
-                for (int j = 0; j < V; ++j) d[i].v[j] = fmaf(m, xf.v[j], d[i].v[j]);
+                for (int j = 0; j < 8; ++j) d[i].v[j] = fmaf(m, xf.v[j], d[i].v[j]);
             }
         }
         float s2[2] = {0.0f, 0.0f};  // q oh, u d
         const bool token = dgate && a.gate_kind == 2;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int c = c0 + i * step;
-            if (c >= a.H) continue;
-            stf<XT, V>(dx + row + c, d[i]);
+            const Part<W> p(c0, step, i);
+            if (p.c >= a.H) continue;
+            st_part<XT, W>(dx + row, p, a.H, d[i]);
             if (!o) continue;
-            F<V> g, pg;
-            if (RING && ring.gain[2] >= 0) g = lds_gain<V>(nb_smem, ring.gain[2], c, a.H);
-            else g = gate_at<V>(a, t, c);
-            if constexpr (RING) pg = lds_gain<V>(nb_smem, ring.gain[1], c, a.H);
-            else pg = a.post_norm ? gain_at<V>(a.post_gain, c) : ones<V>();
-            F<V> oh = widen<BT, V>(ov[i]), u, e;
+            F<8> g, pg;
+            if (RING && ring.gain[2] >= 0) g = lds_gain(nb_smem, ring.gain[2], p.c, a.H);
+            else g = gate_at<W>(a, t, p);
+            if constexpr (RING) pg = lds_gain(nb_smem, ring.gain[1], p.c, a.H);
+            else pg = a.post_norm ? gain_at<W>(a.post_gain, p, a.H) : ones<8>();
+            F<8> oh = widen<BT, 8, W>(ov[i]), u, e;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 oh.v[j] *= ro_t;
                 u.v[j] = oh.v[j] * pg.v[j];
                 e.v[j] = d[i].v[j] * (a.alpha * g.v[j]);
             }
             if (token) {
 #pragma unroll
-                for (int j = 0; j < V; ++j) s2[1] = fmaf(u.v[j], d[i].v[j], s2[1]);
+                for (int j = 0; j < 8; ++j) s2[1] = fmaf(u.v[j], d[i].v[j], s2[1]);
             }
-            add(1, i, c, u, d[i]);  // times alpha at the end
-            add(0, i, c, e, oh);
+            add(1, i, p, u, d[i]);  // times alpha at the end
+            add(0, i, p, e, oh);
             if (dgate && a.gate_kind == 3) {
-                F<V> dg;
+                F<8> dg;
 #pragma unroll
-                for (int j = 0; j < V; ++j) dg.v[j] = a.alpha * (u.v[j] * d[i].v[j]);
-                stf<float, V>(dgate + row + c, dg);
+                for (int j = 0; j < 8; ++j) dg.v[j] = a.alpha * (u.v[j] * d[i].v[j]);
+                st_part<float, W>(dgate + row, p, a.H, dg);
             }
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
+            for (int j = 0; j < 8; ++j) {
                 s2[0] = fmaf(e.v[j], u.v[j], s2[0]);
                 d[i].v[j] = e.v[j] * pg.v[j];  // q
             }
@@ -444,12 +457,12 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
             }
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int c = c0 + i * step;
-                if (c >= a.H) continue;
-                F<V> r = widen<BT, V>(ov[i]);
+                const Part<W> p(c0, step, i);
+                if (p.c >= a.H) continue;
+                F<8> r = widen<BT, 8, W>(ov[i]);
 #pragma unroll
-                for (int j = 0; j < V; ++j) r.v[j] = ro_t * fmaf(m, r.v[j], d[i].v[j]);
-                stf<BT, V>(d_o + row + c, r);
+                for (int j = 0; j < 8; ++j) r.v[j] = ro_t * fmaf(m, r.v[j], d[i].v[j]);
+                st_part<BT, W>(d_o + row, p, a.H, r);
             }
         }
         __syncthreads();  // part is free for the next row
@@ -460,10 +473,10 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
         for (int k = 0; k < kNormSums; ++k)
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                const int c = c0 + i * step;
-                if (!s_of[k] || c >= a.H) continue;
+                const Part<W> p(c0, step, i);
+                if (!s_of[k] || p.c >= a.H) continue;
 #pragma unroll
-                for (int j = 0; j < V; ++j) s_of[k][sum_at<V>(c + j, a.H)] = acc[RING ? k : 0][RING ? i : 0].v[j];
+                for (int j = 0; j < 8; ++j) s_of[k][sum_at<W>(p.c + j, a.H)] = acc[RING ? k : 0][RING ? i : 0].v[j];
             }
     }
     cluster_sync();
@@ -471,7 +484,7 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
     float* mine = partial + (int64_t)(blockIdx.x / cs) * keep.n * a.H;
     for (int i = rank * (int)blockDim.x + (int)threadIdx.x; i < keep.n * a.H; i += cs * (int)blockDim.x) {
         const int k = i / a.H, c = i - k * a.H;
-        const float* p = sums + k * a.H + sum_at<V>(c, a.H);
+        const float* p = sums + k * a.H + sum_at<W>(c, a.H);
         float s = 0.0f;
         for (int q = 0; q < cs; ++q) s += ld_cluster(p, q);
         mine[i] = k == keep.at[1] ? a.alpha * s : s;  // dgate
@@ -479,12 +492,13 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
     cluster_sync();  // no CTA leaves while another reads its sums
 }
 
-// out[c] = sum over the partial rows, 32 columns by 8 runs of rows per CTA;
+// out[c] = sum over the partial rows, 32 columns by RUNS runs of rows per CTA;
 // blockIdx.y picks the sum
-__global__ void __launch_bounds__(256)
+template <int RUNS>
+__global__ void __launch_bounds__(32 * RUNS)
 norm_reduce_kernel(const float* __restrict__ partial, int rows, int H, NormSums keep, float* dpost, float* dgate,
                    float* dpre) {
-    __shared__ float part[8][32];
+    __shared__ float part[RUNS][32];
     float* out = blockIdx.y == 0 ? dpost : blockIdx.y == 1 ? dgate : dpre;
     const int k = keep.at[blockIdx.y];
     pdl_trigger();
@@ -495,12 +509,12 @@ norm_reduce_kernel(const float* __restrict__ partial, int rows, int H, NormSums 
     float s = 0.0f;
     if (c < H)
 #pragma unroll 4
-        for (int r = run; r < rows; r += 8) s += partial[((int64_t)r * keep.n + k) * H + c];
+        for (int r = run; r < rows; r += RUNS) s += partial[((int64_t)r * keep.n + k) * H + c];
     part[run][lane] = s;
     __syncthreads();
     if (run == 0 && c < H) {
 #pragma unroll
-        for (int i = 1; i < 8; ++i) s += part[i][lane];
+        for (int i = 1; i < RUNS; ++i) s += part[i][lane];
         out[c] = s;
     }
 }

@@ -202,21 +202,27 @@ struct Picks {
     }
 };
 
-// xs[inv[t, j]] = x[t]: block = (token, run of 256 vectors)
-template <typename V>
+// xs[inv[t, j]] = x[t]: block = (token, run of 256 N elements of type T, which
+// stands for 16 bytes of a row or, where rows or pointers allow no more, for one or two
+// of its elements, N of them a thread)
+template <typename T, int N>
 __global__ void __launch_bounds__(256)
-dispatch_kernel(const V* __restrict__ x, int64_t P, int nvec, int per_row, int k,
-                const int32_t* __restrict__ inv, V* __restrict__ xs) {
+dispatch_kernel(const T* __restrict__ x, int64_t P, int nvec, int per_row, int k,
+                const int32_t* __restrict__ inv, T* __restrict__ xs) {
     const int64_t t = blockIdx.x / per_row;
-    const int c = (int)(blockIdx.x - t * per_row) * 256 + threadIdx.x;
+    const int c = (int)(blockIdx.x - t * per_row) * 256 * N + threadIdx.x;
     pdl_trigger();
     pdl_wait();
-    V v;
-    if (c < nvec) v = x[t * nvec + c];
+    T v[N];
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+        if (c + 256 * i < nvec) v[i] = x[t * nvec + c + 256 * i];
     const Picks picks(inv, nullptr, t, k, P);
     for (unsigned live = picks.live; live; live &= live - 1) {
         const int64_t p = __shfl_sync(0xffffffffu, picks.row, __ffs(live) - 1);
-        if (c < nvec) xs[p * nvec + c] = v;
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            if (c + 256 * i < nvec) xs[p * nvec + c + 256 * i] = v[i];
     }
 }
 
@@ -225,8 +231,8 @@ dispatch_kernel(const V* __restrict__ x, int64_t P, int nvec, int per_row, int k
 // at a time so that their loads are in flight together; the next item's picks
 // are read while this one's rows are on their way, and the residual is asked
 // for before them, so that a warp waits for HBM about once an item.
-template <typename OT, typename YT, int N>
-__global__ void __launch_bounds__(256, 3)
+template <typename OT, typename YT, int N, int W>
+__global__ void __launch_bounds__(256, W == N ? 3 : 2)
 rows_sum_kernel(const OT* __restrict__ o, int64_t P, int T, int H, int k,
                 const int32_t* __restrict__ inv, const float* __restrict__ w,
                 const YT* residual, YT* y) {
@@ -239,24 +245,24 @@ rows_sum_kernel(const OT* __restrict__ o, int64_t P, int T, int H, int k,
     Picks picks(inv, w, item / per, k, P);
     for (;;) {
         const int64_t t = item / per;
-        const int c = ((int)(item - t * per) * 32 + (threadIdx.x & 31)) * N;
-        const bool in = c < H;
-        F<N> acc, res;
+        const int c = (int)(item - t * per) * 32 * N + (threadIdx.x & 31) * W;
+        F<N> acc;
+        Cols<YT, N, W> res;
 #pragma unroll
         for (int i = 0; i < N; ++i) acc.v[i] = 0.0f;
-        if (residual && in) res = ldf<YT, N>(residual + t * H + c);
+        if (residual) res = ldc<YT, N, W>(residual + t * H, c, 32 * W, H);
         item += step;
         Picks after = picks;
         bool first = true;
         for (unsigned live = picks.live; live || first;) {
-            Vec<OT, N> v[8];
+            Cols<OT, N, W> v[8];
             const unsigned group = live;
 #pragma unroll
             for (int j = 0; j < 8; ++j)
                 if (live) {
                     const int64_t p = __shfl_sync(0xffffffffu, picks.row, __ffs(live) - 1);
                     live &= live - 1;
-                    if (in) v[j] = ldv<OT, N>(o + p * H + c);
+                    v[j] = ldc<OT, N, W>(o + p * H, c, 32 * W, H);
                 }
             if (first && item < items) after = Picks(inv, w, item / per, k, P);
             first = false;
@@ -266,18 +272,17 @@ rows_sum_kernel(const OT* __restrict__ o, int64_t P, int T, int H, int k,
                 if (m) {
                     const float wj = __shfl_sync(0xffffffffu, picks.w, __ffs(m) - 1);
                     m &= m - 1;
-                    const F<N> f = widen<OT, N>(v[j]);
+                    const F<N> f = widen<OT, N, W>(v[j]);
 #pragma unroll
                     for (int i = 0; i < N; ++i) acc.v[i] = fmaf(wj, f.v[i], acc.v[i]);
                 }
         }
-        if (in) {
-            if (residual) {
+        if (residual) {
+            const F<N> r = widen<YT, N, W>(res);
 #pragma unroll
-                for (int i = 0; i < N; ++i) acc.v[i] += res.v[i];
-            }
-            stf<YT, N>(y + t * H + c, acc);
+            for (int i = 0; i < N; ++i) acc.v[i] += r.v[i];
         }
+        stc<YT, N, W>(y + t * H, c, 32 * W, H, narrow_cols<YT, N, W>(acc));
         if (item >= items) return;
         picks = after;
     }
@@ -286,8 +291,8 @@ rows_sum_kernel(const OT* __restrict__ o, int64_t P, int T, int H, int k,
 // Gradients of the weighted sum: one warp per pick walks its row, writes w * dy
 // into it and keeps the dot product of dy and o, with no barrier; the warps of a
 // token's picks meet its dy in L1.
-template <typename YT, typename OT, int N>
-__global__ void __launch_bounds__(256, 3)
+template <typename YT, typename OT, int N, int W>
+__global__ void __launch_bounds__(256, W == N ? 3 : 2)
 rows_sum_backward_kernel(const YT* __restrict__ dy, const OT* __restrict__ o, int64_t P, int H,
                          int k, const int32_t* __restrict__ inv, const float* __restrict__ w,
                          OT* __restrict__ d_o, float* __restrict__ dw) {
@@ -309,28 +314,27 @@ rows_sum_backward_kernel(const YT* __restrict__ dy, const OT* __restrict__ o, in
     F<N> dot;  // a sum per element of the vector: N short chains
 #pragma unroll
     for (int e = 0; e < N; ++e) dot.v[e] = 0.0f;
-    for (int c0 = lane * N; c0 < H; c0 += 32 * N * U) {
-        F<N> g[U];
-        Vec<OT, N> v[U];
+    for (int c0 = lane * W; c0 < H; c0 += 32 * N * U) {
+        Cols<YT, N, W> g[U];
+        Cols<OT, N, W> v[U];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int c = c0 + u * 32 * N;
-            if (c >= H) continue;
-            if (dw) v[u] = ldv<OT, N>(o_row + c);
-            g[u] = ldf<YT, N>(g_row + c);
+            if (dw) v[u] = ldc<OT, N, W>(o_row, c, 32 * W, H);
+            g[u] = ldc<YT, N, W>(g_row, c, 32 * W, H);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int c = c0 + u * 32 * N;
-            if (c >= H) continue;
+            F<N> gf = widen<YT, N, W>(g[u]);
             if (dw) {
-                const F<N> f = widen<OT, N>(v[u]);
+                const F<N> f = widen<OT, N, W>(v[u]);
 #pragma unroll
-                for (int e = 0; e < N; ++e) dot.v[e] = fmaf(f.v[e], g[u].v[e], dot.v[e]);
+                for (int e = 0; e < N; ++e) dot.v[e] = fmaf(f.v[e], gf.v[e], dot.v[e]);
             }
 #pragma unroll
-            for (int e = 0; e < N; ++e) g[u].v[e] *= wj;
-            if (d_o) stf<OT, N>(d_row + c, g[u]);
+            for (int e = 0; e < N; ++e) gf.v[e] *= wj;
+            if (d_o) stc<OT, N, W>(d_row, c, 32 * W, H, narrow_cols<OT, N, W>(gf));
         }
     }
     if (dw) {

@@ -105,4 +105,50 @@ template <typename T, int N> __device__ __forceinline__ Vec<T, N> narrow(const F
 template <typename T, int N> __device__ __forceinline__ F<N> ldf(const T* p) { return widen<T, N>(ldv<T, N>(p)); }
 template <typename T, int N> __device__ __forceinline__ void stf(T* p, const F<N>& a) { stv<T, N>(p, narrow<T, N>(a)); }
 
+// N elements of a row as N / W chunks of W neighbours, `stride` elements apart: W = N
+// where rows and pointers allow one wide access; else a thread's chunks lie a
+// warp's (or CTA's) worth of chunks apart, so that each access of a warp is still
+// one run of memory, and as many bytes are in flight.  Chunks at column H or
+// later are left out (a multiple of W).
+template <typename T, int N, int W> struct Cols { Vec<T, W> q[N / W]; };
+
+template <typename T, int N, int W>
+__device__ __forceinline__ Cols<T, N, W> ldc(const T* row, int c, int stride, int H) {
+    Cols<T, N, W> r;
+#pragma unroll
+    for (int i = 0; i < N / W; ++i)
+        if (c + i * stride < H) r.q[i] = ldv<T, W>(row + c + i * stride);
+        else
+#pragma unroll
+            for (int j = 0; j < (int)(sizeof(r.q[i].u) / 4); ++j) r.q[i].u[j] = 0;
+    return r;
+}
+template <typename T, int N, int W>
+__device__ __forceinline__ void stc(T* row, int c, int stride, int H, const Cols<T, N, W>& a) {
+#pragma unroll
+    for (int i = 0; i < N / W; ++i)
+        if (c + i * stride < H) stv<T, W>(row + c + i * stride, a.q[i]);
+}
+template <typename T, int N, int W> __device__ __forceinline__ F<N> widen(const Cols<T, N, W>& a) {
+    F<N> r;
+#pragma unroll
+    for (int i = 0; i < N / W; ++i) {
+        const F<W> f = widen<T, W>(a.q[i]);
+#pragma unroll
+        for (int j = 0; j < W; ++j) r.v[i * W + j] = f.v[j];
+    }
+    return r;
+}
+template <typename T, int N, int W> __device__ __forceinline__ Cols<T, N, W> narrow_cols(const F<N>& a) {
+    Cols<T, N, W> r;
+#pragma unroll
+    for (int i = 0; i < N / W; ++i) {
+        F<W> f;
+#pragma unroll
+        for (int j = 0; j < W; ++j) f.v[j] = a.v[i * W + j];
+        r.q[i] = narrow<T, W>(f);
+    }
+    return r;
+}
+
 }  // namespace coli

@@ -20,9 +20,9 @@ ALPHA, EPS = 0.7, 1e-5
 
 
 def chain(H):
-    """Roundings on the way of one term into a sum over the row: 16 or 32 of a thread
-    (or fewer), 5 in a warp, 5 across warps, and a few of the factors."""
-    return (16 if H <= 8192 else 32) + 5 + 5 + 6
+    """Roundings on the way of one term into a sum over the row: at most 32 of a thread (four
+    vectors of eight), 5 in a warp, 5 across warps, and a few of the factors."""
+    return 32 + 5 + 5 + 6
 
 
 class Case:
@@ -66,7 +66,8 @@ def rstd(v):
     return 1.0 / torch.sqrt(v.square().mean(1) + EPS)
 
 
-SHAPES = [(1, 6144), (1, 1), (3, 2), (5, 127), (17, 1024), (9, 6144), (3, 8192), (2, 8196), (2, 16384), (2, 9001), (300, 260)]
+SHAPES = [(1, 6144), (1, 1), (3, 2), (5, 127), (17, 1024), (9, 6144), (3, 8192), (2, 8196), (2, 16384), (2, 9001), (300, 260),
+          (9, 6143), (9, 4098), (3000, 33)]
 TYPES = [(F, F), (F, B), (B, B)]
 
 
@@ -165,8 +166,9 @@ def check_backward(c, dxo=True, dn=True):
     d = d0 + (rx * (v - xh * mean) if dn else 0)
     size = d0.abs() + (rx * (v.abs() + xh.abs() * (v * xh).abs().mean(1, keepdim=True)) if dn else 0)
     assert ((dx.double() - d).abs() <= C * size + HALF[c.xt] * d.abs()).all()
-    # the sums over tokens: rows of a CTA one after the other, then at most 37 + 8 partial rows
-    S = C + (-(-T // 296) + 45) * U24
+    # the sums over tokens: rows of a CTA one after the other (148 CTAs at least), two CTAs of a
+    # cluster, then partial rows of at most 16 x 148 / 2 / 32 in a run and the sums of 32 runs
+    S = C + (-(-T // 148) + 2 + 37 + 32) * U24
     if dn:
         t = c.dn.double() * xh
         assert ((dpre.double() - t.sum(0)).abs() <= S * t.abs().sum(0) + 1e-30).all()

@@ -65,10 +65,11 @@ def test_quantize_bits(fmt, dt, K):
 
 @pytest.mark.parametrize("fmt", list(FMT))
 @pytest.mark.parametrize("rows", [1, 127, 128, 129, 300])
-def test_quantize_many_rows(fmt, rows):
-    x = np.random.default_rng(rows).standard_normal((rows, 224)).astype(np.float32)
-    codes, scales = quantize(fmt, dev(x), rows, 224)
-    check_codes(fmt, codes, scales, ff.quantize(x, fmt), rows, 224)
+@pytest.mark.parametrize("K", [32, 96, 128, 160, 224, 256, 544])
+def test_quantize_many_rows(fmt, rows, K):
+    x = np.random.default_rng(rows).standard_normal((rows, K)).astype(np.float32)
+    codes, scales = quantize(fmt, dev(x), rows, K)
+    check_codes(fmt, codes, scales, ff.quantize(x, fmt), rows, K)
 
 
 @pytest.mark.parametrize("fmt", list(FMT))

@@ -90,7 +90,8 @@ def test_sort_of_no_tokens():
     assert off.tolist() == [0] * 5
 
 
-SHAPES = [(1, 6144, 8), (1, 1, 1), (3, 7, 2), (5, 256, 32), (65, 1000, 9), (40, 6144, 8), (257, 129, 3), (2, 8200, 10)]
+SHAPES = [(1, 6144, 8), (1, 1, 1), (3, 7, 2), (5, 256, 32), (65, 1000, 9), (40, 6144, 8), (257, 129, 3), (2, 8200, 10),
+          (30, 6143, 8), (9, 6142, 4), (700, 34, 5)]
 TYPES = [torch.float32, torch.bfloat16]
 
 
@@ -150,10 +151,9 @@ def test_combine_residual_may_alias_y():
 
 
 def dot_bound(H, dt):
-    # the longest chain of one lane's fused steps (16-byte vectors with a sum per element, or
-    # single elements), then at most 8 of its own sums and 5 in the warp
-    n = 16 // dt.itemsize if H % (16 // dt.itemsize) == 0 else 1
-    return (-(-H // (32 * n)) + 13) * U24 * 1.01
+    # the longest chain of one lane's fused steps (16 bytes of columns at a time, with a sum per
+    # element), then at most 8 of its own sums and 5 in the warp
+    return (-(-H // (32 * (16 // dt.itemsize))) + 13) * U24 * 1.01
 
 
 @pytest.mark.parametrize("ot,yt", [(a, b) for a in TYPES for b in TYPES])
@@ -247,7 +247,7 @@ def test_unaligned_rows(H):
     assert torch.equal(do, do0)
     # the two kernels add the products in different orders
     size = gathered(xs0, inv).abs().mul(y0.double().abs()[:, None]).sum(2)
-    assert ((dw - dw0).double().abs() <= (dot_bound(H, torch.bfloat16) + dot_bound(2 * H + 1, torch.bfloat16)) * size).all()
+    assert ((dw - dw0).double().abs() <= 2 * dot_bound(H, torch.bfloat16) * size).all()
 
 
 def test_rows_outside_the_buffer_are_not_computed():
