@@ -196,6 +196,10 @@ fp4_quantize_kernel(Fp4QuantArgs a, int warps, int rows_per, int lanes, const T*
 constexpr int kFpScaleWarps = 4;
 constexpr int kFpStoreWarps = 8;   // at most
 constexpr int kFpMaxE = 1024;
+// Stages that a cut tile's pieces have at least: shorter ones save less than joining
+// them takes (8 rows, 20 experts of 1024 x 2048: 6.7 us with 8, 8.8 with 4; 512 rows, 64
+// experts of 6144 x 2048: 74 and 80 us; pairs, 400 rows of 1000 x 2048: 8.0 and 15.2).
+constexpr int kFpMinUnits = 8;
 constexpr int kFpMaxGrid = 160;    // B200 has 148 SMs; the workspace is sized for this many
 // the workspace: error flags, a flag per CTA and store warp, then partial sums
 constexpr int kFpFlagBytes = 256;
@@ -210,9 +214,6 @@ struct FpShape {
     static constexpr int ctas = PAIR ? 2 : 1;
     static constexpr int rows = NT / ctas;                   // of X in a CTA's shared memory
     static constexpr int box = PAIR ? rows / 2 : rows;       // rows per TMA box of X
-    // stages that a cut tile's pieces have at least: fewer cost less time than joining them
-    // (one tile of 24 stages: MIN_UNITS)
-    static constexpr int min_units = PAIR ? 8 : 4;
     static constexpr int store_warps = NT > 32 ? kFpStoreWarps : 4;
     static constexpr int groups = store_warps / 4;           // warps to a quarter of the lanes
     static constexpr int threads = 32 * (6 + store_warps);
@@ -577,7 +578,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     if (PAIR) cluster_sync();  // the other CTA's barriers are set up
     tc_fence_after();
     const uint32_t tmem = uniform(tmem_slot);
-    const FpRun run(a, plan, gridDim.x / C::ctas, C::min_units);
+    const FpRun run(a, plan, gridDim.x / C::ctas, kFpMinUnits);
     FpPieces q(a, run, unit);
     bool ok = true;  // cleared by a wait that gave up: then no further waits
 
