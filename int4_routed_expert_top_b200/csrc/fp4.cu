@@ -51,6 +51,15 @@ int encode_codes_map(CUtensorMap* m, const void* base, int64_t rows, int K, int 
     return COLI_OK;
 }
 
+template <typename T>
+int launch_quantize(coli_fp4 fmt, coli_act act, dim3 grid, int threads, const Fp4QuantArgs& a, int warps, int rows_per,
+                    int lanes, const void* x, void* values, cudaStream_t st) {
+    const bool nv = fmt == COLI_NVFP4, glu = act == COLI_ACT_SWIGLU;
+    const auto kern = nv ? (glu ? fp4_quantize_kernel<T, true, true> : fp4_quantize_kernel<T, true, false>)
+                         : (glu ? fp4_quantize_kernel<T, false, true> : fp4_quantize_kernel<T, false, false>);
+    return launch_pdl(kern, grid, threads, 0, st, "fp4 quantize", a, warps, rows_per, lanes, (const T*)x, (T*)values);
+}
+
 template <int NT, bool NV, bool PAIR, typename YT>
 int launch_product(const FpArgs& a, const void* x_codes, const void* w_codes, void* y, cudaStream_t st) {
     using C = FpShape<NT, NV, PAIR>;
@@ -118,7 +127,6 @@ int coli_moe_fp4_quantize(coli_fp4 fmt, const void* x, coli_dtype xt, int64_t n_
     Fp4QuantArgs a;
     a.n_src = n_src; a.rows = rows;
     a.K = K; a.words = words_of(fmt, K);
-    a.swiglu = act == COLI_ACT_SWIGLU;
     a.src = src; a.count = count; a.gscale = gscale;
     a.codes = static_cast<uint8_t*>(codes);
     a.scales = static_cast<uint32_t*>(scales);
@@ -131,12 +139,8 @@ int coli_moe_fp4_quantize(coli_fp4 fmt, const void* x, coli_dtype xt, int64_t n_
     const dim3 grid((unsigned)((rows + cta_rows - 1) / cta_rows), parts);
     const int threads = 32 * warps * rows_per;
     if (xt == COLI_F32)
-        return launch_pdl(fmt == COLI_NVFP4 ? fp4_quantize_kernel<float, true> : fp4_quantize_kernel<float, false>, grid,
-                          threads, 0, S(stream), "fp4 quantize", a, warps, rows_per, lanes, (const float*)x, (float*)values);
-    return launch_pdl(fmt == COLI_NVFP4 ? fp4_quantize_kernel<__nv_bfloat16, true>
-                                        : fp4_quantize_kernel<__nv_bfloat16, false>,
-                      grid, threads, 0, S(stream), "fp4 quantize", a, warps, rows_per, lanes, (const __nv_bfloat16*)x,
-                      (__nv_bfloat16*)values);
+        return launch_quantize<float>(fmt, act, grid, threads, a, warps, rows_per, lanes, x, values, S(stream));
+    return launch_quantize<__nv_bfloat16>(fmt, act, grid, threads, a, warps, rows_per, lanes, x, values, S(stream));
 }
 
 int coli_moe_fp4_product_workspace_size(coli_fp4 fmt, int64_t P, int32_t K, int32_t E, int32_t R, size_t* bytes) {

@@ -15,7 +15,7 @@
 // rows).  As many whole waves of tiles as there are go to the CTAs in turn, so
 // that the SMs work on neighbouring tiles, whose weights and rows then come from
 // L2 (runs of tiles per CTA read 3.6 GB from HBM where this order reads
-// WAVE_READ, at 4096 tokens x 8 picks on 32 experts of 4096 x 6144).  The tiles
+// 0.55 GB, at 4096 tokens x 8 picks on 32 experts of 4096 x 6144).  The tiles
 // that are left over, all of them at few rows, are cut by units into equal runs, one
 // per CTA, so that every SM streams the same number of bytes.  A tile that a
 // run's border cuts leaves f32 partial sums in the workspace: every
@@ -34,7 +34,14 @@
 // up to 224 rows (tcgen05 cta_group::2): each holds 128 of the weight rows and half
 // of the others in its shared memory and the accumulators of its weight rows, and
 // CTA 0 issues the products for both.  A stage is then 33 KB per SM instead of the
-// 43 KB of a 128 x 192 tile for 1.17 times the work: PAIR_TIME.
+// 43 KB of a 128 x 192 tile for 1.17 times the work.
+//
+// Measured (B200): 8 rows, one to an expert, of 4096 x 6144: 23.2 us, 4.6 TB/s of
+// weights (launch, schedule and first loads are some 6 us of it); 512 rows on 64
+// experts of 6144 x 2048: 73 us, 6.3 TB/s, 0.97 of a copy's rate; 32768 rows on 32
+// experts of 4096 x 6144 with skewed counts: 363 us, 4.5 PFLOP/s, the tensor pipe
+// 70% active; one matrix of 18944 x 6144 and 14336 rows: 5.4 PFLOP/s, 7.0 with all
+// codes zero: under sustained load the chip's power limit sets the clock (1.4 GHz).
 //
 // CTA roles: warp 0 copies (codes by 2-D TMA with the 128-byte swizzle, the
 // weights' scales by bulk copy), four warps bring the rows' scales (rows of an
@@ -58,7 +65,6 @@ namespace coli {
 struct Fp4QuantArgs {
     int64_t n_src, rows;
     int K, words;            // words: 4-block scale words per row
-    int swiglu;
     const int32_t* src;
     const int32_t* count;
     const float* gscale;
@@ -100,7 +106,7 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 constexpr int kQuantCols = 512;
 constexpr int kQuantWarps = 16;  // of a CTA, at most
 
-template <typename T, bool NV>
+template <typename T, bool NV, bool GLU>
 __global__ void __launch_bounds__(32 * kQuantWarps)
 fp4_quantize_kernel(Fp4QuantArgs a, int warps, int rows_per, int lanes, const T* __restrict__ x,
                     T* __restrict__ values) {
@@ -116,22 +122,27 @@ fp4_quantize_kernel(Fp4QuantArgs a, int warps, int rows_per, int lanes, const T*
     const bool live = r < rows, in = live && c < a.K;  // K is a multiple of 32: all 16 columns or none
     const int64_t from = !live ? 0 : a.src ? a.src[r] : r;
     const float g = NV && a.gscale ? *a.gscale : 1.0f;
+    const bool read = in && from >= 0 && from < a.n_src;
+    const T* p = x + from * (GLU ? 2 * a.K : a.K) + c;
+    Vec<T, 8> raw[GLU ? 4 : 2];
+#pragma unroll
+    for (int i = 0; i < (GLU ? 4 : 2); ++i) {
+        if (read) raw[i] = ldv<T, 8>(p + (i & 1) * 8 + (i >> 1) * a.K);
+        else
+#pragma unroll
+            for (int j = 0; j < (int)(sizeof(raw[i].u) / 4); ++j) raw[i].u[j] = 0;
+    }
     float v[16];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) v[i] = 0.0f;
-    if (in && from >= 0 && from < a.n_src) {
-        const T* p = x + from * (a.swiglu ? 2 * a.K : a.K) + c;
-        const F<8> lo = ldf<T, 8>(p), hi = ldf<T, 8>(p + 8);
+    for (int h = 0; h < 2; ++h) {
+        F<8> f = widen<T, 8>(raw[h]);
+        if (GLU) {
+            const F<8> u = widen<T, 8>(raw[GLU ? 2 + h : 0]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) { v[i] = lo.v[i]; v[8 + i] = hi.v[i]; }
-        if (a.swiglu) {
-            const F<8> ulo = ldf<T, 8>(p + a.K), uhi = ldf<T, 8>(p + a.K + 8);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                v[i] = silu_f(v[i]) * ulo.v[i];
-                v[8 + i] = silu_f(v[8 + i]) * uhi.v[i];
-            }
+            for (int i = 0; i < 8; ++i) f.v[i] = silu_f(f.v[i]) * u.v[i];
         }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[8 * h + i] = f.v[i];
     }
     // the largest magnitude; infinities and NaN come out on top, as bits too
     float top = 0.0f;
@@ -155,10 +166,7 @@ fp4_quantize_kernel(Fp4QuantArgs a, int warps, int rows_per, int lanes, const T*
         r_d = __uint_as_float((uint32_t)(254 - b) << 23);
     }
 #pragma unroll
-    for (int i = 0; i < 16; i += 2) {
-        const float2 q = f2unpack(f2mul(f2pack(v[i], v[i + 1]), f2pack(r_d, r_d)));
-        v[i] = q.x; v[i + 1] = q.y;
-    }
+    for (int i = 0; i < 16; ++i) v[i] = __fmul_rn(v[i], r_d);
     uint32_t code[2] = {e2m1x8(v), e2m1x8(v + 8)};
     if (bad || (NV && !(d > 0.0f))) code[0] = code[1] = 0;
     // four blocks' bytes make a word: a block is 1 (NV) or 2 lanes
