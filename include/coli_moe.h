@@ -454,7 +454,7 @@ int coli_moe_sort(const int32_t* idx, const float* w, int32_t T, int32_t k, int3
                   void* ws, size_t ws_bytes, coli_stream_t stream);
 
 /* Tokens copied into the order of their picks: xs[inv[t, j]] = x[t].  x device
- * [T, H], xs device [T*k, H], both of type xt (f32 or bf16), any H >= 1.  Rows
+ * [T, H], xs device [T*k, H], both of type xt (f32 or bf16), 1 <= H <= 2^24.  Rows
  * of xs that no pick names are left untouched.  An entry of inv outside
  * [0, T*k) counts as a pick not computed, here and in the calls below. */
 int coli_moe_dispatch(const void* x, coli_dtype xt, int32_t T, int32_t H, int32_t k,

@@ -32,7 +32,7 @@ int picks_ok(const char* what, int T, int k) {
 int rows_ok(const char* what, int T, int H, int k) {
     const int rc = picks_ok(what, T, k);
     if (rc) return rc;
-    if (H < 1 || (int64_t)T * ((H + 255) / 256) > INT32_MAX)  // one CTA per 256 columns at most
+    if (H < 1 || H > (1 << 24) || (int64_t)T * ((H + 255) / 256) > INT32_MAX)  // one CTA per 256 columns at most
         return fail(COLI_E_INVAL, "%s: bad sizes T=%d H=%d", what, T, H);
     return COLI_OK;
 }
@@ -73,6 +73,20 @@ int launch_rows_sum(const void* o, int T, int H, int k, const int32_t* inv, cons
     const int grid = (int)std::min<int64_t>((items + 7) / 8, (W == N ? 3 : 2) * 148);
     return launch_pdl(kern, dim3(grid), 256, 0, st, "combine", (const OT*)o, (int64_t)T * k, T, H, k, inv, w,
                       (const YT*)residual, (YT*)y);
+}
+
+int rows_sum(const char* what, const void* o, coli_dtype ot, int T, int H, int k, const int32_t* inv, const float* w,
+             const void* residual, void* y, coli_dtype yt, cudaStream_t st) {
+    const int rc = rows_ok(what, T, H, k);
+    if (rc) return rc;
+    if (!type_ok(ot) || !type_ok(yt)) return fail(COLI_E_INVAL, "%s: bad dtype", what);
+    if (T == 0) return COLI_OK;
+    if (!o || !inv || !y) return fail(COLI_E_INVAL, "%s: NULL pointer", what);
+    if (ot == COLI_F32)
+        return yt == COLI_F32 ? launch_rows_sum<float, float>(o, T, H, k, inv, w, residual, y, st)
+                              : launch_rows_sum<float, __nv_bfloat16>(o, T, H, k, inv, w, residual, y, st);
+    return yt == COLI_F32 ? launch_rows_sum<__nv_bfloat16, float>(o, T, H, k, inv, w, residual, y, st)
+                          : launch_rows_sum<__nv_bfloat16, __nv_bfloat16>(o, T, H, k, inv, w, residual, y, st);
 }
 
 template <typename YT, typename OT>
@@ -311,22 +325,13 @@ int coli_moe_dispatch(const void* x, coli_dtype xt, int32_t T, int32_t H, int32_
 
 int coli_moe_dispatch_backward(const void* dxs, coli_dtype xt, int32_t T, int32_t H, int32_t k,
                                const int32_t* inv, void* dx, coli_stream_t stream) {
-    return coli_moe_combine(dxs, xt, T, H, k, inv, nullptr, nullptr, dx, xt, stream);
+    return rows_sum("dispatch_backward", dxs, xt, T, H, k, inv, nullptr, nullptr, dx, xt, S(stream));
 }
 
 int coli_moe_combine(const void* o, coli_dtype ot, int32_t T, int32_t H, int32_t k,
                      const int32_t* inv, const float* w, const void* residual, void* y,
                      coli_dtype yt, coli_stream_t stream) {
-    int rc = rows_ok("combine", T, H, k);
-    if (rc) return rc;
-    if (!type_ok(ot) || !type_ok(yt)) return fail(COLI_E_INVAL, "combine: bad dtype");
-    if (T == 0) return COLI_OK;
-    if (!o || !inv || !y) return fail(COLI_E_INVAL, "combine: NULL pointer");
-    if (ot == COLI_F32)
-        return yt == COLI_F32 ? launch_rows_sum<float, float>(o, T, H, k, inv, w, residual, y, S(stream))
-                              : launch_rows_sum<float, __nv_bfloat16>(o, T, H, k, inv, w, residual, y, S(stream));
-    return yt == COLI_F32 ? launch_rows_sum<__nv_bfloat16, float>(o, T, H, k, inv, w, residual, y, S(stream))
-                          : launch_rows_sum<__nv_bfloat16, __nv_bfloat16>(o, T, H, k, inv, w, residual, y, S(stream));
+    return rows_sum("combine", o, ot, T, H, k, inv, w, residual, y, yt, S(stream));
 }
 
 int coli_moe_combine_backward(const void* dy, coli_dtype yt, const void* o, coli_dtype ot, int32_t T,

@@ -566,7 +566,6 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     }
     if (threadIdx.x == 32) {
         for (int s = 0; s < C::stages; ++s) {
-
             // the copies' announcement, the lanes of the scale warps; in CTA 0 of a pair, CTA 1's stage
             mbar_init(&full[s], 1 + 32 * kFpScaleWarps + (PAIR && rank == 0 ? 1 : 0));
             mbar_init(&empty[s], 1);

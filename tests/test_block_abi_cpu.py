@@ -42,6 +42,7 @@ PRODUCT = dict(fmt=0, xc=A, xs=A, P=8, K=64, wc=A, ws=A, E=2, R=128, off=A, al=N
     ("coli_moe_dispatch", DISPATCH, dict(xs=None), INVAL),
     ("coli_moe_dispatch", DISPATCH, dict(xt=2), INVAL),
     ("coli_moe_dispatch", DISPATCH, dict(H=0), INVAL),
+    ("coli_moe_dispatch", DISPATCH, dict(T=1, H=(1 << 24) + 1), INVAL),
     ("coli_moe_dispatch", DISPATCH, dict(T=1 << 24, k=32, H=1 << 17), INVAL),
     ("coli_moe_dispatch_backward", DISPATCH, dict(inv=None), INVAL),
     ("coli_moe_combine", COMBINE, dict(o=None), INVAL),

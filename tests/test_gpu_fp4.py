@@ -238,3 +238,39 @@ def test_product_is_the_same_every_time():
         assert torch.equal(a, product("mx", xc, xb, wc, wb, 8, 256, off, None, F, 700, 1024))
     assert float((a[400:650] - product("mx", xc[400:650], xb[400:650], wc[5 * 256:6 * 256], wb[5 * 256:6 * 256], 1, 256,
                                        None, None, F, 250, 1024)).abs().max()) <= 1e-5 * float(a.abs().max())
+
+
+def test_product_one_expert_with_offsets():
+    """E = 1 with offsets: only the rows they name."""
+    rng = np.random.default_rng(11)
+    for P in (20, 90):
+        xc, xb = weights("mx", P, 256, rng)
+        wc, wb = weights("mx", 128, 256, rng)
+        all_rows = product("mx", xc, xb, wc, wb, 1, 128, None, None, F, P, 256)
+        some = product("mx", xc, xb, wc, wb, 1, 128, [3, P - 5], None, F, P, 256)
+        assert (some[:3] == 9.0).all() and (some[P - 5:] == 9.0).all()
+        X, W = dev(ff.values(xc, xb, "mx")), dev(ff.values(wc, wb, "mx"))
+        want, size = X @ W.T, X.abs() @ W.abs().T
+        for y, lo, hi in ((all_rows, 0, P), (some, 3, P - 5)):
+            assert ((y[lo:hi].double() - want[lo:hi]).abs() <= 28 * 2.0 ** -22 * size[lo:hi]).all()
+
+
+def test_product_two_streams_at_once():
+    """Two calls with their own workspaces, their CTAs taking turns on the SMs."""
+    rng = np.random.default_rng(12)
+    calls = []
+    for n, R in ((40, 19200), (700, 9728), (3, 38400)):
+        xc, xb = weights("mx", n, 512, rng)
+        wc, wb = weights("mx", R, 512, rng)
+        args = [dev(xc.reshape(-1)), dev(ff.tile_scales(xb)), n, 512, dev(wc.reshape(-1)), dev(ff.tile_scales(wb)), 1, R]
+        size = cm.coli_moe_fp4_product_workspace_size(FMT["mx"], n, 512, 1, R)
+        want, ws = torch.empty(n, R, device="cuda"), torch.zeros(size, dtype=torch.uint8, device="cuda")
+        cm.coli_moe_fp4_product(FMT["mx"], *args, want, ws)
+        calls.append((args, want, torch.empty_like(want), ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for args, _, y, ws, stream in calls:
+            cm.coli_moe_fp4_product(FMT["mx"], *args, y, ws, stream=stream)
+    torch.cuda.synchronize()
+    for _, want, y, ws, _ in calls:
+        assert cm.coli_moe_fp4_product_status(ws) == 0 and torch.equal(y, want)
