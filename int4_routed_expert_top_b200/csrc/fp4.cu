@@ -31,10 +31,18 @@ int sm_count() {
     return sms;
 }
 
-// Rows of an expert per tile: 32 streams the weights with the deepest ring, 224 (a
-// pair of CTAs) makes the most of each byte in shared memory.
+// Rows of an expert per tile: 32 for a CTA by itself, 224 for a pair of CTAs.  Pairs
+// where an expert has more than 32 rows on average, since its weights then pass an
+// SM once and not several times (32 experts of 4096 x 6144: 73 us by itself and 75
+// in pairs at 16 rows each, 88 and 74 at 33, 167 and 84 at 97, 524 and 169 at 385), and
+// where that gives tiles for half of the 74 pairs at least; with fewer the cut tiles'
+// joining takes more than it saves (one expert of 4096 x 6144: 22 us by itself and 27 in
+// pairs for 385 rows, 32 tiles; of 18944 x 6144: 43 and 15 us for 193 rows, 74 tiles).
 constexpr int kFpSmallNT = 32, kFpLargeNT = 224;
-bool pairs_apply(int64_t P, int E) { return P > (int64_t)48 * E; }
+bool pairs_apply(int64_t P, int E, int R) {
+    const int64_t tiles = E * ((R + 255) / 256) * ((P + (int64_t)kFpLargeNT * E - 1) / ((int64_t)kFpLargeNT * E));
+    return P > (int64_t)kFpSmallNT * E && tiles >= 40;
+}
 
 // bytes [rows][K/2], boxes of 128 bytes x box_rows, 128-byte swizzle
 int encode_codes_map(CUtensorMap* m, const void* base, int64_t rows, int K, int box_rows) {
@@ -149,7 +157,7 @@ int coli_moe_fp4_product_workspace_size(coli_fp4 fmt, int64_t P, int32_t K, int3
     if (!bytes) return fail(COLI_E_INVAL, "fp4_product_workspace_size: NULL pointer");
     if (E < 1 || E > kFpMaxE || R < 1 || (E > 1 && R % 128) || (int64_t)E * R > INT32_MAX)
         return fail(COLI_E_INVAL, "fp4_product: bad sizes E=%d R=%d", E, R);
-    *bytes = kFpHeadBytes + (size_t)kFpMaxGrid * 128 * (pairs_apply(P, E) ? kFpLargeNT : kFpSmallNT) * 4;
+    *bytes = kFpHeadBytes + (size_t)kFpMaxGrid * 128 * (pairs_apply(P, E, R) ? kFpLargeNT : kFpSmallNT) * 4;
     return COLI_OK;
 }
 
@@ -178,7 +186,7 @@ int coli_moe_fp4_product(coli_fp4 fmt, const void* x_codes, const void* x_scales
     a.err = static_cast<int32_t*>(ws);
     a.flags = reinterpret_cast<uint64_t*>(static_cast<char*>(ws) + kFpFlagBytes);
     a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kFpHeadBytes);
-    if (pairs_apply(P, E)) return launch_product_t<kFpLargeNT, true>(fmt, yt, a, x_codes, w_codes, y, S(stream));
+    if (pairs_apply(P, E, R)) return launch_product_t<kFpLargeNT, true>(fmt, yt, a, x_codes, w_codes, y, S(stream));
     return launch_product_t<kFpSmallNT, false>(fmt, yt, a, x_codes, w_codes, y, S(stream));
 }
 

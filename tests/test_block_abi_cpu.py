@@ -134,7 +134,7 @@ def test_sizes():
     assert cm.coli_moe_fp4_bytes(cm.COLI_MXFP4, 130, 160) == (130 * 80, 2 * 2 * 512)
     assert cm.coli_moe_fp4_bytes(cm.COLI_NVFP4, 130, 160) == (130 * 80, 2 * 3 * 512)
     small = cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, 8, 64, 256, 128)
-    assert small < cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, 1 << 16, 64, 32, 128)
+    assert small < cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, 1 << 16, 64, 32, 256)
 
 
 def test_plain_format_hand_values():

@@ -170,8 +170,11 @@ def test_product_one_group(fmt, R, K, n):
 
 
 @pytest.mark.parametrize("fmt", list(FMT))
-@pytest.mark.parametrize("R,K,n", [(128, 256, 49), (128, 512, 128), (256, 288, 129), (100, 1024, 192), (384, 2048, 193), (512, 512, 224), (640, 768, 225),
-                                   (1000, 96, 500), (256, 6144, 400), (128, 128, 449)])
+# 40 tiles of 256 x 224 or more: pairs of CTAs; the others one CTA by itself with several row tiles
+@pytest.mark.parametrize("R,K,n", [(128, 256, 49), (100, 1024, 192), (384, 2048, 193), (1000, 96, 500), (256, 6144, 400),
+                                   (10240, 256, 49), (10240, 512, 128), (10112, 288, 129), (10100, 1024, 192),
+                                   (10240, 2048, 193), (10496, 512, 224), (5248, 768, 225), (5120, 96, 440),
+                                   (10240, 6144, 40), (20000, 128, 449)])
 def test_product_one_group_many_rows(fmt, R, K, n):
     for yt in (F, B):
         check_product(fmt, 1, R, K, [n], yt)
@@ -181,7 +184,9 @@ def test_product_one_group_many_rows(fmt, R, K, n):
 @pytest.mark.parametrize("R,K,sizes", [
     (128, 256, [0, 1, 0, 5, 2, 0]), (256, 512, [0] * 30 + [1] + [0] * 33), (128, 96, [31, 32, 33, 64, 65]),
     (256, 1024, [7] * 9), (128, 512, [0, 300, 0, 1, 200, 17]), (384, 2048, [130, 259, 5, 0]),
-    (128, 64, [1] * 1024), (4096, 256, [1, 0, 0, 1, 1, 0, 2, 0] * 4)])
+    (128, 64, [1] * 1024), (4096, 256, [1, 0, 0, 1, 1, 0, 2, 0] * 4),
+    (1792, 256, [0, 300, 0, 1, 200, 17]), (1920, 512, [0, 300, 0, 1, 200, 17]),     # pairs
+    (2688, 2048, [130, 259, 5, 0]), (256, 160, [33] * 45), (128, 320, [40, 0, 225, 3] * 12)])
 def test_product_groups(fmt, R, K, sizes):
     for yt in (F, B):
         check_product(fmt, len(sizes), R, K, sizes, yt, seed=len(sizes))
@@ -206,6 +211,7 @@ def test_product_accuracy(fmt):
     """The sum over 6144 columns in f32: near the rounding of one f32 sum, for few and many rows."""
     assert check_product(fmt, 1, 256, 6144, [5]) <= 5e-6
     assert check_product(fmt, 1, 256, 6144, [300]) <= 5e-6
+    assert check_product(fmt, 1, 10240, 6144, [60]) <= 5e-6
 
 
 def test_product_nan_scale_stays_in_its_row():
@@ -228,26 +234,27 @@ def test_product_offsets_out_of_range_stay_in_bounds():
     assert torch.equal(good, same)
 
 
-def test_product_is_the_same_every_time():
+@pytest.mark.parametrize("R", [256, 1408])
+def test_product_is_the_same_every_time(R):
     rng = np.random.default_rng(10)
     xc, xb = weights("mx", 700, 1024, rng)
-    wc, wb = weights("mx", 8 * 256, 1024, rng)
+    wc, wb = weights("mx", 8 * R, 1024, rng)
     off = [0, 100, 100, 350, 360, 400, 650, 651, 700]
-    a = product("mx", xc, xb, wc, wb, 8, 256, off, None, F, 700, 1024)
+    a = product("mx", xc, xb, wc, wb, 8, R, off, None, F, 700, 1024)
     for _ in range(3):
-        assert torch.equal(a, product("mx", xc, xb, wc, wb, 8, 256, off, None, F, 700, 1024))
-    assert float((a[400:650] - product("mx", xc[400:650], xb[400:650], wc[5 * 256:6 * 256], wb[5 * 256:6 * 256], 1, 256,
+        assert torch.equal(a, product("mx", xc, xb, wc, wb, 8, R, off, None, F, 700, 1024))
+    assert float((a[400:650] - product("mx", xc[400:650], xb[400:650], wc[5 * R:6 * R], wb[5 * R:6 * R], 1, R,
                                        None, None, F, 250, 1024)).abs().max()) <= 1e-5 * float(a.abs().max())
 
 
 def test_product_one_expert_with_offsets():
     """E = 1 with offsets: only the rows they name."""
     rng = np.random.default_rng(11)
-    for P in (20, 90):
+    for P, R in ((20, 128), (90, 128), (90, 10240)):
         xc, xb = weights("mx", P, 256, rng)
-        wc, wb = weights("mx", 128, 256, rng)
-        all_rows = product("mx", xc, xb, wc, wb, 1, 128, None, None, F, P, 256)
-        some = product("mx", xc, xb, wc, wb, 1, 128, [3, P - 5], None, F, P, 256)
+        wc, wb = weights("mx", R, 256, rng)
+        all_rows = product("mx", xc, xb, wc, wb, 1, R, None, None, F, P, 256)
+        some = product("mx", xc, xb, wc, wb, 1, R, [3, P - 5], None, F, P, 256)
         assert (some[:3] == 9.0).all() and (some[P - 5:] == 9.0).all()
         X, W = dev(ff.values(xc, xb, "mx")), dev(ff.values(wc, wb, "mx"))
         want, size = X @ W.T, X.abs() @ W.abs().T
