@@ -431,8 +431,10 @@ int coli_moe_forward_noalloc(const coli_moe_layer* layer, const void* x,
  * coli_moe_combine -> coli_moe_block_norm.  (The source pages have no
  * counterpart to these calls.)
  *
- * Matrices are row-major and contiguous.  Unless a call says otherwise its
- * buffers must not overlap one another.  A call for zero tokens or rows
+ * Matrices are row-major and contiguous, and every buffer is aligned to its
+ * elements (COLI_E_INVAL otherwise).  Unless a call says otherwise its buffers must
+ * not overlap one another; calls that may run at the same time need a workspace
+ * each.  A call for zero tokens or rows
  * succeeds and writes nothing (coli_moe_sort writes its offsets). */
 
 /* Picks sorted by expert.  idx device i32 [T, k]: the experts of every token;

@@ -82,6 +82,8 @@ int rows_sum(const char* what, const void* o, coli_dtype ot, int T, int H, int k
     if (!type_ok(ot) || !type_ok(yt)) return fail(COLI_E_INVAL, "%s: bad dtype", what);
     if (T == 0) return COLI_OK;
     if (!o || !inv || !y) return fail(COLI_E_INVAL, "%s: NULL pointer", what);
+    const int os = type_size(ot), ys = type_size(yt), el = elements_ok(what, {{o, os}, {inv, 4}, {w, 4}, {residual, ys}, {y, ys}});
+    if (el) return el;
     if (ot == COLI_F32)
         return yt == COLI_F32 ? launch_rows_sum<float, float>(o, T, H, k, inv, w, residual, y, st)
                               : launch_rows_sum<float, __nv_bfloat16>(o, T, H, k, inv, w, residual, y, st);
@@ -288,6 +290,7 @@ int coli_moe_sort(const int32_t* idx, const float* w, int32_t T, int32_t k, int3
     if (!offsets || (T > 0 && (!idx || !inv))) return fail(COLI_E_INVAL, "sort: NULL pointer");
     if (need && (!ws || ws_bytes < need || !aligned(ws, 4)))
         return fail(COLI_E_WORKSPACE, "sort: workspace of %zu bytes, %zu needed", ws ? ws_bytes : 0, need);
+    if ((rc = elements_ok("sort", {{idx, 4}, {w, 4}, {offsets, 4}, {pair_tok, 4}, {pair_slot, 4}, {inv, 4}}))) return rc;
     const int64_t P = (int64_t)T * k;
     const int one_smem = (kSortWarps * E + E + 1) * 4, place_smem = one_smem + E * 4;
     if (P <= kSortOneCta) {
@@ -315,6 +318,7 @@ int coli_moe_dispatch(const void* x, coli_dtype xt, int32_t T, int32_t H, int32_
     if (!type_ok(xt)) return fail(COLI_E_INVAL, "dispatch: bad dtype");
     if (T == 0) return COLI_OK;
     if (!x || !inv || !xs) return fail(COLI_E_INVAL, "dispatch: NULL pointer");
+    if ((rc = elements_ok("dispatch", {{x, type_size(xt)}, {inv, 4}, {xs, type_size(xt)}}))) return rc;
     const int64_t bytes = (int64_t)H * type_size(xt);
     if (bytes % 16 == 0 && aligned(x, 16) && aligned(xs, 16))
         return launch_dispatch<uint4, 1>(x, T, (int)(bytes / 16), k, inv, xs, S(stream));
@@ -342,6 +346,9 @@ int coli_moe_combine_backward(const void* dy, coli_dtype yt, const void* o, coli
     if (!type_ok(ot) || !type_ok(yt)) return fail(COLI_E_INVAL, "combine_backward: bad dtype");
     if (T == 0) return COLI_OK;
     if (!dy || !inv || (!d_o && !dw) || (dw && !o)) return fail(COLI_E_INVAL, "combine_backward: NULL pointer");
+    if ((rc = elements_ok("combine_backward", {{dy, type_size(yt)}, {o, type_size(ot)}, {inv, 4}, {w, 4},
+                                               {d_o, type_size(ot)}, {dw, 4}})))
+        return rc;
     if (yt == COLI_F32)
         return ot == COLI_F32 ? launch_rows_sum_backward<float, float>(dy, o, T, H, k, inv, w, d_o, dw, S(stream))
                               : launch_rows_sum_backward<float, __nv_bfloat16>(dy, o, T, H, k, inv, w, d_o, dw, S(stream));
@@ -360,6 +367,9 @@ int coli_moe_block_norm(const coli_norm_desc* desc, const void* x, const void* o
     if (o && (desc->gate_kind != COLI_GATE_NONE) != (gate != nullptr))
         return fail(COLI_E_INVAL, "block_norm: gate and gate_kind disagree");
     const int xs = type_size(desc->xt), bs = type_size(desc->bt);
+    if ((rc = elements_ok("block_norm", {{x, xs}, {x_out, xs}, {o, bs}, {n_out, bs}, {desc->post_gain, 4},
+                                         {desc->pre_gain, 4}, {gate, 4}, {rstd_post, 4}, {rstd_pre, 4}})))
+        return rc;
     const int W = chunk_of<8>(desc->H, {{x, xs}, {x_out, xs}, {o, bs}, {n_out, bs}, {desc->post_gain, 4},
                                         {desc->pre_gain, 4}, {gate, 4}});
     const NormArgs a = norm_args(*desc, gate, T);
@@ -393,6 +403,11 @@ int coli_moe_block_norm_backward(const coli_norm_desc* desc, const void* x_out, 
     if ((dgate && (!o || desc->gate_kind == COLI_GATE_NONE)) || (dpost_gain && (!o || !desc->post_norm)) ||
         (dpre_gain && !dn))
         return fail(COLI_E_INVAL, "block_norm_backward: gradient of an input that this call does not have");
+    const int xs = type_size(desc->xt), bs = type_size(desc->bt);
+    if ((rc = elements_ok("block_norm_backward", {{x_out, xs}, {dx_out, xs}, {dx, xs}, {o, bs}, {dn, bs}, {d_o, bs},
+                                                  {desc->post_gain, 4}, {desc->pre_gain, 4}, {gate, 4}, {rstd_post, 4},
+                                                  {rstd_pre, 4}, {dpost_gain, 4}, {dgate, 4}, {dpre_gain, 4}})))
+        return rc;
     // sums over tokens: partial rows in the workspace, then the second kernel
     const bool channel = dgate && desc->gate_kind == COLI_GATE_CHANNEL;
     NormSums keep;
@@ -406,7 +421,6 @@ int coli_moe_block_norm_backward(const coli_norm_desc* desc, const void* x_out, 
     float* partial = static_cast<float*>(ws);
     int grid = 0;
     if (T > 0) {
-        const int xs = type_size(desc->xt), bs = type_size(desc->bt);
         const int W = chunk_of<8>(desc->H, {{x_out, xs}, {dx_out, xs}, {dx, xs}, {o, bs}, {dn, bs}, {d_o, bs},
                                             {desc->post_gain, 4}, {desc->pre_gain, 4}, {gate, 4}, {dgate, 4}});
         const NormArgs a = norm_args(*desc, gate, T);

@@ -121,7 +121,7 @@ int coli_moe_fp4_bytes(coli_fp4 fmt, int64_t rows, int32_t K, size_t* code_bytes
 int coli_moe_fp4_quantize(coli_fp4 fmt, const void* x, coli_dtype xt, int64_t n_src, int64_t rows, int32_t K,
                           coli_act act, const int32_t* src, const int32_t* count, const float* gscale, void* codes,
                           void* scales, void* values, coli_stream_t stream) {
-    const int rc = fp4_ok("fp4_quantize", fmt, rows, K);
+    int rc = fp4_ok("fp4_quantize", fmt, rows, K);
     if (rc) return rc;
     if (xt != COLI_F32 && xt != COLI_BF16) return fail(COLI_E_INVAL, "fp4_quantize: bad dtype");
     if (act != COLI_ACT_NONE && act != COLI_ACT_SWIGLU) return fail(COLI_E_INVAL, "fp4_quantize: bad act %d", (int)act);
@@ -132,6 +132,7 @@ int coli_moe_fp4_quantize(coli_fp4 fmt, const void* x, coli_dtype xt, int64_t n_
     if ((!x && n_src > 0) || !codes || !scales) return fail(COLI_E_INVAL, "fp4_quantize: NULL pointer");
     if (!aligned_to(x, 32) || !aligned_to(codes, 16) || !aligned_to(scales, 16) || !aligned_to(values, 32))
         return fail(COLI_E_INVAL, "fp4_quantize: x and values must be 32-byte aligned, codes and scales 16-byte");
+    if ((rc = elements_ok("fp4_quantize", {{src, 4}, {count, 4}, {gscale, 4}}))) return rc;
     Fp4QuantArgs a;
     a.n_src = n_src; a.rows = rows;
     a.K = K; a.words = words_of(fmt, K);
@@ -165,7 +166,7 @@ int coli_moe_fp4_product(coli_fp4 fmt, const void* x_codes, const void* x_scales
                          const void* w_codes, const void* w_scales, int32_t E, int32_t R, const int32_t* offsets,
                          const float* alpha, void* y, coli_dtype yt, void* ws, size_t ws_bytes, coli_stream_t stream) {
     size_t need;
-    const int rc = coli_moe_fp4_product_workspace_size(fmt, P, K, E, R, &need);
+    int rc = coli_moe_fp4_product_workspace_size(fmt, P, K, E, R, &need);
     if (rc) return rc;
     if (yt != COLI_F32 && yt != COLI_BF16) return fail(COLI_E_INVAL, "fp4_product: bad dtype");
     if (!offsets && E > 1) return fail(COLI_E_INVAL, "fp4_product: %d experts need offsets", E);
@@ -175,6 +176,7 @@ int coli_moe_fp4_product(coli_fp4 fmt, const void* x_codes, const void* x_scales
         return fail(COLI_E_INVAL, "fp4_product: codes and scales must be 16-byte aligned");
     if (!ws || ws_bytes < need || !aligned16(ws))
         return fail(COLI_E_WORKSPACE, "fp4_product: workspace of %zu bytes, %zu needed", ws ? ws_bytes : 0, need);
+    if ((rc = elements_ok("fp4_product", {{offsets, 4}, {alpha, 4}, {y, yt == COLI_F32 ? 4 : 2}}))) return rc;
     FpArgs a;
     a.xs = static_cast<const uint32_t*>(x_scales);
     a.ws = static_cast<const uint8_t*>(w_scales);

@@ -100,9 +100,10 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 // A lane holds 16 columns of a row (two or four loads of 16 or 32 bytes), a warp
 // 512: a block is one lane (NVFP4) or two, so its maximum takes at most one
 // shuffle.  Every warp of a CTA has one chunk of one of its rows: that hides the
-// loads better than a warp's loop over its row does.  Rows of 256 columns or
-// fewer share a warp (`lanes` to a row: 8, 16 or 32; a scale word is 4 or 8).  Bound by HBM (x once, codes, scales and
-// values once).
+// loads better than a warp's loop over its row does.  Rows of 256 columns or fewer
+// share a warp (`lanes` to a row: 8, 16 or 32; a scale word is 4 or 8).  Bound by HBM (x
+// once, codes, scales and values once) where values are written: 32768 x 6144 f32
+// 251 us, 6.8 TB/s; without them by its instructions: bf16 107 us, 4.8 TB/s.
 constexpr int kQuantCols = 512;
 constexpr int kQuantWarps = 16;  // of a CTA, at most
 
@@ -542,7 +543,9 @@ __device__ __forceinline__ bool fp_wait_flags(const uint64_t* flags, int64_t ste
             ok = false;
         }
     }
-    return __all_sync(0xffffffffu, ok);
+    ok = __all_sync(0xffffffffu, ok);
+    __syncwarp();  // what one lane has acquired, all lanes read
+    return ok;
 }
 
 template <int NT, bool NV, bool PAIR, typename YT>

@@ -7,8 +7,11 @@
 #include <cuda_runtime.h>
 
 #include <cstdarg>
+#include <cstdint>
 #include <cstdio>
+#include <initializer_list>
 #include <mutex>
+#include <utility>
 
 #include "coli_moe.h"
 
@@ -24,6 +27,14 @@ inline int fail(int code, const char* fmt, ...) {
     vsnprintf(g_err, sizeof(g_err), fmt, ap);
     va_end(ap);
     return code;
+}
+
+// every address a multiple of its elements' size (a kernel would fault on others)
+inline int elements_ok(const char* what, std::initializer_list<std::pair<const void*, int>> buffers) {
+    for (const auto& b : buffers)
+        if (reinterpret_cast<uintptr_t>(b.first) % b.second)
+            return fail(COLI_E_INVAL, "%s: a buffer's address is no multiple of its elements' %d bytes", what, b.second);
+    return COLI_OK;
 }
 
 inline int check_launch(const char* what) {

@@ -96,7 +96,6 @@ template <typename T, int N> __device__ __forceinline__ Vec<T, N> narrow(const F
     }
     return r;
 }
-template <typename T, int N> __device__ __forceinline__ F<N> ldf(const T* p) { return widen<T, N>(ldv<T, N>(p)); }
 template <typename T, int N> __device__ __forceinline__ void stf(T* p, const F<N>& a) { stv<T, N>(p, narrow<T, N>(a)); }
 
 // N elements of a row as N / W chunks of W neighbours, `stride` elements apart: W = N

@@ -119,6 +119,23 @@ def test_norm_refusals(name, good, change, want):
     assert cm.coli_moe_last_error()
 
 
+@pytest.mark.parametrize("name,good,buffers", [
+    ("coli_moe_sort", {**SORT, "w": A}, "idx w off tok slot inv"),
+    ("coli_moe_dispatch", DISPATCH, "x inv xs"),
+    ("coli_moe_dispatch_backward", DISPATCH, "x inv xs"),
+    ("coli_moe_combine", {**COMBINE, "res": A}, "o inv w res y"),
+    ("coli_moe_combine_backward", COMBINE_B, "dy o inv w do dw"),
+    ("coli_moe_fp4_quantize", {**QUANT, "fmt": 1, "src": A, "count": A, "g": A, "v": A}, "x src count g c sc v"),
+    ("coli_moe_fp4_product", {**PRODUCT, "al": A}, "xc xs wc ws off al y"),
+    ("coli_moe_block_norm", {**NORM, "rp": A, "rx": A}, "x o gate xo no rp rx"),
+    ("coli_moe_block_norm_backward", NORM_B, "xo o gate rp rx dxo dn dx do dpost dgate dpre"),
+])
+def test_addresses_between_elements_are_refused(name, good, buffers):
+    for b in buffers.split():
+        assert code(name, *{**good, b: A + 1}.values()) == INVAL, b
+        assert cm.coli_moe_last_error()
+
+
 def test_nothing_to_do_succeeds():
     assert code("coli_moe_dispatch", *{**DISPATCH, "T": 0, "x": None}.values()) == 0
     assert code("coli_moe_combine", *{**COMBINE, "T": 0}.values()) == 0
