@@ -60,12 +60,11 @@ int encode_codes_map(CUtensorMap* m, const void* base, int64_t rows, int K, int 
 }
 
 template <typename T>
-int launch_quantize(coli_fp4 fmt, coli_act act, dim3 grid, int threads, const Fp4QuantArgs& a, int warps, int rows_per,
-                    int lanes, const void* x, void* values, cudaStream_t st) {
+int launch_quantize(coli_fp4 fmt, coli_act act, dim3 grid, dim3 threads, const Fp4QuantArgs& a, int lg, const void* x, void* values, cudaStream_t st) {
     const bool nv = fmt == COLI_NVFP4, glu = act == COLI_ACT_SWIGLU;
     const auto kern = nv ? (glu ? fp4_quantize_kernel<T, true, true> : fp4_quantize_kernel<T, true, false>)
                          : (glu ? fp4_quantize_kernel<T, false, true> : fp4_quantize_kernel<T, false, false>);
-    return launch_pdl(kern, grid, threads, 0, st, "fp4 quantize", a, warps, rows_per, lanes, (const T*)x, (T*)values);
+    return launch_pdl(kern, grid, threads, 0, st, "fp4 quantize", a, lg, (const T*)x, (T*)values);
 }
 
 template <int NT, bool NV, bool PAIR, typename YT>
@@ -134,22 +133,22 @@ int coli_moe_fp4_quantize(coli_fp4 fmt, const void* x, coli_dtype xt, int64_t n_
         return fail(COLI_E_INVAL, "fp4_quantize: x and values must be 32-byte aligned, codes and scales 16-byte");
     if ((rc = elements_ok("fp4_quantize", {{src, 4}, {count, 4}, {gscale, 4}}))) return rc;
     Fp4QuantArgs a;
-    a.n_src = n_src; a.rows = rows;
-    a.K = K; a.words = words_of(fmt, K);
+    a.n_src = (uint32_t)std::min<int64_t>(n_src, (int64_t)1 << 31);  // src holds 31-bit indexes
+    a.rows = (int)rows; a.K = K; a.words = words_of(fmt, K);
     a.src = src; a.count = count; a.gscale = gscale;
     a.codes = static_cast<uint8_t*>(codes);
     a.scales = static_cast<uint32_t*>(scales);
     // a warp per chunk of a row, several rows to a CTA or a warp where they are short
-    const int lanes = K > 256 ? 32 : K > 128 ? 16 : 8;
+    const int lg = K > 256 ? 5 : K > 128 ? 4 : 3;
     const int chunks = (K + kQuantCols - 1) / kQuantCols;
     const int parts = (chunks + kQuantWarps - 1) / kQuantWarps, warps = (chunks + parts - 1) / parts;
     const int rows_per = std::max(1, 8 / warps);
-    const int cta_rows = rows_per * (32 / lanes);
+    const int cta_rows = rows_per << (5 - lg);
     const dim3 grid((unsigned)((rows + cta_rows - 1) / cta_rows), parts);
-    const int threads = 32 * warps * rows_per;
+    const dim3 threads(32 * warps, rows_per);
     if (xt == COLI_F32)
-        return launch_quantize<float>(fmt, act, grid, threads, a, warps, rows_per, lanes, x, values, S(stream));
-    return launch_quantize<__nv_bfloat16>(fmt, act, grid, threads, a, warps, rows_per, lanes, x, values, S(stream));
+        return launch_quantize<float>(fmt, act, grid, threads, a, lg, x, values, S(stream));
+    return launch_quantize<__nv_bfloat16>(fmt, act, grid, threads, a, lg, x, values, S(stream));
 }
 
 int coli_moe_fp4_product_workspace_size(coli_fp4 fmt, int64_t P, int32_t K, int32_t E, int32_t R, size_t* bytes) {

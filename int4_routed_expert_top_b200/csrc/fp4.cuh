@@ -63,8 +63,8 @@ namespace coli {
 // quantiser
 // ---------------------------------------------------------------------------
 struct Fp4QuantArgs {
-    int64_t n_src, rows;
-    int K, words;            // words: 4-block scale words per row
+    uint32_t n_src;          // of the source, 2^31 at most
+    int rows, K, words;      // words: 4-block scale words per row
     const int32_t* src;
     const int32_t* count;
     const float* gscale;
@@ -74,7 +74,7 @@ struct Fp4QuantArgs {
 
 // word index of the scales of (row r, blocks 4w .. 4w + 3)
 __device__ __forceinline__ int64_t scale_word(int64_t r, int w, int words) {
-    return ((r >> 7) * words + w) * 128 + (r & 31) * 4 + ((r >> 5) & 3);
+    return ((int64_t)(int)(r >> 7) * words + w) * 128 + ((int)r & 31) * 4 + ((int)(r >> 5) & 3);
 }
 
 // eight f32 to E2M1 (nearest, ties to even, saturating), the first in the lowest
@@ -101,30 +101,30 @@ __device__ __forceinline__ float max3_abs(float a, float b, float c) {
 // 512: a block is one lane (NVFP4) or two, so its maximum takes at most one
 // shuffle.  Every warp of a CTA has one chunk of one of its rows: that hides the
 // loads better than a warp's loop over its row does.  Rows of 256 columns or fewer
-// share a warp (`lanes` to a row: 8, 16 or 32; a scale word is 4 or 8).  Bound by HBM (x
+// share a warp (1 << lg lanes to a row: 8, 16 or 32; a scale word is 4 or 8).  Bound by HBM (x
 // once, codes, scales and values once) where values are written: 32768 x 6144 f32
-// 251 us, 6.8 TB/s; without them by its instructions: bf16 107 us, 4.8 TB/s.
+// 251 us, 6.8 TB/s; bf16 without them 84 us, 6.1 TB/s (107 us with rows and chunks
+// found by divisions and 64-bit indexes).
 constexpr int kQuantCols = 512;
 constexpr int kQuantWarps = 16;  // of a CTA, at most
 
 template <typename T, bool NV, bool GLU>
 __global__ void __launch_bounds__(32 * kQuantWarps)
-fp4_quantize_kernel(Fp4QuantArgs a, int warps, int rows_per, int lanes, const T* __restrict__ x,
-                    T* __restrict__ values) {
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, mine = warp / warps;
-    // rows_per rows of a warp each (or of `warps` warps), or 32 / lanes rows to a warp
-    const int64_t r = ((int64_t)blockIdx.x * rows_per + mine) * (32 / lanes) + lane / lanes;
-    const int c0 = ((int)blockIdx.y * warps + warp - mine * warps) * kQuantCols;
-    const int c = c0 + (lane & (lanes - 1)) * 16;
+fp4_quantize_kernel(Fp4QuantArgs a, int lg, const T* __restrict__ x, T* __restrict__ values) {
+    const int lane = threadIdx.x & 31;
+    // threadIdx.y: a row (or 32 >> lg rows of 1 << lg lanes); the warps along x: its chunks
+    const uint32_t r0 = (blockIdx.x * blockDim.y + threadIdx.y) << (5 - lg), r = r0 + (lane >> lg);
+    const int c0 = (int)(blockIdx.y * blockDim.x + (threadIdx.x & ~31u)) * (kQuantCols / 32);
+    const int c = c0 + (lane & ((1 << lg) - 1)) * 16;
     pdl_trigger();
     pdl_wait();
-    const int64_t rows = a.count ? min(a.rows, (int64_t)*a.count) : a.rows;
-    if (c0 >= a.K || r - lane / lanes >= rows) return;        // the whole warp
+    const uint32_t rows = a.count ? (uint32_t)max(min(a.rows, *a.count), 0) : (uint32_t)a.rows;
+    if (c0 >= a.K || r0 >= rows) return;               // the whole warp
     const bool live = r < rows, in = live && c < a.K;  // K is a multiple of 32: all 16 columns or none
-    const int64_t from = !live ? 0 : a.src ? a.src[r] : r;
+    const uint32_t from = !live ? 0 : a.src ? (uint32_t)a.src[r] : r;
     const float g = NV && a.gscale ? *a.gscale : 1.0f;
-    const bool read = in && from >= 0 && from < a.n_src;
-    const T* p = x + from * (GLU ? 2 * a.K : a.K) + c;
+    const bool read = in && from < a.n_src;            // a negative entry is 2^31 or more
+    const T* p = x + (int64_t)((uint64_t)from * (uint32_t)(GLU ? 2 * a.K : a.K)) + c;
     Vec<T, 8> raw[GLU ? 4 : 2];
 #pragma unroll
     for (int i = 0; i < (GLU ? 4 : 2); ++i) {
@@ -179,7 +179,8 @@ fp4_quantize_kernel(Fp4QuantArgs a, int warps, int rows_per, int lanes, const T*
     const int at = c / (64 * per);
     if (live && (lane & (4 * per - 1)) == 0 && at < a.words) a.scales[scale_word(r, at, a.words)] = word;
     if (!in) return;
-    *reinterpret_cast<uint2*>(a.codes + (r * a.K + c) / 2) = make_uint2(code[0], code[1]);
+    const int64_t at_c = (int64_t)((uint64_t)r * (uint32_t)a.K) + c;
+    *reinterpret_cast<uint2*>(a.codes + at_c / 2) = make_uint2(code[0], code[1]);
     if (values) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -192,7 +193,7 @@ fp4_quantize_kernel(Fp4QuantArgs a, int warps, int rows_per, int lanes, const T*
                 q.v[2 * i + 1] = __fmul_rn(__high2float(two), d);
                 if (bad) q.v[2 * i] = q.v[2 * i + 1] = __uint_as_float(0x7fc00000u);
             }
-            stf<T, 8>(values + r * a.K + c + 8 * h, q);
+            stf<T, 8>(values + at_c + 8 * h, q);
         }
     }
 }

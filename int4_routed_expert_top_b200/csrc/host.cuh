@@ -72,11 +72,11 @@ inline int set_smem(const void* fn, int bytes) {
 // kernel may start while that one finishes and waits (griddepcontrol.wait)
 // before it reads what that one wrote.
 template <typename... Args>
-inline int launch_pdl(void (*kern)(Args...), dim3 grid, int threads, int smem, cudaStream_t st,
+inline int launch_pdl(void (*kern)(Args...), dim3 grid, dim3 threads, int smem, cudaStream_t st,
                const char* what, Args... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
-    cfg.blockDim = dim3(threads);
+    cfg.blockDim = threads;
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];
