@@ -134,7 +134,7 @@ NormShape norm_shape(int H, int T, int W, bool backward) {
     NormShape s;
     s.W = W;
     const int vecs = (H + 7) / 8;
-    if (vecs <= 256 || (!backward && T < 2 * 148 && vecs <= 1024))
+    if (vecs <= (backward ? 768 : T < 2 * 148 ? 1024 : 256))
         s.N = 1;
     else
         s.N = vecs <= 2 * 256 ? 2 : vecs <= 3 * 512 ? 3 : 4;
@@ -186,7 +186,7 @@ int norm_backward_cluster(int grid) { return grid >= kNormCluster ? kNormCluster
 // most 16 CTAs, and their sums in 200 KB of shared memory)
 int norm_plain_ctas(const coli_norm_desc& d, int T) {
     const int threads = norm_shape(d.H, T, 1, true).threads;
-    return kNormSms * std::max(1, std::min({16, std::max(2, 1024 / threads), 200 * 1024 / (kNormSums * d.H * 4)}));
+    return kNormSms * std::max(1, std::min({16, 768 / threads, 200 * 1024 / (kNormKept * d.H * 4)}));
 }
 int norm_backward_grid(int T, int ctas) {
     const int grid = std::min(T, ctas);
@@ -195,17 +195,18 @@ int norm_backward_grid(int T, int ctas) {
 // CTAs of the ring form: as many per SM as have two stages with every input, at
 // most six, and two rows or more for each; 0 where that leaves none
 int norm_ring_ctas(const coli_norm_desc& d, int T) {
-    const int need = 3 * d.H * 4 + 2 * 2 * d.H * (type_size(d.xt) + type_size(d.bt));
+    const int need = 2 * d.H * 4 + 2 * 2 * d.H * (type_size(d.xt) + type_size(d.bt));
     const int per_sm = std::min({6, kNormRingBytes / need, T / (2 * kNormSms)});
     return d.H <= kNormRingMaxH && d.H % 8 == 0 ? per_sm * kNormSms : 0;
 }
 
 // the ring of a call: no stages where it does not apply
 NormRing norm_ring(const coli_norm_desc& d, int ctas, bool wide, bool x_out, bool dx_out, bool o, bool dn) {
-    NormRing r = {0, 0, {-1, -1, -1, -1}, {-1, -1, -1}, 0};
+    NormRing r = {0, 0, {-1, -1, -1, -1}, {-1, -1}, 0};
     if (!wide || ctas < 1) return r;
-    const bool vec[3] = {dn && d.pre_gain, o && d.post_norm && d.post_gain, o && d.gate_kind == COLI_GATE_CHANNEL};
-    for (int i = 0; i < 3; ++i) {
+    const bool vec[2] = {dn && d.pre_gain, o && d.gate_kind != COLI_GATE_FULL &&
+                                               ((d.post_norm && d.post_gain) || d.gate_kind == COLI_GATE_CHANNEL)};
+    for (int i = 0; i < 2; ++i) {
         if (!vec[i]) continue;
         r.gain[i] = r.first;
         r.first += d.H * 4;
@@ -218,7 +219,7 @@ NormRing norm_ring(const coli_norm_desc& d, int ctas, bool wide, bool x_out, boo
     }
     r.stages = std::min(kNormMaxStages, (kNormRingBytes / (ctas / kNormSms) - 1024 - r.first) / r.stage);
     // room for the sums at the end as well
-    if (r.stages < 2 || kNormSums * d.H * 4 > r.first + r.stages * r.stage) r.stages = 0;
+    if (r.stages < 2 || kNormKept * d.H * 4 > r.first + r.stages * r.stage) r.stages = 0;
     return r;
 }
 
@@ -229,7 +230,7 @@ struct NormBackward {
                       const void* dx_out, const void* dn, void* dx, void* d_o, float* dgate, float* partial, int grid,
                       cudaStream_t st) {
         const auto kern = block_norm_backward_kernel<XT, BT, W, N, RING>;
-        const int smem = RING ? ring.first + ring.stages * ring.stage : keep.n * a.H * 4;
+        const int smem = RING ? ring.first + ring.stages * ring.stage : std::min(keep.n, kNormKept) * a.H * 4;
         int rc = set_smem((const void*)kern, smem);
         if (rc) return rc;
         cudaLaunchConfig_t cfg = {};

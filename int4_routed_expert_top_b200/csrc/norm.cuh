@@ -36,6 +36,7 @@ namespace coli {
 
 constexpr int kNormMaxH = 16384;
 constexpr int kNormSums = 3;  // dpost_gain, dgate (channel gates), dpre_gain
+constexpr int kNormKept = 2;  // sums over tokens that a CTA keeps: z, of which the first two are made, and dpre_gain
 
 struct NormArgs {
     int H, T;
@@ -214,21 +215,21 @@ __device__ __forceinline__ void sum_add(float* sums, const Part<W>& p, int H, co
     }
 }
 
-// Where each sum lives among the kept ones, -1 for one that is not asked for.
+// Where each sum lives among the partial rows, -1 for one that is not asked for.
 struct NormSums {
     int at[kNormSums];
     int n;
 };
 
 // Shared memory of the ring form: the vectors of H that every row needs
-// (pre_gain, post_gain, a channel gate: in sum_at's order), then the stages, each
+// (pre_gain; w of the gradient, see below: in sum_at's order), then the stages, each
 // with the rows x_out, dx_out, o, dn one after the other.  What a call does not
 // have is not there.
 struct NormRing {
     int stages;
     int stage;          // bytes, a multiple of 16
     int off[4];         // of a row in its stage, -1: absent
-    int gain[3];        // of a vector, -1: absent
+    int gain[2];        // of a vector, -1: absent
     int first;          // of the first stage
 };
 constexpr int kNormMaxStages = 4;
@@ -245,9 +246,11 @@ __device__ __forceinline__ Vec<T, 8> lds_row(const uint8_t* row, int c) {
     return r;
 }
 
-// eight elements from column c of a vector kept in sum_at's order, 1 where there is none
-__device__ __forceinline__ F<8> lds_gain(const uint8_t* smem, int off, int c, int H) {
-    F<8> r = ones<8>();
+// eight elements from column c of a vector kept in sum_at's order, `fill` where there is none
+__device__ __forceinline__ F<8> lds_gain(const uint8_t* smem, int off, int c, int H, float fill) {
+    F<8> r;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) r.v[j] = fill;
     if (off >= 0) {
         const float* p = reinterpret_cast<const float*>(smem + off);
 #pragma unroll
@@ -259,50 +262,48 @@ __device__ __forceinline__ F<8> lds_gain(const uint8_t* smem, int off, int c, in
     return r;
 }
 
-// partial [clusters][sums.n][H]
+// One barrier a row.  With w = alpha gate post_gain (a token's gate g_t apart: w =
+// post_gain, c = alpha g_t; else c = 1), d' = dx' + r_x v and d = d' - r_x <v xh> xh,
+//   sum q oh = c (sum w oh d' - r_x <v xh> sum w oh xh)
+// so the three sums over the row are taken together, before d is known.  Of the sums
+// over tokens one, z = sum_t c d oh (c includes alpha gate where the gate is full),
+// makes two gradients where the gate is the same for every token: dpost_gain = alpha
+// gate z, dgate = alpha post_gain z.
+// partial [clusters][keep.n][H]
 template <typename XT, typename BT, int W, int N, bool RING>
-__global__ void __launch_bounds__(RING && N == 1 ? 768 : 512)
+__global__ void __launch_bounds__(N == 1 ? 768 : 512)
 block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x_out, const BT* o,
                            const float* rstd_post, const float* rstd_pre, const XT* dx_out, const BT* dn, XT* dx,
                            BT* d_o, float* dgate, float* partial) {
     extern __shared__ __align__(128) uint8_t nb_smem[];   // the ring, or the sums; at the end the sums
-    __shared__ float part[2][64];
+    __shared__ float part[2][96];                         // of even and odd rows
     __shared__ __align__(8) uint64_t full[kNormMaxStages];
     __shared__ float rstds[kNormMaxStages][2];
     float* sums = reinterpret_cast<float*>(nb_smem);
     static_assert(!RING || W == 8, "rows of the ring are read in vectors of eight");
     const int step = (int)blockDim.x * 8, c0 = (int)threadIdx.x * W;
-    float* s_of[kNormSums];
-#pragma unroll
-    for (int i = 0; i < kNormSums; ++i) s_of[i] = keep.at[i] >= 0 ? sums + keep.at[i] * a.H : nullptr;
-    F<8> acc[RING ? kNormSums : 1][RING ? N : 1];
+    const bool token = a.gate_kind == 2, full_gate = a.gate_kind == 3;
+    const bool keep_z = keep.at[0] >= 0 || keep.at[1] >= 0, keep_pre = keep.at[2] >= 0;
+    float* z_sums = sums;
+    float* pre_sums = sums + (keep_z ? a.H : 0);
+    const int kept = (keep_z ? 1 : 0) + (keep_pre ? 1 : 0);
+    F<8> z_acc[RING ? N : 1], pre_acc[RING ? N : 1];
     if (RING) {
 #pragma unroll
-        for (int k = 0; k < kNormSums; ++k)
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-            for (int i = 0; i < N; ++i)
-#pragma unroll
-                for (int j = 0; j < 8; ++j) acc[RING ? k : 0][RING ? i : 0].v[j] = 0.0f;
+            for (int j = 0; j < 8; ++j) z_acc[RING ? i : 0].v[j] = pre_acc[RING ? i : 0].v[j] = 0.0f;
         if (threadIdx.x == 0) {
             for (int i = 0; i < ring.stages; ++i) mbar_init(&full[i], 2);  // the rows, the two rstd
             fence_mbar_init();
         }
     } else {
-        for (int i = threadIdx.x; i < keep.n * a.H; i += blockDim.x) sums[i] = 0.0f;
+        for (int i = threadIdx.x; i < kept * a.H; i += blockDim.x) sums[i] = 0.0f;
     }
     __syncthreads();
-    // sum k += f * h
-    const auto add = [&](int k, int i, const Part<W>& p, const F<8>& f, const F<8>& h) {
-        if (!s_of[k]) return;
-        if (RING) {
-            F<8>& s = acc[RING ? k : 0][RING ? i : 0];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) s.v[j] = fmaf(f.v[j], h.v[j], s.v[j]);
-        } else {
-            sum_add<W>(s_of[k], p, a.H, f, h);
-        }
-    };
     const float inv_h = 1.0f / (float)a.H;
+    const float fill = token ? 1.0f : a.alpha;            // w without gains
+    const float* post_gain = a.post_norm ? a.post_gain : nullptr;
     // row t into stage `at` (one thread)
     const auto fetch = [&](int64_t t, int at) {
         if (t >= a.T) return;
@@ -323,29 +324,48 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
     if (RING) {
         if (threadIdx.x == 0)
             for (int i = 0; i < ring.stages; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
-        const float* from[3] = {a.pre_gain, a.post_gain, a.gate};
-#pragma unroll
-        for (int k = 0; k < 3; ++k)
-            if (ring.gain[k] >= 0)
-                for (int c = threadIdx.x; c < a.H; c += blockDim.x)
-                    reinterpret_cast<float*>(nb_smem + ring.gain[k])[sum_at<W>(c, a.H)] = from[k][c];
+        for (int c = threadIdx.x; c < a.H; c += blockDim.x) {
+            const int to = sum_at<W>(c, a.H);
+            if (ring.gain[0] >= 0) reinterpret_cast<float*>(nb_smem + ring.gain[0])[to] = a.pre_gain[c];
+            if (ring.gain[1] >= 0)
+                reinterpret_cast<float*>(nb_smem + ring.gain[1])[to] =
+                    fill * (a.gate_kind == 1 ? a.gate[c] : 1.0f) * (post_gain ? post_gain[c] : 1.0f);
+        }
         __syncthreads();
     }
-    int at = 0;
+    // w at this part of token t's row
+    const auto weight = [&](int64_t t, const Part<W>& p) {
+        if (RING && !full_gate) return lds_gain(nb_smem, ring.gain[1], p.c, a.H, fill);
+        F<8> w = gain_at<W>(post_gain, p, a.H);
+        if (a.gate_kind == 1 || full_gate) {
+            const F<8> g = gate_at<W>(a, t, p);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w.v[j] *= fill * g.v[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w.v[j] *= fill;
+        }
+        return w;
+    };
+    int at = 0, odd = 0;
     uint32_t phase = 0;
-    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x) {
+    for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, odd ^= 1) {
         const int64_t row = t * a.H;
         F<8> d[N];
         Cols<XT, 8, W> xv[N];
-        Cols<BT, 8, W> ov[N], gv[N];
-        float s1[1] = {0.0f};
-        float rx_t = 0.0f, ro_t = 1.0f;
+        Cols<BT, 8, W> ov[N];
+        float s[3] = {0.0f, 0.0f, 0.0f};  // v xh, w oh d', w oh xh
+        float rx = 0.0f, ro = 1.0f;
         const uint8_t* st = nb_smem + ring.first + at * ring.stage;
         // a copy that never lands (a wait of seconds) makes the row NaN
         bool landed = true;
         if (RING) landed = mbar_wait(&full[at], phase, nullptr);
-        if (dn) rx_t = RING ? rstds[at][0] : rstd_pre[t];
-        if (o && a.post_norm) ro_t = RING ? rstds[at][1] : rstd_post[t];
+        if (dn) rx = RING ? rstds[at][0] : rstd_pre[t];
+        if (o && a.post_norm) ro = RING ? rstds[at][1] : rstd_post[t];
+        const float c = token && o ? a.alpha * a.gate[t] : 1.0f;
+        Cols<BT, 8, W> gv[N];
+        constexpr bool keep_w = !RING && N <= 2;           // as registers allow
+        F<8> kept_w[keep_w ? N : 1];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const Part<W> p(c0, step, i);
@@ -371,29 +391,49 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
             }
             if (!landed) d[i].v[0] = __uint_as_float(0x7fc00000u);
         }
-        if (dn) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const Part<W> p(c0, step, i);
-                if (p.c >= a.H) continue;
+        for (int i = 0; i < N; ++i) {
+            const Part<W> p(c0, step, i);
+            if (p.c >= a.H) continue;
+            F<8> xh;
+            if (dn) {
                 F<8> pg;
-                if constexpr (RING) pg = lds_gain(nb_smem, ring.gain[0], p.c, a.H);
+                if constexpr (RING) pg = lds_gain(nb_smem, ring.gain[0], p.c, a.H, 1.0f);
                 else pg = gain_at<W>(a.pre_gain, p, a.H);
                 const F<8> xf = widen<XT, 8, W>(xv[i]), gf = widen<BT, 8, W>(gv[i]);
-                F<8> xh;
 #pragma unroll
                 for (int j = 0; j < 8; ++j) {
-                    xh.v[j] = xf.v[j] * rx_t;
+                    xh.v[j] = xf.v[j] * rx;
                     const float v = gf.v[j] * pg.v[j];
-                    s1[0] = fmaf(v, xh.v[j], s1[0]);
-                    d[i].v[j] = fmaf(rx_t, v, d[i].v[j]);
+                    s[0] = fmaf(v, xh.v[j], s[0]);
+                    d[i].v[j] = fmaf(rx, v, d[i].v[j]);
                 }
-                add(2, i, p, gf, xh);
+                if (keep_pre) {
+                    if constexpr (RING) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) pre_acc[i].v[j] = fmaf(gf.v[j], xh.v[j], pre_acc[i].v[j]);
+                    } else {
+                        sum_add<W>(pre_sums, p, a.H, gf, xh);
+                    }
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) xh.v[j] = 0.0f;
             }
-            cta_sum(s1, part[0]);
-        } else if (RING) {
-            __syncthreads();
+            if (o) {
+                const F<8> w = weight(t, p);
+                if (keep_w) kept_w[keep_w ? i : 0] = w;
+                const F<8> of = widen<BT, 8, W>(ov[i]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const float woh = of.v[j] * ro * w.v[j];
+                    s[1] = fmaf(woh, d[i].v[j], s[1]);
+                    s[2] = fmaf(woh, xh.v[j], s[2]);
+                }
+            }
         }
+        if (dn || (o && (a.post_norm || token))) cta_sum(s, part[odd]);
+        else if (RING) __syncthreads();
         // every thread has its part of the row: the stage takes the row that comes next in it
         if (RING) {
             if (threadIdx.x == 0) fetch(t + (int64_t)ring.stages * gridDim.x, at);
@@ -402,94 +442,77 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
                 phase ^= 1;
             }
         }
-        if (dn) {
-            const float m = -rx_t * rx_t * (s1[0] * inv_h);
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                if (c0 + i * step >= a.H) continue;
-                const F<8> xf = widen<XT, 8, W>(xv[i]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) d[i].v[j] = fmaf(m, xf.v[j], d[i].v[j]);
-            }
-        }
-        float s2[2] = {0.0f, 0.0f};  // q oh, u d
-        const bool token = dgate && a.gate_kind == 2;
+        const float mean = s[0] * inv_h;                  // <v xh>
+        const float s_q = fmaf(-rx * mean, s[2], s[1]);   // sum q oh, without c
+        if (o && token && dgate && threadIdx.x == 0) dgate[t] = a.alpha * s_q;
+        const float to_d = -rx * rx * mean;
+        const float c_ro = c * ro, to_o = -ro * ro * (c * s_q * inv_h);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const Part<W> p(c0, step, i);
             if (p.c >= a.H) continue;
+            if (dn) {
+                const F<8> xf = widen<XT, 8, W>(xv[i]);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) d[i].v[j] = fmaf(to_d, xf.v[j], d[i].v[j]);
+            }
             st_part<XT, W>(dx + row, p, a.H, d[i]);
             if (!o) continue;
-            F<8> g, pg;
-            if (RING && ring.gain[2] >= 0) g = lds_gain(nb_smem, ring.gain[2], p.c, a.H);
-            else g = gate_at<W>(a, t, p);
-            if constexpr (RING) pg = lds_gain(nb_smem, ring.gain[1], p.c, a.H);
-            else pg = a.post_norm ? gain_at<W>(a.post_gain, p, a.H) : ones<8>();
-            F<8> oh = widen<BT, 8, W>(ov[i]), u, e;
+            const F<8> w = keep_w ? kept_w[keep_w ? i : 0] : weight(t, p);
+            const F<8> of = widen<BT, 8, W>(ov[i]);
+            F<8> oh, r;  // c oh; the gradient of o
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
-                oh.v[j] *= ro_t;
-                u.v[j] = oh.v[j] * pg.v[j];
-                e.v[j] = d[i].v[j] * (a.alpha * g.v[j]);
+                oh.v[j] = of.v[j] * c_ro;
+                r.v[j] = fmaf(c_ro, w.v[j] * d[i].v[j], a.post_norm ? to_o * of.v[j] : 0.0f);
             }
-            if (token) {
+            st_part<BT, W>(d_o + row, p, a.H, r);
+            if (full_gate) {
+                const F<8> g = gate_at<W>(a, t, p), pg = gain_at<W>(post_gain, p, a.H);
+                if (dgate) {
+                    F<8> dg;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) s2[1] = fmaf(u.v[j], d[i].v[j], s2[1]);
+                    for (int j = 0; j < 8; ++j) dg.v[j] = a.alpha * (oh.v[j] * pg.v[j] * d[i].v[j]);
+                    st_part<float, W>(dgate + row, p, a.H, dg);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) oh.v[j] *= a.alpha * g.v[j];
             }
-            add(1, i, p, u, d[i]);  // times alpha at the end
-            add(0, i, p, e, oh);
-            if (dgate && a.gate_kind == 3) {
-                F<8> dg;
+            if (keep_z) {
+                if constexpr (RING) {
 #pragma unroll
-                for (int j = 0; j < 8; ++j) dg.v[j] = a.alpha * (u.v[j] * d[i].v[j]);
-                st_part<float, W>(dgate + row, p, a.H, dg);
-            }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                s2[0] = fmaf(e.v[j], u.v[j], s2[0]);
-                d[i].v[j] = e.v[j] * pg.v[j];  // q
+                    for (int j = 0; j < 8; ++j) z_acc[i].v[j] = fmaf(d[i].v[j], oh.v[j], z_acc[i].v[j]);
+                } else {
+                    sum_add<W>(z_sums, p, a.H, d[i], oh);
+                }
             }
         }
-        if (o) {
-            float m = 0.0f;
-            if (a.post_norm || token) {
-                cta_sum(s2, part[1]);
-                if (token && threadIdx.x == 0) dgate[t] = a.alpha * s2[1];
-                if (a.post_norm) m = -ro_t * (s2[0] * inv_h);
-            }
-#pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const Part<W> p(c0, step, i);
-                if (p.c >= a.H) continue;
-                F<8> r = widen<BT, 8, W>(ov[i]);
-#pragma unroll
-                for (int j = 0; j < 8; ++j) r.v[j] = ro_t * fmaf(m, r.v[j], d[i].v[j]);
-                st_part<BT, W>(d_o + row, p, a.H, r);
-            }
-        }
-        __syncthreads();  // part is free for the next row
     }
     if (keep.n == 0) return;
+    __syncthreads();
     if (RING) {  // every row has been read: the ring's memory takes the sums
 #pragma unroll
-        for (int k = 0; k < kNormSums; ++k)
+        for (int i = 0; i < N; ++i) {
+            const Part<W> p(c0, step, i);
+            if (p.c >= a.H) continue;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const Part<W> p(c0, step, i);
-                if (!s_of[k] || p.c >= a.H) continue;
-#pragma unroll
-                for (int j = 0; j < 8; ++j) s_of[k][sum_at<W>(p.c + j, a.H)] = acc[RING ? k : 0][RING ? i : 0].v[j];
+            for (int j = 0; j < 8; ++j) {
+                if (keep_z) z_sums[sum_at<W>(p.c + j, a.H)] = z_acc[RING ? i : 0].v[j];
+                if (keep_pre) pre_sums[sum_at<W>(p.c + j, a.H)] = pre_acc[RING ? i : 0].v[j];
             }
+        }
     }
     cluster_sync();
     const int cs = (int)cluster_size(), rank = (int)cluster_rank();
     float* mine = partial + (int64_t)(blockIdx.x / cs) * keep.n * a.H;
     for (int i = rank * (int)blockDim.x + (int)threadIdx.x; i < keep.n * a.H; i += cs * (int)blockDim.x) {
-        const int k = i / a.H, c = i - k * a.H;
-        const float* p = sums + k * a.H + sum_at<W>(c, a.H);
+        const int k = i / a.H, col = i - k * a.H;
+        const float* p = (k == keep.at[2] ? pre_sums : z_sums) + sum_at<W>(col, a.H);
         float s = 0.0f;
         for (int q = 0; q < cs; ++q) s += ld_cluster(p, q);
-        mine[i] = k == keep.at[1] ? a.alpha * s : s;  // dgate
+        if (k == keep.at[0] && !token && !full_gate) s *= a.alpha * (a.gate_kind == 1 ? a.gate[col] : 1.0f);
+        if (k == keep.at[1]) s *= a.alpha * (post_gain ? post_gain[col] : 1.0f);
+        mine[i] = s;
     }
     cluster_sync();  // no CTA leaves while another reads its sums
 }
