@@ -128,8 +128,11 @@ NormArgs norm_args(const coli_norm_desc& d, const float* gate, int T) {
 
 // neighbours of an access, vectors of eight per thread and threads of a row
 struct NormShape { int W, N, threads; };
-// Many tokens: about 256 threads a row, so that an SM holds several rows.  Few
-// (less than two rows per SM): one vector a thread (the time of one row is what counts).
+// Forward, many tokens: about 256 threads a row, so that an SM holds several rows; few
+// (less than two rows per SM): one vector a thread (the time of one row is what
+// counts).  Rows without 16-byte access need more registers a vector, so fewer vectors
+// (4000 x 6143, f32 stream: 111 us with two, 129 with three).  Backward: one vector a
+// thread where a CTA can be that large (the same rows: 194 us, with three 356).
 NormShape norm_shape(int H, int T, int W, bool backward) {
     NormShape s;
     s.W = W;
@@ -137,7 +140,7 @@ NormShape norm_shape(int H, int T, int W, bool backward) {
     if (vecs <= (backward ? 768 : T < 2 * 148 ? 1024 : 256))
         s.N = 1;
     else
-        s.N = vecs <= 2 * 256 ? 2 : vecs <= 3 * 512 ? 3 : 4;
+        s.N = vecs <= (W == 8 ? 512 : 1024) ? 2 : vecs <= 3 * 512 ? 3 : 4;
     s.threads = ((vecs + s.N - 1) / s.N + 31) / 32 * 32;
     return s;
 }
@@ -173,20 +176,21 @@ struct NormForward {
 };
 
 // The backward pass: with many tokens, CTAs whose rows come through a ring (their
-// sums over tokens fill the registers: 8192 columns at 512 threads); else two CTAs
-// per SM, so that one's loads cover the other's sums over the row.  Clusters of two add the sums over tokens before they leave an SM
-// (clusters of four leave SMs without a CTA where a GPC's number of them is no
+// sums over tokens fill the registers: 8192 columns at 512 threads); else as many CTAs
+// per SM as its registers hold.  Clusters of two add the sums over tokens before they
+// leave an SM (clusters of four leave SMs without a CTA where a GPC's number of them is no
 // multiple of four: the ring's 37 did not fit at once and took twice as long).
 constexpr int kNormSms = 148;
 constexpr int kNormRingMaxH = 8192;
 constexpr int kNormRingBytes = 224 * 1024;   // of an SM
 constexpr int kNormCluster = 2;
 int norm_backward_cluster(int grid) { return grid >= kNormCluster ? kNormCluster : 1; }
-// CTAs of the plain form: two per SM, more where rows are short (1024 threads, at
-// most 16 CTAs, and their sums in 200 KB of shared memory)
+// CTAs of the plain form: 768 threads per SM (80 registers each), at most 8 CTAs (4000
+// tokens of 130: 19 us, with 16 27 us, for the sums of every CTA are added up), and
+// their sums in 200 KB of shared memory
 int norm_plain_ctas(const coli_norm_desc& d, int T) {
     const int threads = norm_shape(d.H, T, 1, true).threads;
-    return kNormSms * std::max(1, std::min({16, 768 / threads, 200 * 1024 / (kNormKept * d.H * 4)}));
+    return kNormSms * std::max(1, std::min({8, 768 / threads, 200 * 1024 / (kNormKept * d.H * 4)}));
 }
 int norm_backward_grid(int T, int ctas) {
     const int grid = std::min(T, ctas);

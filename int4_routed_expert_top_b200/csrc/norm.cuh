@@ -19,12 +19,12 @@
 // of its CTA; the CTAs of a cluster then add theirs through distributed shared
 // memory, write one partial row, and a second kernel adds those: always in the
 // same order, so the result does not change between runs.
-// A row's four inputs and two barriers leave an SM waiting for HBM most of the
+// A row's four inputs and its barriers leave an SM waiting for HBM most of the
 // time if it only loads a row when it gets to it (4096 x 6144, f32 stream, bf16
 // blocks: 193 us).  With many tokens the rows therefore come through a ring in
-// shared memory: one thread issues the bulk copies of the rows ahead (110 us, 4.1
-// TB/s; what is left is the arithmetic, 15 operations and twice as many other
-// instructions per element).  The sums are then in registers.  Rows that leave no
+// shared memory: one thread issues the bulk copies of the rows ahead (90 us, 5.0
+// TB/s, with one barrier a row; with the two that follow the formulas 110 us).  The
+// sums are then in registers.  Rows that leave no
 // room for two stages, unaligned rows and few tokens take the loads as they come.
 // Forward: 8192 x 6144 bf16 78 us (5.2 TB/s), one token 3.0 us.
 #pragma once

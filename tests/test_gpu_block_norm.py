@@ -270,3 +270,27 @@ def test_unaligned_tensors_take_single_elements():
     cm.coli_moe_block_norm(c.desc, off(c.x), off(c.o), c.T, xo, n, gate=off(c.gate), rstd_post=rp, rstd_pre=rx)
     assert (xo.double() - want[0].double()).abs().max() <= 2.0 ** -7 * want[0].double().abs().max()
     check_backward(c)
+
+
+@pytest.mark.parametrize("gate", ["none", "channel", "token"])
+@pytest.mark.parametrize("T,H", [(3, 40), (2, 33), (700, 1024)])
+def test_infinities_of_a_block_without_its_norm_stay_where_they_are(T, H, gate):
+    # without post_norm the gradient of o does not depend on o: alpha gate dx, two or three
+    # products of f32 and one rounding, whatever o holds
+    c = Case(T, H, F, B, gate, post=False, gains=False)
+    c.o[:, 1::7] = float("inf")
+    c.o[:, 2::7] = float("nan")
+    dx, do = torch.empty_like(c.x), torch.empty_like(c.o)
+    cm.coli_moe_block_norm_backward(c.desc, None, c.o, T, c.dxo, None, dx, do, None, gate=c.gate)
+    assert torch.equal(dx, c.dxo)
+    want = c.desc.alpha * c.gate64() * c.dxo.double()
+    assert ((do.double() - want).abs() <= (3 * U24 + HALF[B] * 1.01) * want.abs() + 1e-30).all()
+    if gate == "channel":  # a channel's gate alone sees its own values
+        ws = torch.empty(cm.coli_moe_block_norm_backward_workspace_size(c.desc, T), dtype=torch.uint8, device="cuda")
+        dgate = torch.empty_like(c.gate)
+        cm.coli_moe_block_norm_backward(c.desc, None, c.o, T, c.dxo, None, dx, do, ws, gate=c.gate, dgate=dgate)
+        terms = c.desc.alpha * c.o.double() * c.dxo.double()
+        finite = torch.isfinite(c.o.float()).all(0)
+        assert torch.equal(torch.isfinite(dgate), finite)
+        err = (dgate.double() - terms.sum(0)).abs()[finite]
+        assert (err <= (T + 10) * U24 * terms.abs().sum(0)[finite]).all()
