@@ -113,50 +113,57 @@ block_norm_kernel(NormArgs a, const XT* x, const BT* o, XT* x_out, BT* n_out, fl
     const int step = (int)blockDim.x * 8, c0 = (int)threadIdx.x * W;
     pdl_trigger();
     pdl_wait();
+    // u gate alpha = o (r_o c) w, w = post_gain times a gate of the channels, c = alpha times a token's
+    const float* post_gain = a.post_norm ? a.post_gain : nullptr;
+    const auto weight = [&](const Part<W>& p) {
+        F<8> w = gain_at<W>(post_gain, p, a.H);
+        if (a.gate_kind == 1 || a.gate_kind == 3) {
+            const F<8> g = gate_at<W>(a, t, p);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) w.v[j] *= g.v[j];
+        }
+        return w;
+    };
     Cols<XT, 8, W> xv[N];
     Cols<BT, 8, W> ov[N];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const Part<W> p(c0, step, i);
+        if (p.c >= a.H) continue;
         if (o) ov[i] = ld_part<BT, W>(o + row, p, a.H);
         xv[i] = ld_part<XT, W>(x + row, p, a.H);
     }
-    F<8> early_post, early_gate, early_pre;  // N == 1: asked for before the sums
-    if (N == 1) {
+    F<8> early_w, early_pre;  // N == 1: asked for before the sums
+    if (N == 1 && c0 < a.H) {
         const Part<W> p(c0, step, 0);
-        if (o) {
-            early_gate = gate_at<W>(a, t, p);
-            if (a.post_norm) early_post = gain_at<W>(a.post_gain, p, a.H);
-        }
+        if (o) early_w = weight(p);
         if (n_out) early_pre = gain_at<W>(a.pre_gain, p, a.H);
     }
     float s[1] = {0.0f};
     if (o) {
-        float r = 1.0f;
+        float rc = a.alpha * (a.gate_kind == 2 ? a.gate[t] : 1.0f);
         if (a.post_norm) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
+                if (c0 + i * step >= a.H) continue;
                 const F<8> f = widen<BT, 8, W>(ov[i]);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) s[0] = fmaf(f.v[j], f.v[j], s[0]);
             }
             cta_sum(s, part[0]);
-            r = 1.0f / sqrtf(s[0] / (float)a.H + a.eps);
+            const float r = 1.0f / sqrtf(s[0] / (float)a.H + a.eps);
             if (rstd_post && threadIdx.x == 0) rstd_post[t] = r;
+            rc *= r;
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const Part<W> p(c0, step, i);
-            const F<8> g = N == 1 ? early_gate : gate_at<W>(a, t, p);
-            F<8> f = widen<BT, 8, W>(ov[i]);
-            if (a.post_norm) {
-                const F<8> pg = N == 1 ? early_post : gain_at<W>(a.post_gain, p, a.H);
+            if (p.c >= a.H) continue;
+            const F<8> w = N == 1 ? early_w : weight(p);
+            const F<8> of = widen<BT, 8, W>(ov[i]), xf = widen<XT, 8, W>(xv[i]);
+            F<8> f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) f.v[j] = f.v[j] * r * pg.v[j];
-            }
-            const F<8> xf = widen<XT, 8, W>(xv[i]);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) f.v[j] = fmaf(a.alpha * g.v[j], f.v[j], xf.v[j]);
+            for (int j = 0; j < 8; ++j) f.v[j] = fmaf(of.v[j] * rc, w.v[j], xf.v[j]);
             xv[i] = narrow_cols<XT, 8, W>(f);  // the stored value, which the norm below reads
             stc<XT, 8, W>(x_out + row, p.c, p.stride, a.H, xv[i]);
         }
@@ -166,6 +173,7 @@ block_norm_kernel(NormArgs a, const XT* x, const BT* o, XT* x_out, BT* n_out, fl
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const Part<W> p(c0, step, i);
+        if (p.c >= a.H) continue;
         const F<8> f = widen<XT, 8, W>(xv[i]);
 #pragma unroll
         for (int j = 0; j < 8; ++j)
@@ -177,6 +185,7 @@ block_norm_kernel(NormArgs a, const XT* x, const BT* o, XT* x_out, BT* n_out, fl
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const Part<W> p(c0, step, i);
+        if (p.c >= a.H) continue;
         const F<8> pg = N == 1 ? early_pre : gain_at<W>(a.pre_gain, p, a.H);
         F<8> f = widen<XT, 8, W>(xv[i]);
 #pragma unroll
