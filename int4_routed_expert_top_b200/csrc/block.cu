@@ -131,7 +131,7 @@ struct NormShape { int W, N, threads; };
 // Forward, many tokens: about 256 threads a row, so that an SM holds several rows; few
 // (less than two rows per SM): one vector a thread (the time of one row is what
 // counts).  Rows without 16-byte access need more registers a vector, so fewer vectors
-// (4000 x 6143, f32 stream: 111 us with two, 129 with three).  Backward: one vector a
+// (4000 x 6143, f32 stream: 85 us with two, 97 with three).  Backward: one vector a
 // thread where a CTA can be that large (the same rows: 194 us, with three 356).
 NormShape norm_shape(int H, int T, int W, bool backward) {
     NormShape s;
@@ -208,8 +208,7 @@ int norm_ring_ctas(const coli_norm_desc& d, int T) {
 NormRing norm_ring(const coli_norm_desc& d, int ctas, bool wide, bool x_out, bool dx_out, bool o, bool dn) {
     NormRing r = {0, 0, {-1, -1, -1, -1}, {-1, -1}, 0};
     if (!wide || ctas < 1) return r;
-    const bool vec[2] = {dn && d.pre_gain, o && d.gate_kind != COLI_GATE_FULL &&
-                                               ((d.post_norm && d.post_gain) || d.gate_kind == COLI_GATE_CHANNEL)};
+    const bool vec[2] = {dn, o && d.gate_kind != COLI_GATE_FULL};
     for (int i = 0; i < 2; ++i) {
         if (!vec[i]) continue;
         r.gain[i] = r.first;

@@ -22,11 +22,12 @@
 // A row's four inputs and its barriers leave an SM waiting for HBM most of the
 // time if it only loads a row when it gets to it (4096 x 6144, f32 stream, bf16
 // blocks: 193 us).  With many tokens the rows therefore come through a ring in
-// shared memory: one thread issues the bulk copies of the rows ahead (90 us, 5.0
+// shared memory: one thread issues the bulk copies of the rows ahead (88 us, 5.2
 // TB/s, with one barrier a row; with the two that follow the formulas 110 us).  The
 // sums are then in registers.  Rows that leave no
 // room for two stages, unaligned rows and few tokens take the loads as they come.
-// Forward: 8192 x 6144 bf16 78 us (5.2 TB/s), one token 3.0 us.
+// Forward: 8192 x 6144 bf16 66 us (6.1 TB/s; 78 us with columns past the row filled in
+// after every load), one token 2.9 us.
 #pragma once
 
 #include "pipeline.cuh"
@@ -255,18 +256,14 @@ __device__ __forceinline__ Vec<T, 8> lds_row(const uint8_t* row, int c) {
     return r;
 }
 
-// eight elements from column c of a vector kept in sum_at's order, `fill` where there is none
-__device__ __forceinline__ F<8> lds_gain(const uint8_t* smem, int off, int c, int H, float fill) {
+// eight elements from column c of a vector kept in sum_at's order
+__device__ __forceinline__ F<8> lds_gain(const uint8_t* smem, int off, int c, int H) {
     F<8> r;
+    const float* p = reinterpret_cast<const float*>(smem + off);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) r.v[j] = fill;
-    if (off >= 0) {
-        const float* p = reinterpret_cast<const float*>(smem + off);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const float4 v = *reinterpret_cast<const float4*>(p + sum_at<8>(c + 4 * h, H));
-            r.v[4 * h] = v.x; r.v[4 * h + 1] = v.y; r.v[4 * h + 2] = v.z; r.v[4 * h + 3] = v.w;
-        }
+    for (int h = 0; h < 2; ++h) {
+        const float4 v = *reinterpret_cast<const float4*>(p + sum_at<8>(c + 4 * h, H));
+        r.v[4 * h] = v.x; r.v[4 * h + 1] = v.y; r.v[4 * h + 2] = v.z; r.v[4 * h + 3] = v.w;
     }
     return r;
 }
@@ -335,7 +332,7 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
             for (int i = 0; i < ring.stages; ++i) fetch(blockIdx.x + (int64_t)i * gridDim.x, i);
         for (int c = threadIdx.x; c < a.H; c += blockDim.x) {
             const int to = sum_at<W>(c, a.H);
-            if (ring.gain[0] >= 0) reinterpret_cast<float*>(nb_smem + ring.gain[0])[to] = a.pre_gain[c];
+            if (ring.gain[0] >= 0) reinterpret_cast<float*>(nb_smem + ring.gain[0])[to] = a.pre_gain ? a.pre_gain[c] : 1.0f;
             if (ring.gain[1] >= 0)
                 reinterpret_cast<float*>(nb_smem + ring.gain[1])[to] =
                     fill * (a.gate_kind == 1 ? a.gate[c] : 1.0f) * (post_gain ? post_gain[c] : 1.0f);
@@ -344,7 +341,7 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
     }
     // w at this part of token t's row
     const auto weight = [&](int64_t t, const Part<W>& p) {
-        if (RING && !full_gate) return lds_gain(nb_smem, ring.gain[1], p.c, a.H, fill);
+        if (RING && !full_gate) return lds_gain(nb_smem, ring.gain[1], p.c, a.H);
         F<8> w = gain_at<W>(post_gain, p, a.H);
         if (a.gate_kind == 1 || full_gate) {
             const F<8> g = gate_at<W>(a, t, p);
@@ -407,7 +404,7 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
             F<8> xh;
             if (dn) {
                 F<8> pg;
-                if constexpr (RING) pg = lds_gain(nb_smem, ring.gain[0], p.c, a.H, 1.0f);
+                if constexpr (RING) pg = lds_gain(nb_smem, ring.gain[0], p.c, a.H);
                 else pg = gain_at<W>(a.pre_gain, p, a.H);
                 const F<8> xf = widen<XT, 8, W>(xv[i]), gf = widen<BT, 8, W>(gv[i]);
 #pragma unroll
