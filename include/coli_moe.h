@@ -449,7 +449,8 @@ int coli_moe_forward_noalloc(const coli_moe_layer* layer, const void* x,
  *   inv [T, k]       row of each pick, -1 for a pick not computed
  * Unlike coli_moe_union there is no limit from E * T: 1 <= k <= 32, 1 <= E <=
  * 1024, T * k <= 2^30.  ws: device, coli_moe_sort_workspace_size bytes, 4-byte
- * aligned. */
+ * aligned; one made for the largest T serves every smaller one (as do those of
+ * the calls below). */
 int coli_moe_sort_workspace_size(int32_t T, int32_t k, int32_t E, size_t* bytes);
 int coli_moe_sort(const int32_t* idx, const float* w, int32_t T, int32_t k, int32_t E,
                   int32_t* offsets, int32_t* pair_tok, int32_t* pair_slot, int32_t* inv,

@@ -280,8 +280,10 @@ int coli_moe_sort_workspace_size(int32_t T, int32_t k, int32_t E, size_t* bytes)
     const int rc = picks_ok("sort_workspace_size", T, k);
     if (rc) return rc;
     if (E < 1 || E > 1024) return fail(COLI_E_INVAL, "sort_workspace_size: E=%d outside [1, 1024]", E);
-    const int64_t P = (int64_t)T * k;
-    *bytes = P <= kSortOneCta ? 0 : (size_t)((P + sort_chunk(P) - 1) / sort_chunk(P)) * E * 4;
+    // counts of the most chunks that P picks or fewer are cut into: a chunk grows by whole groups of
+    // picks, so that a few more picks may need fewer chunks, and a workspace for P serves fewer too
+    const int64_t P = (int64_t)T * k, group = 32 * kSortWarps;
+    *bytes = P <= kSortOneCta ? 0 : (size_t)std::min<int64_t>((P + group - 1) / group, kSortMaxChunks) * E * 4;
     return COLI_OK;
 }
 

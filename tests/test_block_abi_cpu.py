@@ -184,3 +184,29 @@ def test_plain_format_round_trip_and_layout():
         err = np.abs(val - x)
         d = np.repeat(np.abs(x).reshape(133, -1, ff.BLOCK[fmt]).max(2), ff.BLOCK[fmt], 1)
         assert (err <= 0.26 * d).all()
+
+
+def never_smaller(sizes):
+    return all(a <= b for a, b in zip(sizes, sizes[1:]))
+
+
+@pytest.mark.parametrize("k,E", [(1, 8), (8, 256), (10, 512), (32, 1024)])
+def test_sort_workspace_of_more_tokens_serves_fewer(k, E):
+    """A workspace made once for the largest batch takes every smaller one."""
+    around = sorted({max(0, n // k + d) for n in (0, 512, 1024, 2048, 32768, 65536, 98304, 1 << 20) for d in range(-3, 4)}
+                    | set(range(2000, 8300)))
+    assert never_smaller([cm.coli_moe_sort_workspace_size(T, k, E) for T in around])
+
+
+def test_product_workspace_of_more_rows_serves_fewer():
+    for E, R, K in ((1, 1, 32), (1, 4096, 6144), (1, 10240, 256), (32, 4096, 6144), (256, 128, 64), (1024, 128, 32)):
+        rows = sorted({n + d for n in (1, 32, 224, 448, 1000, 7168, 32 * E, 224 * E, 30000, 1 << 24) for d in range(0, 3)}
+                      | set(range(0, 3000, 7)))
+        assert never_smaller([cm.coli_moe_fp4_product_workspace_size(cm.COLI_NVFP4, P, K, E, R) for P in rows])
+
+
+@pytest.mark.parametrize("H", [1, 8, 64, 130, 1024, 6143, 6144, 8192, 8200, 16384])
+@pytest.mark.parametrize("xt,bt", [(0, 0), (0, 1), (1, 1)])
+def test_norm_gradient_workspace_of_more_tokens_serves_fewer(H, xt, bt):
+    desc = cm.NormDesc(H, xt, bt, 1, cm.COLI_GATE_CHANNEL, 1.0, 1e-5, None, None)
+    assert never_smaller([cm.coli_moe_block_norm_backward_workspace_size(desc, T) for T in range(0, 2000)])

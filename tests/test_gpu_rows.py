@@ -83,6 +83,19 @@ def test_sort_all_to_one_expert_and_no_outputs_but_inv():
     assert torch.equal(off, off2) and torch.equal(inv, inv2)
 
 
+def test_sort_workspace_made_once_for_the_largest_batch():
+    """4097 tokens x 8 picks are cut into 33 chunks, 4096 into 64: one workspace for both."""
+    k, E = 8, 64
+    ws = torch.empty(cm.coli_moe_sort_workspace_size(4097, k, E), dtype=torch.uint8, device="cuda")
+    for T in (4097, 4096, 2113, 129, 128):
+        idx = picks(T, k, E, 0.1, T)
+        off, inv = torch.empty(E + 1, dtype=torch.int32, device="cuda"), torch.empty(T, k, dtype=torch.int32, device="cuda")
+        cm.coli_moe_sort(torch.from_numpy(idx).cuda(), T, k, E, off, None, None, inv, ws)
+        off0, _, inv0 = plain_sort(idx, E)
+        np.testing.assert_array_equal(off.cpu().numpy(), off0)
+        np.testing.assert_array_equal(inv.cpu().numpy(), inv0)
+
+
 def test_sort_of_no_tokens():
     off = torch.full((5,), -7, dtype=torch.int32, device="cuda")
     z = torch.empty(0, dtype=torch.int32, device="cuda")
