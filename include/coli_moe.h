@@ -434,8 +434,10 @@ int coli_moe_forward_noalloc(const coli_moe_layer* layer, const void* x,
  * Matrices are row-major and contiguous, and every buffer is aligned to its
  * elements (COLI_E_INVAL otherwise).  Unless a call says otherwise its buffers must
  * not overlap one another; calls that may run at the same time need a workspace
- * each.  A call for zero tokens or rows
- * succeeds and writes nothing (coli_moe_sort writes its offsets). */
+ * each.  A call for zero tokens or rows succeeds, takes NULL for every buffer
+ * that would hold none, and writes only what does not shrink with them:
+ * coli_moe_sort its offsets, coli_moe_block_norm_backward zeros (sums over no
+ * tokens) in dpost_gain, dpre_gain and a channel gate's dgate. */
 
 /* Picks sorted by expert.  idx device i32 [T, k]: the experts of every token;
  * a pick is computed when 0 <= idx < E and, with w (device f32 [T, k] or

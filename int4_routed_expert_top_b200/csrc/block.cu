@@ -401,13 +401,16 @@ int coli_moe_block_norm_backward(const coli_norm_desc* desc, const void* x_out, 
     int rc = norm_ok("block_norm_backward", desc, T);
     if (rc) return rc;
     if ((rc = coli_moe_block_norm_backward_workspace_size(desc, T, &need))) return rc;
-    if (!dx || (!dx_out && !dn) || (dn && (!x_out || !rstd_pre)) || (o != nullptr) != (d_o != nullptr) ||
-        (o && desc->post_norm && !rstd_post))
-        return fail(COLI_E_INVAL, "block_norm_backward: NULL pointer");
-    if (o && (desc->gate_kind != COLI_GATE_NONE) != (gate != nullptr))
-        return fail(COLI_E_INVAL, "block_norm_backward: gate and gate_kind disagree");
-    if ((dgate && (!o || desc->gate_kind == COLI_GATE_NONE)) || (dpost_gain && (!o || !desc->post_norm)) ||
-        (dpre_gain && !dn))
+    // zero tokens: empty tensors have no address, so only what the sums over tokens go to is looked at
+    if (T > 0) {
+        if (!dx || (!dx_out && !dn) || (dn && (!x_out || !rstd_pre)) || (o != nullptr) != (d_o != nullptr) ||
+            (o && desc->post_norm && !rstd_post))
+            return fail(COLI_E_INVAL, "block_norm_backward: NULL pointer");
+        if (o && (desc->gate_kind != COLI_GATE_NONE) != (gate != nullptr))
+            return fail(COLI_E_INVAL, "block_norm_backward: gate and gate_kind disagree");
+    }
+    if ((dgate && ((T > 0 && !o) || desc->gate_kind == COLI_GATE_NONE)) ||
+        (dpost_gain && ((T > 0 && !o) || !desc->post_norm)) || (dpre_gain && T > 0 && !dn))
         return fail(COLI_E_INVAL, "block_norm_backward: gradient of an input that this call does not have");
     const int xs = type_size(desc->xt), bs = type_size(desc->bt);
     if ((rc = elements_ok("block_norm_backward", {{x_out, xs}, {dx_out, xs}, {dx, xs}, {o, bs}, {dn, bs}, {d_o, bs},
@@ -421,7 +424,7 @@ int coli_moe_block_norm_backward(const coli_norm_desc* desc, const void* x_out, 
     keep.at[0] = dpost_gain ? keep.n++ : -1;
     keep.at[1] = channel ? keep.n++ : -1;
     keep.at[2] = dpre_gain ? keep.n++ : -1;
-    if (keep.n && (!ws || ws_bytes < need || !aligned(ws, 16)))
+    if (keep.n && need && (!ws || ws_bytes < need || !aligned(ws, 16)))
         return fail(COLI_E_WORKSPACE, "block_norm_backward: workspace of %zu bytes, %zu needed", ws ? ws_bytes : 0,
                     need);
     float* partial = static_cast<float*>(ws);

@@ -210,3 +210,14 @@ def test_product_workspace_of_more_rows_serves_fewer():
 def test_norm_gradient_workspace_of_more_tokens_serves_fewer(H, xt, bt):
     desc = cm.NormDesc(H, xt, bt, 1, cm.COLI_GATE_CHANNEL, 1.0, 1e-5, None, None)
     assert never_smaller([cm.coli_moe_block_norm_backward_workspace_size(desc, T) for T in range(0, 2000)])
+
+
+def test_norm_gradient_of_no_tokens_needs_no_addresses():
+    """Empty tensors have no address: nothing but the sums over tokens is asked of the call."""
+    none = {**NORM_B, "T": 0, **{b: None for b in "xo o gate rp rx dxo dn dx do dpost dgate dpre ws".split()}, "n": 0}
+    for desc in (norm(gate_kind=0), norm(), norm(gate_kind=2), norm(gate_kind=3, post_norm=0)):
+        assert code("coli_moe_block_norm_backward", *{**none, "desc": desc}.values()) == 0
+    # what no tensor of any length could be is refused still
+    assert code("coli_moe_block_norm_backward", *{**none, "desc": norm(gate_kind=0), "dgate": A}.values()) == INVAL
+    assert code("coli_moe_block_norm_backward", *{**none, "desc": norm(post_norm=0), "dpost": A}.values()) == INVAL
+    assert code("coli_moe_block_norm_backward", *{**none, "dpre": A + 2}.values()) == INVAL

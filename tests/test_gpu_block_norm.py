@@ -248,6 +248,24 @@ def test_no_tokens():
     assert float(dgate.abs().sum() + dpost.abs().sum() + dpre.abs().sum()) == 0.0  # sums over no tokens
 
 
+@pytest.mark.parametrize("gate", ["none", "channel", "token", "full"])
+def test_an_empty_batch_forward_and_backward(gate):
+    """Empty tensors and no workspace, as a rank without tokens has them."""
+    c = Case(1, 64, F, F, gate)
+    e, r = torch.empty(0, 64, device="cuda"), torch.empty(0, device="cuda")
+    g = {"none": None, "channel": c.gate, "token": r, "full": e}[gate]
+    assert cm.coli_moe_block_norm_backward_workspace_size(c.desc, 0) == 0
+    dpost, dpre = (torch.full((64,), 9.0, device="cuda") for _ in range(2))
+    dgate = None if g is None else torch.full_like(g, 9.0)
+    cm.coli_moe_block_norm(c.desc, e, e, 0, e, e, gate=g, rstd_post=r, rstd_pre=r)
+    cm.coli_moe_block_norm_backward(c.desc, e, e, 0, e, e, e, e, None, gate=g, rstd_post=r, rstd_pre=r,
+                                    dpost_gain=dpost, dgate=dgate, dpre_gain=dpre)
+    for d in (dpost, dpre, dgate):
+        assert d is None or (d == 0).all()                   # sums over no tokens
+    cm.coli_moe_block_norm_backward(c.desc, e, e, 0, e, e, e, e, None, gate=g, rstd_post=r, rstd_pre=r)
+    cm.coli_moe_block_norm_backward(c.desc, e, None, 0, e, None, e, None, None)
+
+
 def test_unusual_rows():
     """A row of zeros, one of infinities and one with a NaN stay apart from their neighbours."""
     c = Case(5, 256, F, F, "none")
