@@ -40,7 +40,7 @@ int sm_count() {
 // pairs for 385 rows, 32 tiles; of 18944 x 6144: 43 and 15 us for 193 rows, 74 tiles).
 constexpr int kFpSmallNT = 32, kFpLargeNT = 224;
 bool pairs_apply(int64_t P, int E, int R) {
-    const int64_t tiles = E * ((R + 255) / 256) * ((P + (int64_t)kFpLargeNT * E - 1) / ((int64_t)kFpLargeNT * E));
+    const int64_t tiles = (int64_t)E * ((R - 1) / 256 + 1) * ((P + (int64_t)kFpLargeNT * E - 1) / ((int64_t)kFpLargeNT * E));
     return P > (int64_t)kFpSmallNT * E && tiles >= 40;
 }
 

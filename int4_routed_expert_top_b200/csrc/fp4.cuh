@@ -271,7 +271,7 @@ struct FpPlan {
 template <int NT, int M>
 __device__ __forceinline__ void fp_plan(const FpArgs& a, FpPlan& p) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int RT = (a.R + M - 1) / M;
+    const int RT = (a.R - 1) / M + 1;                     // R may be 2^31 - 1
     if (!a.offsets) {
         if (threadIdx.x == 0) {
             p.begin[0] = 0;
@@ -352,7 +352,7 @@ __device__ __noinline__ FpTile fp_tile(const FpPlan& p, int E, int64_t tile) {
     FpTile t;
     t.e = lo;
     const int rows = p.begin[lo + 1] - p.begin[lo];
-    const int nj = (rows + NT - 1) / NT;
+    const int nj = (rows - 1) / NT + 1;  // a tile's expert has rows, up to 2^31 - 1
     const int i = (int)(tile - p.tile0[lo]);
     t.rt = i / nj;
     const int j = i - t.rt * nj;
@@ -601,7 +601,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             // this CTA's share of the rows: half of N, itself a multiple of 16
             const int half = (t.n + C::step - 1) / C::step * 16;
             const int first = PAIR ? rank * half : 0, count = min(half, t.n - first);
-            const int p0 = uniform((int)t.p0 + first);
+            const int p0 = uniform((int)min(t.p0 + first, a.P - 1));  // past the last row: nothing to copy
             const int boxes = uniform(PAIR ? max(0, (count + C::box - 1) / C::box) : 1);
             const int wrow = uniform(t.e * a.R + t.rt * C::M + rank * 128);
             const int k0 = uniform(q.k0), k1 = uniform(q.k1);

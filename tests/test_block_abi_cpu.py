@@ -221,3 +221,12 @@ def test_norm_gradient_of_no_tokens_needs_no_addresses():
     assert code("coli_moe_block_norm_backward", *{**none, "desc": norm(gate_kind=0), "dgate": A}.values()) == INVAL
     assert code("coli_moe_block_norm_backward", *{**none, "desc": norm(post_norm=0), "dpost": A}.values()) == INVAL
     assert code("coli_moe_block_norm_backward", *{**none, "dpre": A + 2}.values()) == INVAL
+
+
+def test_product_sizes_up_to_31_bits():
+    """The number of row tiles of the largest matrices, in 64 bits: a pair of CTAs for each either way."""
+    most = 2 ** 31 - 1
+    pairs = cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, 40, 32, 1, 1 << 30)
+    assert pairs > cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, 32, 32, 1, 1 << 30)
+    assert cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, 40, 32, 1, most) == pairs
+    assert cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, most, 32, 1, 1) == pairs

@@ -281,3 +281,32 @@ def test_product_two_streams_at_once():
     torch.cuda.synchronize()
     for _, want, y, ws, _ in calls:
         assert cm.coli_moe_fp4_product_status(ws) == 0 and torch.equal(y, want)
+
+
+@pytest.mark.parametrize("P,R", [(2 ** 31 - 1, 1), (1, 2 ** 31 - 1), (33, 2 ** 26 + 1)])
+def test_product_of_the_most_rows(P, R):
+    """As many rows of either side as their 31 bits allow, a K of one block: zeros but for
+    the last rows (and one a third of the way), whose products are whole numbers."""
+    if torch.cuda.mem_get_info()[0] < 70 << 30:
+        pytest.skip("needs 70 GB")
+    K = 32
+
+    def side(n, seed):
+        nc, ns = cm.coli_moe_fp4_bytes(cm.COLI_MXFP4, n, K)
+        codes, scales = (torch.zeros(m, dtype=torch.uint8, device="cuda") for m in (nc, ns))
+        scales.view(-1, 4)[:, 0] = 127
+        at = sorted({n // 3, *range(max(0, n - 300), n)})
+        small = np.random.default_rng(seed).integers(0, 256, (len(at), K // 2)).astype(np.uint8)
+        codes.view(n, K // 2)[torch.tensor(at, device="cuda")] = dev(small)
+        return codes, scales, at, ff.values(small, np.full((len(at), 1), 127, np.uint8), "mx")
+    xc, xs, xat, X = side(P, 1)
+    wc, ws_, wat, W = side(R, 2)
+    y = torch.full((P, R), 9.0, dtype=B, device="cuda")
+    ws = torch.zeros(cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, P, K, 1, R), dtype=torch.uint8, device="cuda")
+    cm.coli_moe_fp4_product(cm.COLI_MXFP4, xc, xs, P, K, wc, ws_, 1, R, y, ws)
+    assert cm.coli_moe_fp4_product_status(ws) == 0
+    i, j = torch.tensor(xat, device="cuda"), torch.tensor(wat, device="cuda")
+    # sums of 32 multiples of 0.25 up to 36: exact in f32, so one rounding to bf16 and nothing else
+    assert torch.equal(y[i][:, j], dev((X @ W.T).astype(np.float32)).to(B))
+    y[i[:, None], j] = 0
+    assert int(torch.count_nonzero(y)) == 0
