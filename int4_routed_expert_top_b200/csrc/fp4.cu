@@ -59,6 +59,29 @@ int encode_codes_map(CUtensorMap* m, const void* base, int64_t rows, int K, int 
     return COLI_OK;
 }
 
+// scale tiles: rows of 512 bytes, boxes of box_rows
+int encode_scales_map(CUtensorMap* m, const void* base, int64_t rows, int box_rows) {
+    EncodeTiledFn fn = encode_fn();
+    if (!fn) return fail(COLI_E_CUDA, "cuTensorMapEncodeTiled is not available");
+    const cuuint64_t dims[2] = {128, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {512};
+    const cuuint32_t box[2] = {128, (cuuint32_t)box_rows};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT32, 2, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(COLI_E_CUDA, "scales tensor map encode failed (%d)", (int)r);
+    return COLI_OK;
+}
+
+// Row tiles of pairs at most, and the bytes of their scales (of a row: whole stages).
+int64_t pair_row_tiles(int64_t P, int E) { return P / kFpLargeNT + E; }
+size_t pair_scale_bytes(coli_fp4 fmt, int64_t P, int K, int E) {
+    const int64_t words = (int64_t)((K + 255) / 256) * (fmt == COLI_NVFP4 ? 4 : 2);
+    return (size_t)(pair_row_tiles(P, E) * words * ((kFpLargeNT + 127) / 128) * 512);
+}
+size_t partial_bytes(int NT) { return (size_t)kFpMaxGrid * 128 * NT * 4; }
+
 template <typename T>
 int launch_quantize(coli_fp4 fmt, coli_act act, dim3 grid, dim3 threads, const Fp4QuantArgs& a, int lg, const void* x, void* values, cudaStream_t st) {
     const bool nv = fmt == COLI_NVFP4, glu = act == COLI_ACT_SWIGLU;
@@ -71,10 +94,20 @@ template <int NT, bool NV, bool PAIR, typename YT>
 int launch_product(const FpArgs& a, const void* x_codes, const void* w_codes, void* y, cudaStream_t st) {
     using C = FpShape<NT, NV, PAIR>;
     const auto kern = fp4_product_kernel<NT, NV, PAIR, YT>;
-    CUtensorMap wmap, xmap;
+    FpMaps<PAIR> maps;
     int rc;
-    if ((rc = encode_codes_map(&wmap, w_codes, (int64_t)a.E * a.R, a.K, 128))) return rc;
-    if ((rc = encode_codes_map(&xmap, x_codes, a.P, a.K, C::box))) return rc;
+    if ((rc = encode_codes_map(&maps.w, w_codes, (int64_t)a.E * a.R, a.K, 128))) return rc;
+    if ((rc = encode_codes_map(&maps.x, x_codes, a.P, a.K, C::box))) return rc;
+    if constexpr (PAIR) {
+        const int64_t blocks = ((int64_t)a.E * a.R + 127) / 128, words = (int64_t)a.KS * C::atoms;
+        if ((rc = encode_scales_map(&maps.ws, a.ws, blocks * a.wwords, C::atoms))) return rc;
+        if ((rc = encode_scales_map(&maps.xs, a.xtiles, a.max_xtiles * words * C::nb, C::atoms * C::nb))) return rc;
+        // a warp per two words of a tile, as many as the SMs hold at once
+        const int64_t ctas = (a.max_xtiles * words / 2 + 7) / 8;
+        if ((rc = launch_pdl(fp4_tile_scales_kernel<NT, C::M, C::nb>, dim3((unsigned)std::min<int64_t>(ctas, 8 * 148)),
+                             kFpTileScaleThreads, 0, st, "fp4 product scales", a, (int)words)))
+            return rc;
+    }
     if ((rc = set_smem((const void*)kern, C::smem))) return rc;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(std::min(sm_count(), kFpMaxGrid) / C::ctas * C::ctas);
@@ -89,7 +122,7 @@ int launch_product(const FpArgs& a, const void* x_codes, const void* w_codes, vo
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = PAIR ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, wmap, xmap, a, (YT*)y);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, maps, a, (YT*)y);
     if (e != cudaSuccess) return fail(COLI_E_CUDA, "fp4 product: %s", cudaGetErrorString(e));
     return check_launch("fp4 product");
 }
@@ -157,7 +190,8 @@ int coli_moe_fp4_product_workspace_size(coli_fp4 fmt, int64_t P, int32_t K, int3
     if (!bytes) return fail(COLI_E_INVAL, "fp4_product_workspace_size: NULL pointer");
     if (E < 1 || E > kFpMaxE || R < 1 || (E > 1 && R % 128) || (int64_t)E * R > INT32_MAX)
         return fail(COLI_E_INVAL, "fp4_product: bad sizes E=%d R=%d", E, R);
-    *bytes = kFpHeadBytes + (size_t)kFpMaxGrid * 128 * (pairs_apply(P, E, R) ? kFpLargeNT : kFpSmallNT) * 4;
+    *bytes = kFpHeadBytes + (pairs_apply(P, E, R) ? partial_bytes(kFpLargeNT) + pair_scale_bytes(fmt, P, K, E)
+                                                  : partial_bytes(kFpSmallNT));
     return COLI_OK;
 }
 
@@ -187,6 +221,8 @@ int coli_moe_fp4_product(coli_fp4 fmt, const void* x_codes, const void* x_scales
     a.err = static_cast<int32_t*>(ws);
     a.flags = reinterpret_cast<uint64_t*>(static_cast<char*>(ws) + kFpFlagBytes);
     a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kFpHeadBytes);
+    a.xtiles = reinterpret_cast<uint4*>(static_cast<char*>(ws) + kFpHeadBytes + partial_bytes(kFpLargeNT));  // pairs
+    a.max_xtiles = pair_row_tiles(P, E);
     if (pairs_apply(P, E, R)) return launch_product_t<kFpLargeNT, true>(fmt, yt, a, x_codes, w_codes, y, S(stream));
     return launch_product_t<kFpSmallNT, false>(fmt, yt, a, x_codes, w_codes, y, S(stream));
 }

@@ -44,11 +44,12 @@
 // codes zero: under sustained load the chip's power limit sets the clock (1.4 GHz).
 //
 // CTA roles: warp 0 copies (codes by 2-D TMA with the 128-byte swizzle, the
-// weights' scales by bulk copy), four warps bring the rows' scales (rows of an
-// expert start anywhere, a scale tile only at multiples of 128, so those are
-// gathered word by word into a tile in shared memory), warp 1 copies scales
-// to TMEM and issues the products, warps 4-7 store.  Accumulators are
-// double-buffered, so a tile's stores overlap the next one's products.
+// weights' scales by bulk copy), warp 1 copies scales to TMEM and issues the
+// products, warps 4-7 (of a pair also 8-11) store.  Rows of an expert start
+// anywhere, a scale tile only at multiples of 128, so the rows' scales are gathered
+// word by word: in a CTA by itself by four warps into a tile in shared memory, for pairs
+// by a kernel of its own before the product, whose tiles then come by TMA.  Accumulators
+// are double-buffered, so a tile's stores overlap the next one's products.
 #pragma once
 
 #include <cuda_fp4.h>
@@ -201,10 +202,11 @@ fp4_quantize_kernel(Fp4QuantArgs a, int lg, const T* __restrict__ x, T* __restri
 // ---------------------------------------------------------------------------
 // product
 // ---------------------------------------------------------------------------
-// warps 0 copies, 1 products, 2-3 and 8-9 scales of the rows, 4-7 and (for tiles of
-// many rows) 10-13 stores
+// warps 0 copies, 1 products, 4-7 stores; by itself 2-3 and 8-9 scales of the rows, in a pair
+// 8-11 stores as well
 constexpr int kFpScaleWarps = 4;
 constexpr int kFpStoreWarps = 8;   // at most
+constexpr int kFpMaxWarps = 12;
 constexpr int kFpMaxE = 1024;
 // Stages that a cut tile's pieces have at least: shorter ones save less than joining
 // them takes (8 rows, 20 experts of 1024 x 2048: 6.7 us with 8, 8.8 with 4; 512 rows, 64
@@ -224,9 +226,9 @@ struct FpShape {
     static constexpr int ctas = PAIR ? 2 : 1;
     static constexpr int rows = NT / ctas;                   // of X in a CTA's shared memory
     static constexpr int box = PAIR ? rows / 2 : rows;       // rows per TMA box of X
-    static constexpr int store_warps = NT > 32 ? kFpStoreWarps : 4;
+    static constexpr int store_warps = PAIR ? kFpStoreWarps : 4;
     static constexpr int groups = store_warps / 4;           // warps to a quarter of the lanes
-    static constexpr int threads = 32 * (6 + store_warps);
+    static constexpr int threads = 32 * (PAIR ? 12 : 10);
     static constexpr int step = 16 * ctas;                   // N is a multiple of it
     static constexpr int atoms = NV ? 4 : 2;                 // 512-byte scale tiles per 256 columns
     static constexpr int nb = (NT + 127) / 128;              // of the rows, per atom
@@ -249,6 +251,8 @@ struct FpShape {
 struct FpArgs {
     const uint32_t* xs;      // scale words of the rows
     const uint8_t* ws;       // scale tiles of the weights
+    uint4* xtiles;           // pairs: the scales of every row tile, see fp4_tile_scales_kernel
+    int64_t max_xtiles;
     int64_t P;
     int K, E, R, KS;         // KS: stages per tile
     int xwords, wwords;      // scale words per row
@@ -263,7 +267,7 @@ struct FpArgs {
 struct FpPlan {
     int32_t begin[kFpMaxE + 1];
     int64_t tile0[kFpMaxE + 1];
-    int64_t warp_sum[6 + kFpStoreWarps];
+    int64_t warp_sum[kFpMaxWarps];
 };
 
 // Each thread takes four experts; offsets are clamped so that no value of them
@@ -333,6 +337,15 @@ struct FpRun {
         sharers = max(min(G, max(tiles - tile0, U / min_units)), (int64_t)1);
     }
     __device__ __forceinline__ int64_t lo(int64_t c) const { return c >= sharers ? U : U * c / sharers; }
+};
+
+// Tensor maps of a launch: codes of the weights and of the rows; for pairs their scale
+// tiles as well (rows of 512 bytes).
+template <bool PAIR> struct FpMaps {
+    CUtensorMap w, x;
+};
+template <> struct FpMaps<true> {
+    CUtensorMap w, x, ws, xs;
 };
 
 struct FpTile {
@@ -549,10 +562,68 @@ __device__ __forceinline__ bool fp_wait_flags(const uint64_t* flags, int64_t ste
     return ok;
 }
 
+// A barrier's wait; of a pair's barriers, which either CTA's copies and products arrive at,
+// acquiring what the cluster has released there.
+template <bool PAIR>
+__device__ __forceinline__ bool fp_wait(uint64_t* bar, uint32_t parity, int32_t* err) {
+    return PAIR ? mbar_wait_cluster(bar, parity, err) : mbar_wait(bar, parity, err);
+}
+
+// boxes of the TMA copies of `count` rows, none for fewer than one
+template <class C> __device__ __forceinline__ int fp_boxes(int count) { return max(0, (count + C::box - 1) / C::box); }
+
+// Scales of the rows for pairs: for every tile of NT rows of an expert and every stage the
+// scale tiles that the products read ([atoms][nb] of 512 bytes, see FpShape), since an
+// expert's rows start anywhere and a scale tile only at multiples of 128.  A pair's
+// products read both CTAs' shared memory on the word of one barrier: what is there has to
+// have come by copies that arrive at that barrier themselves.  (Gathered by cp.async in
+// each CTA, CTA 1's writes need a release to the cluster before every arrival at CTA 0,
+// which takes some 1650 cycles: 842 us for 32768 rows on 32 experts of 4096 x 6144 with one
+// warp that releases, 396 with four, 357 without the release, which nothing then orders;
+// 338 this way, of which this kernel is some 3; 400 rows of 10240 x 2048: 13.9 and 15.5.)
+// A warp takes two words of a tile's rows at a time: 16 loads of a lane in flight.
+constexpr int kFpTileScaleThreads = 256;
+template <int NT, int M, int NB>
+__global__ void __launch_bounds__(kFpTileScaleThreads)
+fp4_tile_scales_kernel(FpArgs a, int words) {   // words: of a tile's row, a multiple of 2
+    __shared__ FpPlan plan;
+    static_assert(4 * kFpTileScaleThreads >= kFpMaxE, "fp_plan takes four experts a thread");
+    pdl_trigger();
+    pdl_wait();
+    fp_plan<NT, M>(a, plan);
+    const int lane = threadIdx.x & 31, RT = (a.R - 1) / M + 1;
+    const int64_t xtiles = min(plan.tile0[a.E] / RT, a.max_xtiles);
+    const int64_t step = (int64_t)gridDim.x * (kFpTileScaleThreads / 32), pairs = words / 2;
+    for (int64_t i = (int64_t)blockIdx.x * (kFpTileScaleThreads / 32) + (threadIdx.x >> 5); i < xtiles * pairs; i += step) {
+        const int64_t xt = i / pairs;
+        const int w0 = 2 * (int)(i - xt * pairs);
+        int lo = 0, hi = a.E;  // the last expert whose first tile is not after this one
+        while (hi - lo > 1) {
+            const int m = (lo + hi) / 2;
+            if (plan.tile0[m] <= xt * RT) lo = m; else hi = m;
+        }
+        const int64_t p0 = plan.begin[lo] + (xt - plan.tile0[lo] / RT) * NT, end = plan.begin[lo + 1];
+        uint32_t v[2][NB][4];
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int h = 0; h < NB; ++h)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int64_t r = p0 + 128 * h + 32 * j + lane;
+                    v[w][h][j] = r < end && w0 + w < a.xwords ? a.xs[scale_word(r, w0 + w, a.xwords)] : 0;
+                }
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+#pragma unroll
+            for (int h = 0; h < NB; ++h)
+                a.xtiles[((xt * words + w0 + w) * NB + h) * 32 + lane] = make_uint4(v[w][h][0], v[w][h][1], v[w][h][2], v[w][h][3]);
+    }
+}
+
 template <int NT, bool NV, bool PAIR, typename YT>
 __global__ void __launch_bounds__(FpShape<NT, NV, PAIR>::threads, 1)
-fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_constant__ CUtensorMap xmap,
-                   FpArgs a, YT* y) {
+fp4_product_kernel(const __grid_constant__ FpMaps<PAIR> maps, FpArgs a, YT* y) {
     using C = FpShape<NT, NV, PAIR>;
     extern __shared__ uint8_t fp_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(fp_raw) + 1023) & ~uintptr_t(1023));
@@ -570,8 +641,8 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     }
     if (threadIdx.x == 32) {
         for (int s = 0; s < C::stages; ++s) {
-            // the copies' announcement, the lanes of the scale warps; in CTA 0 of a pair, CTA 1's stage
-            mbar_init(&full[s], 1 + 32 * kFpScaleWarps + (PAIR && rank == 0 ? 1 : 0));
+            // the copies' announcement (of a pair's: CTA 0's, for both), the lanes of the scale warps
+            mbar_init(&full[s], PAIR ? 1 : 1 + 32 * kFpScaleWarps);
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -596,53 +667,68 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
     if (warp == 0) {
         // ---------------- copies (whole warp, an elected lane issues) ----------------
         Ring ring;
+        const uint32_t bars = PAIR ? uniform(mapa_u32(smem_u32(full), 0)) : 0;  // CTA 0's
         while (uniform((int)q.next())) {
             const FpTile t = fp_tile<NT>(plan, a.E, q.tile);
             // this CTA's share of the rows: half of N, itself a multiple of 16
             const int half = (t.n + C::step - 1) / C::step * 16;
-            const int first = PAIR ? rank * half : 0, count = min(half, t.n - first);
+            const int first = PAIR ? rank * half : 0;
             const int p0 = uniform((int)min(t.p0 + first, a.P - 1));  // past the last row: nothing to copy
-            const int boxes = uniform(PAIR ? max(0, (count + C::box - 1) / C::box) : 1);
+            const int boxes = uniform(PAIR ? fp_boxes<C>(min(half, t.n - first)) : 1);
             const int wrow = uniform(t.e * a.R + t.rt * C::M + rank * 128);
             const int k0 = uniform(q.k0), k1 = uniform(q.k1);
             // past the expert's last weight row (the second half of a tile may be) the products are
             // not stored: any scales do
             const int block = uniform(t.rt * C::M + rank * 128 < a.R ? wrow >> 7 : (wrow >> 7) - 1);
-            const uint8_t* sfa = a.ws + ((int64_t)block * a.wwords + k0 * C::atoms) * 512;
-            const uint32_t bytes = (uint32_t)(C::a_bytes + boxes * C::box * 128);
+            if constexpr (PAIR) {
+                // What both CTAs copy is counted at CTA 0's barrier, which announces it.
+                const int both = uniform(fp_boxes<C>(min(half, t.n)) + fp_boxes<C>(min(half, t.n - half)));
+                const uint32_t bytes = 2 * (C::a_bytes + C::sfa_bytes + C::sfb_bytes) + both * C::box * 128;
+                const int64_t xtile = plan.tile0[t.e] / ((a.R - 1) / C::M + 1) + (t.p0 - plan.begin[t.e]) / NT;
+                const int wsrow = uniform((int)((int64_t)block * a.wwords));
+                const int xsrow = uniform((int)(xtile * a.KS * (C::atoms * C::nb)));
 #pragma unroll 1
-            for (int k = k0; k < k1; ++k) {
-                if (ok && ring.again && !mbar_wait(&empty[ring.s], ring.phase ^ 1, a.err)) ok = false;
-                uint8_t* st = smem + ring.s * C::stage;
-                uint64_t* bar = &full[ring.s];
-                const uint32_t na = (uint32_t)min(C::atoms, a.wwords - k * C::atoms) * 512;
-                mbar_expect_tx_elect(bar, bytes + na);
-                tma_load_2d_elect(st, &wmap, k * 128, wrow, bar);
+                for (int k = k0; k < k1; ++k) {
+                    if (ok && ring.again && !mbar_wait_cluster(&empty[ring.s], ring.phase ^ 1, a.err)) ok = false;
+                    uint8_t* st = smem + ring.s * C::stage;
+                    const uint32_t bar = bars + 8 * ring.s;
+                    if (rank == 0) mbar_expect_tx_elect(&full[ring.s], bytes);
+                    tma_load_2d_pair_elect(st, &maps.w, k * 128, wrow, bar);
 #pragma unroll
-                for (int b = 0; b < C::rows / C::box; ++b)
-                    if (b < boxes)
-                        tma_load_2d_elect(st + C::a_bytes + b * C::box * 128, &xmap, k * 128, p0 + b * C::box, bar);
-                bulk_g2s_elect(st + C::a_bytes + C::b_bytes, sfa, na, bar);
-                sfa += C::atoms * 512;
-                ring.next(C::stages);
+                    for (int b = 0; b < C::rows / C::box; ++b)
+                        if (b < boxes)
+                            tma_load_2d_pair_elect(st + C::a_bytes + b * C::box * 128, &maps.x, k * 128, p0 + b * C::box,
+                                                   bar);
+                    uint8_t* sf = st + C::a_bytes + C::b_bytes;
+                    tma_load_2d_pair_elect(sf, &maps.ws, 0, wsrow + k * C::atoms, bar);
+                    tma_load_2d_pair_elect(sf + C::sfa_bytes, &maps.xs, 0, xsrow + k * (C::atoms * C::nb), bar);
+                    ring.next(C::stages);
+                }
+            } else {
+                const uint8_t* sfa = a.ws + ((int64_t)block * a.wwords + k0 * C::atoms) * 512;
+                const uint32_t bytes = (uint32_t)(C::a_bytes + C::b_bytes);
+#pragma unroll 1
+                for (int k = k0; k < k1; ++k) {
+                    if (ok && ring.again && !mbar_wait(&empty[ring.s], ring.phase ^ 1, a.err)) ok = false;
+                    uint8_t* st = smem + ring.s * C::stage;
+                    uint64_t* bar = &full[ring.s];
+                    const uint32_t na = (uint32_t)min(C::atoms, a.wwords - k * C::atoms) * 512;
+                    mbar_expect_tx_elect(bar, bytes + na);
+                    tma_load_2d_elect(st, &maps.w, k * 128, wrow, bar);
+                    tma_load_2d_elect(st + C::a_bytes, &maps.x, k * 128, p0, bar);
+                    bulk_g2s_elect(st + C::a_bytes + C::b_bytes, sfa, na, bar);
+                    sfa += C::atoms * 512;
+                    ring.next(C::stages);
+                }
             }
         }
-        // the last copies have landed before the CTA may end
+        // the last copies (of a pair, both CTAs') have landed before a CTA may end
         Ring last = ring.back(C::stages);
-        for (int i = 0; i < C::stages; ++i, last.next(C::stages))
-            if (ring.again || last.s < ring.s) mbar_wait(&full[last.s], last.phase, a.err, kSleepTries);
-    } else if (PAIR && warp == 1 && rank == 1) {
-        // ---------------- CTA 1 of a pair tells CTA 0 of its full stages ----------------
-        const int64_t total = uniform(q.stages());
-        Ring ring;
-#pragma unroll 1
-        for (int64_t i = 0; i < total; ++i) {
-            if (ok && !mbar_wait(&full[ring.s], ring.phase, a.err)) ok = false;
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-            if (lane == 0) mbar_arrive_remote(&full[ring.s], 0);
-            __syncwarp();
-            ring.next(C::stages);
-        }
+        if (rank == 0)
+            for (int i = 0; i < C::stages; ++i, last.next(C::stages))
+                if (ring.again || last.s < ring.s) mbar_wait(&full[last.s], last.phase, a.err, kSleepTries);
+    } else if (warp == 1 && rank == 1) {
+        // CTA 0 issues the products of a pair
     } else if (warp == 1) {
         // ---------------- products (whole warp, an elected lane issues) ----------------
         Ring ring;
@@ -662,11 +748,11 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             uint32_t more = 0;                // 0: the tile's first product clears the accumulator
 #pragma unroll 1
             for (int k = k0; k < k1; ++k) {
-                if (!ready && ok && !mbar_wait(&full[ring.s], ring.phase, a.err)) ok = false;
+                if (!ready && ok && !fp_wait<PAIR>(&full[ring.s], ring.phase, a.err)) ok = false;
                 tc_fence_after();
                 // the scale warps' copies are writes of the generic proxy, and the tensor unit reads
                 // them: fenced here, where they are known to have landed
-                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                if (!PAIR) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 const uint32_t st = sbase + ring.s * C::stage;
                 const uint64_t sfa = smem_desc_scales(st + C::a_bytes + C::b_bytes);
                 const uint64_t sfb = sfa + (C::sfa_bytes >> 4);
@@ -675,7 +761,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
                 uint64_t* empty_s = &empty[ring.s];
                 ring.next(C::stages);
                 // asked before this stage is issued, so that the answer is there after it
-                ready = mbar_test(&full[ring.s], ring.phase);
+                ready = PAIR ? mbar_test_cluster(&full[ring.s], ring.phase) : mbar_test(&full[ring.s], ring.phase);
                 if (cols >= 256) {
                     fp4_stage<NV, PAIR>(d, ad, bd, idesc, sfa, sfb, sf, more, second, smem_u32(empty_s));
                 } else {  // the row's last columns
@@ -704,7 +790,9 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             if (PAIR) tc_commit_pair_elect(&accfull[buf]);
             else tc_commit_elect(&accfull[buf]);
         }
-    } else if (warp < 4 || (warp >= 8 && warp < 10)) {
+    } else if (PAIR && warp < 4) {
+        // nothing: a warp reads the accumulator's quarter of its index, so the stores begin at warp 4
+    } else if (!PAIR && (warp < 4 || warp >= 8)) {
         // ---------------- scales of the rows ----------------
         // A stage has atoms * NT / 32 runs of 32 rows' words; warp f takes runs f, f + 4, ..: a
         // lane copies its row's word to where the scale tile has it.  The copies are asynchronous
@@ -773,7 +861,7 @@ fp4_product_kernel(const __grid_constant__ CUtensorMap wmap, const __grid_consta
             const int64_t other = (int64_t)blockIdx.x + C::ctas;  // the first of them
             uint64_t* flags = a.flags + kFpStoreWarps * other + flag;
             const float* theirs = a.partial + other * (128 * NT) + 16 * half * 128 + 32 * quarter + lane;
-            if (ok && !mbar_wait(&accfull[buf], (piece >> 1) & 1, a.err)) ok = false;
+            if (ok && !fp_wait<PAIR>(&accfull[buf], (piece >> 1) & 1, a.err)) ok = false;
             tc_fence_after();
             if (parts && ok && !fp_wait_flags(flags, kFpStoreWarps * C::ctas, parts, a.err)) ok = false;
             const uint32_t d = tmem + ((uint32_t)(32 * quarter) << 16) + NT * buf;

@@ -221,15 +221,6 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint64_t* bar, uint32_t rank
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(addr), "r"(rank));
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-// The arrival alone, ordered after what this thread has seen of its own CTA's
-// shared memory (and after its proxy fence): for data that stays in that memory
-// and is read there, by the tensor unit of this SM.  The release above takes some
-// 1500 cycles under load, as it waits for everything the SM has in flight.
-__device__ __forceinline__ void mbar_arrive_remote(uint64_t* bar, uint32_t rank) {
-    uint32_t addr = smem_u32(bar);
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(addr) : "r"(addr), "r"(rank));
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
 __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, int32_t* err,
                                                   uint32_t tries = kWaitTries) {
     for (uint32_t i = 0; i < tries; ++i) {
@@ -244,6 +235,36 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity
     }
     if (err) atomicOr(err, kErrWaitTimeout);
     return false;
+}
+
+// whether the phase has completed, acquiring at cluster scope, without a wait
+__device__ __forceinline__ bool mbar_test_cluster(uint64_t* bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
+        " selp.b32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// the cluster's address of what lies at shared-memory address `addr` in CTA `rank`
+__device__ __forceinline__ uint32_t mapa_u32(uint32_t addr, uint32_t rank) {
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+// tma_load_2d_elect of a pair of CTAs: into this CTA's shared memory, completion
+// counted on the barrier at cluster address `bar`, in either of the two
+__device__ __forceinline__ void tma_load_2d_pair_elect(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        " @e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4}], [%2];\n}"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(bar), "r"(x), "r"(y)
+        : "memory");
 }
 
 // barrier among the first `threads` threads of the CTA (named barrier 1)

@@ -229,4 +229,4 @@ def test_product_sizes_up_to_31_bits():
     pairs = cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, 40, 32, 1, 1 << 30)
     assert pairs > cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, 32, 32, 1, 1 << 30)
     assert cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, 40, 32, 1, most) == pairs
-    assert cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, most, 32, 1, 1) == pairs
+    assert cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, most, 32, 1, 1) >= pairs

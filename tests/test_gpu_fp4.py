@@ -310,3 +310,62 @@ def test_product_of_the_most_rows(P, R):
     assert torch.equal(y[i][:, j], dev((X @ W.T).astype(np.float32)).to(B))
     y[i[:, None], j] = 0
     assert int(torch.count_nonzero(y)) == 0
+
+
+def pair_inputs(fmt, sizes, R, K, seed):
+    """Inputs of a grouped product whose scales differ from stage to stage by many powers of two."""
+    rng = np.random.default_rng(seed)
+    P, E = sum(sizes), len(sizes)
+    lo, hi, block = (100, 150, 32) if fmt == "mx" else (0x08, 0x78, 16)
+    sides = []
+    for n in (P, E * R):
+        codes = rng.integers(0, 256, (n, K // 2)).astype(np.uint8)
+        stage = rng.integers(lo, hi, (n, -(-K // 256)))     # a base for each 256 columns, and a little about it
+        byte = np.repeat(stage, 256 // block, 1)[:, :K // block] + rng.integers(0, 4, (n, K // block))
+        sides.append((codes, byte.astype(np.uint8)))
+    return sides, np.concatenate([[0], np.cumsum(sizes)])
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("sizes,R,K", [([1, 32, 94, 225, 0, 127, 449, 33], 2560, 1536), ([700], 5120, 2208)])
+def test_product_of_pairs_reads_no_stale_scales(fmt, sizes, R, K):
+    """Two sets of inputs in turn through the same buffers and workspace, many times: the same
+    bits every time, those of a first call, which are right."""
+    P, E = sum(sizes), len(sizes)
+    sets, want = [], []
+    for seed in (1, 2):
+        ((xc, xb), (wc, wb)), off = pair_inputs(fmt, sizes, R, K, seed)
+        y = product(fmt, xc, xb, wc, wb, E, R, off if E > 1 else None, None, F, P, K)
+        X, W = dev(ff.values(xc, xb, fmt)), dev(ff.values(wc, wb, fmt))
+        for e in range(E):
+            lo, hi = int(off[e]), int(off[e + 1])
+            w = W[e * R:(e + 1) * R]
+            size = X[lo:hi].abs() @ w.abs().T   # the bound of check_product
+            assert ((y[lo:hi].double() - X[lo:hi] @ w.T).abs() <= (-(-K // 64) + 24) * 2.0 ** -22 * size).all()
+        want.append(y)
+        sets.append([dev(a) for a in (xc.reshape(-1), ff.tile_scales(xb), wc.reshape(-1), ff.tile_scales(wb))])
+    offsets = dev(off.astype(np.int32))
+    ws = torch.zeros(cm.coli_moe_fp4_product_workspace_size(FMT[fmt], P, K, E, R), dtype=torch.uint8, device="cuda")
+    xc, xs, wc, wsc = (torch.empty_like(a) for a in sets[0])
+    y, wrong = torch.empty_like(want[0]), torch.zeros((), dtype=torch.int64, device="cuda")
+    for i in range(60):
+        for to, a in zip((xc, xs, wc, wsc), sets[i & 1]):
+            to.copy_(a)
+        cm.coli_moe_fp4_product(FMT[fmt], xc, xs, P, K, wc, wsc, E, R, y, ws, offsets=offsets if E > 1 else None)
+        wrong += (y != want[i & 1]).sum()
+    assert int(wrong) == 0 and cm.coli_moe_fp4_product_status(ws) == 0
+
+
+def test_product_of_pairs_with_offsets_that_overlap_stays_in_bounds():
+    """Offsets that are not ascending name more row tiles than P rows have."""
+    P, R, K, E = 900, 2560, 512, 8
+    rng = np.random.default_rng(3)
+    xc, xb = weights("mx", P, K, rng)
+    wc, wb = weights("mx", E * R, K, rng)
+    size = cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, P, K, E, R)
+    y, ws = torch.full((P + 300, R), 9.0, device="cuda"), torch.full((size + 65536,), 7, dtype=torch.uint8, device="cuda")
+    off = dev(np.array([0, P, 0, P, 0, P, 0, P, 0], np.int32))
+    cm.coli_moe_fp4_product(cm.COLI_MXFP4, dev(xc.reshape(-1)), dev(ff.tile_scales(xb)), P, K, dev(wc.reshape(-1)),
+                            dev(ff.tile_scales(wb)), E, R, y[:P], ws[:size], offsets=off)
+    assert cm.coli_moe_fp4_product_status(ws) == 0
+    assert (y[P:] == 9.0).all() and (ws[size:] == 7).all()
