@@ -598,10 +598,12 @@ int coli_moe_fp4_quantize(coli_fp4 fmt, const void* x, coli_dtype xt, int64_t n_
  * are left untouched.  Products are exact, sums in f32 in an order that depends
  * on offsets and sizes alone; one rounding to yt.  1 <= E <= 1024, P < 2^31,
  * E * R < 2^31, K a multiple of 32.  ws: device, 16-byte aligned,
- * coli_moe_fp4_product_workspace_size bytes.  coli_moe_fp4_product_status is
- * coli_moe_status for these calls: it synchronises the stream and reports
- * whether a bounded wait gave up in the last call that used ws (after which ws
- * has to be cleared to zeros before its next use). */
+ * coli_moe_fp4_product_workspace_size bytes, set to anything before its first
+ * use.  Should a bounded wait inside the kernel give up (some ten seconds: other
+ * work held the GPU's SMs, or a fault of this library), the rows of y that it
+ * kept from their sums become NaN, and ws stays marked: until it is cleared to
+ * zeros, calls that use it write NaN, and coli_moe_fp4_product_status, which
+ * synchronises the stream, returns COLI_E_TIMEOUT. */
 int coli_moe_fp4_product_workspace_size(coli_fp4 fmt, int64_t P, int32_t K, int32_t E, int32_t R,
                                         size_t* bytes);
 int coli_moe_fp4_product(coli_fp4 fmt, const void* x_codes, const void* x_scales, int64_t P,
@@ -609,6 +611,14 @@ int coli_moe_fp4_product(coli_fp4 fmt, const void* x_codes, const void* x_scales
                          int32_t R, const int32_t* offsets, const float* alpha, void* y,
                          coli_dtype yt, void* ws, size_t ws_bytes, coli_stream_t stream);
 int coli_moe_fp4_product_status(const void* ws, int32_t* flags, coli_stream_t stream);
+
+/* Test of those waits, as coli_moe_layer_set_wait_test is for a layer's: in later
+ * coli_moe_fp4_product calls of the calling thread every wait gives up after 4096
+ * tries, and withhold = 0: CTA 0 never copies its first stage; 1: no CTA says
+ * that its piece of a tile cut in several is there; < 0 (the default): none of
+ * this.  MXFP4 with f32 results only (COLI_E_UNSUPPORTED else).  Never needed in
+ * normal use.  Host-only. */
+int coli_moe_fp4_set_wait_test(int32_t withhold);
 
 #ifdef __cplusplus
 }

@@ -30,7 +30,7 @@ __all__ = [
     "coli_moe_block_norm", "coli_moe_block_norm_backward_workspace_size",
     "coli_moe_block_norm_backward", "coli_moe_fp4_bytes", "coli_moe_fp4_quantize",
     "coli_moe_fp4_product_workspace_size", "coli_moe_fp4_product",
-    "coli_moe_fp4_product_status",
+    "coli_moe_fp4_product_status", "coli_moe_fp4_set_wait_test",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -59,7 +59,7 @@ EXPORTS = (
     "coli_moe_block_norm", "coli_moe_block_norm_backward_workspace_size",
     "coli_moe_block_norm_backward", "coli_moe_fp4_bytes", "coli_moe_fp4_quantize",
     "coli_moe_fp4_product_workspace_size", "coli_moe_fp4_product",
-    "coli_moe_fp4_product_status",
+    "coli_moe_fp4_product_status", "coli_moe_fp4_set_wait_test",
 )
 
 
@@ -157,6 +157,7 @@ _SIGS = {
     "coli_moe_fp4_product": ([ctypes.c_int, _P, _P, _I64, _I32, _P, _P, _I32, _I32, _P, _P, _P,
                               ctypes.c_int, _P, _SZ, _P], ctypes.c_int),
     "coli_moe_fp4_product_status": ([_P, ctypes.POINTER(_I32), _P], ctypes.c_int),
+    "coli_moe_fp4_set_wait_test": ([_I32], ctypes.c_int),
 }
 for _name, (_args, _res) in _SIGS.items():
     _f = getattr(lib, _name)
@@ -620,8 +621,13 @@ def coli_moe_fp4_product(fmt, x_codes, x_scales, P, K, w_codes, w_scales, E, R, 
 
 
 def coli_moe_fp4_product_status(ws, stream=None) -> int:
-    """Error flags of the last product that used ws (raises on a timeout)."""
+    """0, or raises when a product that used ws gave up a wait since ws was last cleared."""
     flags, d = _I32(0), _device()
-    _ok(lib.coli_moe_fp4_product_status(_buf("ws", ws, _UINT8, 4, d), ctypes.byref(flags),
+    _ok(lib.coli_moe_fp4_product_status(_buf("ws", ws, _UINT8, 8, d), ctypes.byref(flags),
                                         _queue(stream, d)))
     return flags.value
+
+
+def coli_moe_fp4_set_wait_test(withhold: int) -> None:
+    """Test of the product's bounded waits (see the header); < 0: off."""
+    _ok(lib.coli_moe_fp4_set_wait_test(withhold))

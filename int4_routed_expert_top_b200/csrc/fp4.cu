@@ -90,10 +90,13 @@ int launch_quantize(coli_fp4 fmt, coli_act act, dim3 grid, dim3 threads, const F
     return launch_pdl(kern, grid, threads, 0, st, "fp4 quantize", a, lg, (const T*)x, (T*)values);
 }
 
-template <int NT, bool NV, bool PAIR, typename YT>
+// what later products of this thread withhold (coli_moe_fp4_set_wait_test), -1: nothing
+thread_local int32_t g_withhold = -1;
+
+template <int NT, bool NV, bool PAIR, typename YT, bool TW = false>
 int launch_product(const FpArgs& a, const void* x_codes, const void* w_codes, void* y, cudaStream_t st) {
     using C = FpShape<NT, NV, PAIR>;
-    const auto kern = fp4_product_kernel<NT, NV, PAIR, YT>;
+    const auto kern = fp4_product_kernel<NT, NV, PAIR, YT, TW>;
     FpMaps<PAIR> maps;
     int rc;
     if ((rc = encode_codes_map(&maps.w, w_codes, (int64_t)a.E * a.R, a.K, 128))) return rc;
@@ -130,6 +133,11 @@ int launch_product(const FpArgs& a, const void* x_codes, const void* w_codes, vo
 template <int NT, bool PAIR>
 int launch_product_t(coli_fp4 fmt, coli_dtype yt, const FpArgs& a, const void* x_codes, const void* w_codes, void* y,
                      cudaStream_t st) {
+    if (a.withhold >= 0) {
+        if (fmt != COLI_MXFP4 || yt != COLI_F32)
+            return fail(COLI_E_UNSUPPORTED, "fp4_product: the wait test takes MXFP4 with f32 results");
+        return launch_product<NT, false, PAIR, float, true>(a, x_codes, w_codes, y, st);
+    }
     if (fmt == COLI_NVFP4)
         return yt == COLI_F32 ? launch_product<NT, true, PAIR, float>(a, x_codes, w_codes, y, st)
                               : launch_product<NT, true, PAIR, __nv_bfloat16>(a, x_codes, w_codes, y, st);
@@ -218,7 +226,8 @@ int coli_moe_fp4_product(coli_fp4 fmt, const void* x_codes, const void* x_scales
     a.KS = (K + 255) / 256;
     a.xwords = a.wwords = words_of(fmt, K);
     a.offsets = offsets; a.alpha = alpha;
-    a.err = static_cast<int32_t*>(ws);
+    a.err = static_cast<uint64_t*>(ws);
+    a.withhold = g_withhold;
     a.flags = reinterpret_cast<uint64_t*>(static_cast<char*>(ws) + kFpFlagBytes);
     a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kFpHeadBytes);
     a.xtiles = reinterpret_cast<uint4*>(static_cast<char*>(ws) + kFpHeadBytes + partial_bytes(kFpLargeNT));  // pairs
@@ -229,12 +238,18 @@ int coli_moe_fp4_product(coli_fp4 fmt, const void* x_codes, const void* x_scales
 
 int coli_moe_fp4_product_status(const void* ws, int32_t* flags, coli_stream_t stream) {
     if (!ws || !flags) return fail(COLI_E_INVAL, "fp4_product_status: NULL pointer");
-    int32_t f = 0;
-    cudaError_t e = cudaMemcpyAsync(&f, ws, 4, cudaMemcpyDeviceToHost, S(stream));
+    uint64_t word = 0;
+    cudaError_t e = cudaMemcpyAsync(&word, ws, sizeof(word), cudaMemcpyDeviceToHost, S(stream));
     if (e == cudaSuccess) e = cudaStreamSynchronize(S(stream));
     if (e != cudaSuccess) return fail(COLI_E_CUDA, "fp4_product_status: %s", cudaGetErrorString(e));
-    *flags = f;
-    if (f & kErrWaitTimeout) return fail(COLI_E_TIMEOUT, "fp4_product: a bounded wait gave up");
+    *flags = word == kFpBroken ? kErrWaitTimeout : 0;
+    if (*flags) return fail(COLI_E_TIMEOUT, "fp4_product: a bounded wait gave up; the workspace has to be cleared");
+    return COLI_OK;
+}
+
+int coli_moe_fp4_set_wait_test(int32_t withhold) {
+    if (withhold > 1) return fail(COLI_E_INVAL, "fp4_set_wait_test: nothing to withhold named %d", withhold);
+    g_withhold = withhold < 0 ? -1 : withhold;
     return COLI_OK;
 }
 

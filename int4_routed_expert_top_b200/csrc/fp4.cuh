@@ -216,8 +216,12 @@ constexpr int kFpMaxGrid = 160;    // B200 has 148 SMs; the workspace is sized f
 // the workspace: error flags, a flag per CTA and store warp, then partial sums
 constexpr int kFpFlagBytes = 256;
 constexpr int kFpHeadBytes = kFpFlagBytes + kFpMaxGrid * kFpStoreWarps * 8;
-// a raised flag: a value that unset memory does not hold (0 after every call)
-constexpr uint64_t kFpRaised = 0x9d3ac1f5e8276b41ull;
+// a raised flag: a value that unset memory does not hold (0 after every call); and one
+// whose piece is not there, which is also what the workspace's first word becomes when
+// a wait gives up, and stays
+constexpr uint64_t kFpRaised = 0x9d3ac1f5e8276b41ull, kFpBroken = 0x62c53e0a17d894beull;
+// tries of a wait for flags (some ten seconds); of every wait under the wait test
+constexpr uint32_t kFpFlagTries = 1u << 25, kFpTestTries = 4096;
 
 // NT: rows of a tile at most; PAIR: two CTAs to a tile, M = 256 weight rows
 template <int NT, bool NV, bool PAIR>
@@ -229,6 +233,9 @@ struct FpShape {
     static constexpr int store_warps = PAIR ? kFpStoreWarps : 4;
     static constexpr int groups = store_warps / 4;           // warps to a quarter of the lanes
     static constexpr int threads = 32 * (PAIR ? 12 : 10);
+    // the launch bound: 128 registers a thread of a pair, so that the next product's gather of
+    // scales (14336 of them) fits beside its CTAs (400 rows of 10240 x 2048: 14.7 us, 15.4 with 131)
+    static constexpr int bound = PAIR ? 512 : threads;
     static constexpr int step = 16 * ctas;                   // N is a multiple of it
     static constexpr int atoms = NV ? 4 : 2;                 // 512-byte scale tiles per 256 columns
     static constexpr int nb = (NT + 127) / 128;              // of the rows, per atom
@@ -260,7 +267,8 @@ struct FpArgs {
     const float* alpha;
     uint64_t* flags;
     float* partial;
-    int32_t* err;
+    uint64_t* err;
+    int withhold;            // the wait test: 0 CTA 0's first stage, 1 the flags
 };
 
 // Where every expert's tiles start, in shared memory.
@@ -420,15 +428,15 @@ __device__ __forceinline__ uint64_t smem_desc_scales(uint32_t addr) {
 // 32 rows x 16 bytes of shared memory to 32 lanes x 4 columns of TMEM, repeated
 // in the four lane quarters (in both CTAs of a pair, each from its own)
 template <bool PAIR>
-__device__ __forceinline__ void tc_copy_scales_elect(uint32_t dst, uint64_t desc) {
+__device__ __forceinline__ void tc_copy_scales_elect(uint32_t dst, uint64_t desc, uint32_t go) {
     if (PAIR)
         asm volatile(
-            "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-            " @e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n}" ::"r"(dst), "l"(desc) : "memory");
+            "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n setp.ne.and.b32 e, %2, 0, e;\n"
+            " @e tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;\n}" ::"r"(dst), "l"(desc), "r"(go) : "memory");
     else
         asm volatile(
-            "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
-            " @e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}" ::"r"(dst), "l"(desc) : "memory");
+            "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n setp.ne.and.b32 e, %2, 0, e;\n"
+            " @e tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;\n}" ::"r"(dst), "l"(desc), "r"(go) : "memory");
 }
 
 // instruction descriptor of a block-scaled product of E2M1 operands, both
@@ -441,11 +449,12 @@ __device__ __forceinline__ constexpr uint32_t idesc_fp4(int n) {
 
 #define COLI_MMA_FP4(GROUP, KIND)                                                                              \
     asm volatile("{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"             \
+                 " setp.ne.and.b32 e, %7, 0, e;\n"                                                            \
                  " @e tcgen05.mma.cta_group::" GROUP ".kind::" KIND " [%0], %1, %2, %3, [%5], [%6], p;\n}"    \
-                 ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb))
+                 ::"r"(d), "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa), "r"(sfb), "r"(go))
 template <bool NV, bool PAIR>
 __device__ __forceinline__ void tc_mma_fp4_elect(uint32_t d, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
-                                                 uint32_t sfa, uint32_t sfb, uint32_t accumulate) {
+                                                 uint32_t sfa, uint32_t sfb, uint32_t accumulate, uint32_t go) {
     if constexpr (PAIR && NV) COLI_MMA_FP4("2", "mxf4nvf4.block_scale.scale_vec::4X");
     else if constexpr (PAIR) COLI_MMA_FP4("2", "mxf4.block_scale.scale_vec::2X");
     else if constexpr (NV) COLI_MMA_FP4("1", "mxf4nvf4.block_scale.scale_vec::4X");
@@ -466,10 +475,11 @@ __device__ __forceinline__ void tc_mma_fp4_elect(uint32_t d, uint64_t adesc, uin
     " add.u32 u, %6, " #SFB ";\n @e tcgen05.mma.cta_group::" G ".kind::" KIND " [%0], x, z, i, [t], [u], " M ";\n"
 #define COLI_STAGE_BEGIN                                                                                          \
     "{\n .reg .pred e, f, m, n;\n .reg .b64 x, z;\n .reg .b32 t, u, i;\n elect.sync _|e, 0xffffffff;\n"          \
+    " setp.ne.and.b32 e, %11, 0, e;\n"                                                                            \
     " setp.ne.b32 m, %7, 0;\n setp.ne.and.b32 f, %8, 0, e;\n setp.eq.b32 n, 0, 0;\n"
 #define COLI_STAGE_OPERANDS                                                                                       \
     ::"r"(d), "l"(ad), "l"(bd), "r"(idesc), "l"(sfa), "l"(sfb), "r"(sf), "r"(more), "r"(second), "r"(empty),      \
-        "h"((uint16_t)3)                                                                                          \
+        "h"((uint16_t)3), "r"(go)                                                                                 \
         : "memory"
 #define COLI_COMMIT_1 " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%9];\n}"
 #define COLI_COMMIT_2                                                                                             \
@@ -479,7 +489,8 @@ __device__ __forceinline__ void tc_mma_fp4_elect(uint32_t d, uint64_t adesc, uin
 #define COLI_NV "mxf4nvf4.block_scale.scale_vec::4X"
 template <bool NV, bool PAIR>
 __device__ __forceinline__ void fp4_stage(uint32_t d, uint64_t ad, uint64_t bd, uint32_t idesc, uint64_t sfa,
-                                          uint64_t sfb, uint32_t sf, uint32_t more, uint32_t second, uint32_t empty) {
+                                          uint64_t sfb, uint32_t sf, uint32_t more, uint32_t second, uint32_t empty,
+                                          uint32_t go) {
     if constexpr (PAIR && NV)
         asm volatile(COLI_STAGE_BEGIN
                      COLI_CP("2", "e", 0, "4, 0") COLI_CP("2", "e", 16, "5, 0") COLI_CP("2", "f", 20, "5, 32")
@@ -545,17 +556,14 @@ struct Ring {
 
 // Warp-wide wait for the flags of `parts` CTAs' store warps, `step` flags apart, a
 // lane each: some ten seconds at most, since those CTAs may have to wait for an SM
-// that another stream's kernel holds
-__device__ __forceinline__ bool fp_wait_flags(const uint64_t* flags, int64_t step, int64_t parts, int32_t* err) {
+// that another stream's kernel holds.  False as well where a CTA has no piece to give.
+__device__ __forceinline__ bool fp_wait_flags(const uint64_t* flags, int64_t step, int64_t parts, uint32_t tries) {
     bool ok = true;
     for (int64_t c = threadIdx.x & 31; c < parts; c += 32) {
         uint64_t v = 0;
-        for (int i = 0; i < (1 << 25) && v != kFpRaised; ++i)
+        for (uint32_t i = 0; i < tries && v != kFpRaised && v != kFpBroken; ++i)
             asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(flags + c * step) : "memory");
-        if (v != kFpRaised) {
-            atomicOr(err, kErrWaitTimeout);
-            ok = false;
-        }
+        if (v != kFpRaised) ok = false;
     }
     ok = __all_sync(0xffffffffu, ok);
     __syncwarp();  // what one lane has acquired, all lanes read
@@ -565,8 +573,8 @@ __device__ __forceinline__ bool fp_wait_flags(const uint64_t* flags, int64_t ste
 // A barrier's wait; of a pair's barriers, which either CTA's copies and products arrive at,
 // acquiring what the cluster has released there.
 template <bool PAIR>
-__device__ __forceinline__ bool fp_wait(uint64_t* bar, uint32_t parity, int32_t* err) {
-    return PAIR ? mbar_wait_cluster(bar, parity, err) : mbar_wait(bar, parity, err);
+__device__ __forceinline__ bool fp_wait(uint64_t* bar, uint32_t parity, uint32_t tries) {
+    return PAIR ? mbar_wait_cluster(bar, parity, nullptr, tries) : mbar_wait(bar, parity, nullptr, tries);
 }
 
 // boxes of the TMA copies of `count` rows, none for fewer than one
@@ -621,15 +629,33 @@ fp4_tile_scales_kernel(FpArgs a, int words) {   // words: of a tile's row, a mul
     }
 }
 
-template <int NT, bool NV, bool PAIR, typename YT>
-__global__ void __launch_bounds__(FpShape<NT, NV, PAIR>::threads, 1)
+// NaN where a store warp has no sums: groups of 16 columns of y from c0 on, `step` apart
+// (not inlined: the loop that stores has to keep its registers, few enough that the next
+// kernel's CTAs fit beside this one's)
+template <typename YT>
+__device__ __noinline__ void fp_store_nan(YT* yp, int R, int c0, int n, int step) {
+    for (; c0 < n; c0 += step, yp += (int64_t)step * R)
+        for (int i = 0; i < min(16, n - c0); ++i) yp[i * (int64_t)R] = from_f32<YT>(__uint_as_float(0x7fc00000u));
+}
+
+// A wait that gives up (ok) makes its lane issue nothing more.  What is then never issued
+// makes the waits on it give up in turn, the store warps write NaN for the tiles that they
+// begin and raise kFpBroken for those they do not, and the workspace's first word becomes
+// kFpBroken: a call that finds it there has nothing but NaN to give, for the flags may hold
+// what that call left.  Every copy is in flight for microseconds and was issued before the
+// wait that gave up began, so none is when the CTAs leave; products in flight are waited for.
+// TW: the wait test (coli_moe_fp4_set_wait_test), an instantiation of its own so that the
+// others keep their limits at compile time.
+template <int NT, bool NV, bool PAIR, typename YT, bool TW>
+__global__ void __launch_bounds__(FpShape<NT, NV, PAIR>::bound, 1)
 fp4_product_kernel(const __grid_constant__ FpMaps<PAIR> maps, FpArgs a, YT* y) {
     using C = FpShape<NT, NV, PAIR>;
     extern __shared__ uint8_t fp_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(fp_raw) + 1023) & ~uintptr_t(1023));
     __shared__ FpPlan plan;
-    __shared__ __align__(8) uint64_t full[C::stages], empty[C::stages], accfull[2], accempty[2];
+    __shared__ __align__(8) uint64_t full[C::stages], empty[C::stages], accfull[2], accempty[2], done;
     __shared__ uint32_t tmem_slot;
+    constexpr uint32_t tries = TW ? kFpTestTries : kWaitTries;
     const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
     // of the pair's work, this CTA's part
@@ -649,11 +675,12 @@ fp4_product_kernel(const __grid_constant__ FpMaps<PAIR> maps, FpArgs a, YT* y) {
             mbar_init(&accfull[b], 1);
             mbar_init(&accempty[b], C::store_warps * C::ctas);
         }
+        mbar_init(&done, 1);
         fence_mbar_init();
     }
     pdl_trigger();
     pdl_wait();
-    if (blockIdx.x == 0 && threadIdx.x == 64) *a.err = 0;
+    const uint64_t before = *reinterpret_cast<const volatile uint64_t*>(a.err);
     fp_plan<NT, C::M>(a, plan);
     tc_fence_before();
     __syncthreads();
@@ -662,7 +689,7 @@ fp4_product_kernel(const __grid_constant__ FpMaps<PAIR> maps, FpArgs a, YT* y) {
     const uint32_t tmem = uniform(tmem_slot);
     const FpRun run(a, plan, gridDim.x / C::ctas, kFpMinUnits);
     FpPieces q(a, run, unit);
-    bool ok = true;  // cleared by a wait that gave up: then no further waits
+    bool ok = before != kFpBroken;  // cleared by a wait that gave up
 
     if (warp == 0) {
         // ---------------- copies (whole warp, an elected lane issues) ----------------
@@ -689,19 +716,20 @@ fp4_product_kernel(const __grid_constant__ FpMaps<PAIR> maps, FpArgs a, YT* y) {
                 const int xsrow = uniform((int)(xtile * a.KS * (C::atoms * C::nb)));
 #pragma unroll 1
                 for (int k = k0; k < k1; ++k) {
-                    if (ok && ring.again && !mbar_wait_cluster(&empty[ring.s], ring.phase ^ 1, a.err)) ok = false;
+                    if (ok && ring.again && !fp_wait<PAIR>(&empty[ring.s], ring.phase ^ 1, tries)) ok = false;
+                    const uint32_t go = ok && !(TW && a.withhold == 0 && blockIdx.x == 0 && !ring.again && ring.s == 0);
                     uint8_t* st = smem + ring.s * C::stage;
                     const uint32_t bar = bars + 8 * ring.s;
-                    if (rank == 0) mbar_expect_tx_elect(&full[ring.s], bytes);
-                    tma_load_2d_pair_elect(st, &maps.w, k * 128, wrow, bar);
+                    if (rank == 0) mbar_expect_tx_elect(&full[ring.s], bytes, go);
+                    tma_load_2d_pair_elect(st, &maps.w, k * 128, wrow, bar, go);
 #pragma unroll
                     for (int b = 0; b < C::rows / C::box; ++b)
                         if (b < boxes)
                             tma_load_2d_pair_elect(st + C::a_bytes + b * C::box * 128, &maps.x, k * 128, p0 + b * C::box,
-                                                   bar);
+                                                   bar, go);
                     uint8_t* sf = st + C::a_bytes + C::b_bytes;
-                    tma_load_2d_pair_elect(sf, &maps.ws, 0, wsrow + k * C::atoms, bar);
-                    tma_load_2d_pair_elect(sf + C::sfa_bytes, &maps.xs, 0, xsrow + k * (C::atoms * C::nb), bar);
+                    tma_load_2d_pair_elect(sf, &maps.ws, 0, wsrow + k * C::atoms, bar, go);
+                    tma_load_2d_pair_elect(sf + C::sfa_bytes, &maps.xs, 0, xsrow + k * (C::atoms * C::nb), bar, go);
                     ring.next(C::stages);
                 }
             } else {
@@ -709,14 +737,15 @@ fp4_product_kernel(const __grid_constant__ FpMaps<PAIR> maps, FpArgs a, YT* y) {
                 const uint32_t bytes = (uint32_t)(C::a_bytes + C::b_bytes);
 #pragma unroll 1
                 for (int k = k0; k < k1; ++k) {
-                    if (ok && ring.again && !mbar_wait(&empty[ring.s], ring.phase ^ 1, a.err)) ok = false;
+                    if (ok && ring.again && !fp_wait<PAIR>(&empty[ring.s], ring.phase ^ 1, tries)) ok = false;
+                    const uint32_t go = ok && !(TW && a.withhold == 0 && blockIdx.x == 0 && !ring.again && ring.s == 0);
                     uint8_t* st = smem + ring.s * C::stage;
                     uint64_t* bar = &full[ring.s];
                     const uint32_t na = (uint32_t)min(C::atoms, a.wwords - k * C::atoms) * 512;
-                    mbar_expect_tx_elect(bar, bytes + na);
-                    tma_load_2d_elect(st, &maps.w, k * 128, wrow, bar);
-                    tma_load_2d_elect(st + C::a_bytes, &maps.x, k * 128, p0, bar);
-                    bulk_g2s_elect(st + C::a_bytes + C::b_bytes, sfa, na, bar);
+                    mbar_expect_tx_elect(bar, bytes + na, go);
+                    tma_load_2d_elect(st, &maps.w, k * 128, wrow, bar, go);
+                    tma_load_2d_elect(st + C::a_bytes, &maps.x, k * 128, p0, bar, go);
+                    bulk_g2s_elect(st + C::a_bytes + C::b_bytes, sfa, na, bar, go);
                     sfa += C::atoms * 512;
                     ring.next(C::stages);
                 }
@@ -724,9 +753,10 @@ fp4_product_kernel(const __grid_constant__ FpMaps<PAIR> maps, FpArgs a, YT* y) {
         }
         // the last copies (of a pair, both CTAs') have landed before a CTA may end
         Ring last = ring.back(C::stages);
-        if (rank == 0)
+        if (rank == 0 && ok)
             for (int i = 0; i < C::stages; ++i, last.next(C::stages))
-                if (ring.again || last.s < ring.s) mbar_wait(&full[last.s], last.phase, a.err, kSleepTries);
+                if ((ring.again || last.s < ring.s) && !fp_wait<PAIR>(&full[last.s], last.phase, TW ? tries : kSleepTries))
+                    ok = false;
     } else if (warp == 1 && rank == 1) {
         // CTA 0 issues the products of a pair
     } else if (warp == 1) {
@@ -742,13 +772,14 @@ fp4_product_kernel(const __grid_constant__ FpMaps<PAIR> maps, FpArgs a, YT* y) {
             const int second = C::nb > 1 ? uniform(t.n > 128 ? 1 : 0) : 0;
             const int k0 = uniform(q.k0), k1 = uniform(q.k1);
             const int buf = piece & 1;
-            if (piece >= 2 && ok && !mbar_wait_cluster(&accempty[buf], ((piece >> 1) - 1) & 1, a.err)) ok = false;
+            if (piece >= 2 && ok && !mbar_wait_cluster(&accempty[buf], ((piece >> 1) - 1) & 1, nullptr, tries)) ok = false;
             tc_fence_after();
             const uint32_t d = tmem + NT * buf;
             uint32_t more = 0;                // 0: the tile's first product clears the accumulator
 #pragma unroll 1
             for (int k = k0; k < k1; ++k) {
-                if (!ready && ok && !fp_wait<PAIR>(&full[ring.s], ring.phase, a.err)) ok = false;
+                if (!ready && ok && !fp_wait<PAIR>(&full[ring.s], ring.phase, tries)) ok = false;
+                const uint32_t go = ok;
                 tc_fence_after();
                 // the scale warps' copies are writes of the generic proxy, and the tensor unit reads
                 // them: fenced here, where they are known to have landed
@@ -763,15 +794,15 @@ fp4_product_kernel(const __grid_constant__ FpMaps<PAIR> maps, FpArgs a, YT* y) {
                 // asked before this stage is issued, so that the answer is there after it
                 ready = PAIR ? mbar_test_cluster(&full[ring.s], ring.phase) : mbar_test(&full[ring.s], ring.phase);
                 if (cols >= 256) {
-                    fp4_stage<NV, PAIR>(d, ad, bd, idesc, sfa, sfb, sf, more, second, smem_u32(empty_s));
+                    fp4_stage<NV, PAIR>(d, ad, bd, idesc, sfa, sfb, sf, more, second, smem_u32(empty_s), go);
                 } else {  // the row's last columns
 #pragma unroll
                     for (int i = 0; i < C::atoms; ++i) {
                         if (i * (256 / C::atoms) >= cols) break;
-                        tc_copy_scales_elect<PAIR>(sf + 4 * i, sfa + 32 * i);
-                        tc_copy_scales_elect<PAIR>(sf + 4 * C::atoms + 4 * C::nb * i, sfb + 32 * C::nb * i);
+                        tc_copy_scales_elect<PAIR>(sf + 4 * i, sfa + 32 * i, go);
+                        tc_copy_scales_elect<PAIR>(sf + 4 * C::atoms + 4 * C::nb * i, sfb + 32 * C::nb * i, go);
                         if (second)
-                            tc_copy_scales_elect<PAIR>(sf + 4 * C::atoms + 4 * C::nb * i + 4, sfb + 32 * C::nb * i + 32);
+                            tc_copy_scales_elect<PAIR>(sf + 4 * C::atoms + 4 * C::nb * i + 4, sfb + 32 * C::nb * i + 32, go);
                     }
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -779,17 +810,20 @@ fp4_product_kernel(const __grid_constant__ FpMaps<PAIR> maps, FpArgs a, YT* y) {
                         const int at = NV ? j : j >> 1;              // scale tile
                         const uint32_t id = NV ? 0u : 2u * (j & 1);  // first byte of its words
                         tc_mma_fp4_elect<NV, PAIR>(d, ad + 2 * j, bd + 2 * j, idesc | id << 29 | id << 4, sf + 4 * at,
-                                                   sf + 4 * C::atoms + 4 * C::nb * at, j > 0 ? 1u : more);
+                                                   sf + 4 * C::atoms + 4 * C::nb * at, j > 0 ? 1u : more, go);
                     }
-                    if (PAIR) tc_commit_pair_elect(empty_s);
-                    else tc_commit_elect(empty_s);
+                    if (PAIR) tc_commit_pair_elect(empty_s, go);
+                    else tc_commit_elect(empty_s, go);
                 }
                 more = 1;
                 if (C::sf_sets == 2) sf = 2 * (tmem + C::sf0) + C::sf_cols - sf;
             }
-            if (PAIR) tc_commit_pair_elect(&accfull[buf]);
-            else tc_commit_elect(&accfull[buf]);
+            if (PAIR) tc_commit_pair_elect(&accfull[buf], ok);
+            else tc_commit_elect(&accfull[buf], ok);
         }
+        if (PAIR) tc_commit_of_pair_elect(&done, !ok);
+        else tc_commit_elect(&done, !ok);
+        if (!ok) mbar_wait(&done, 0, nullptr, tries);
     } else if (PAIR && warp < 4) {
         // nothing: a warp reads the accumulator's quarter of its index, so the stores begin at warp 4
     } else if (!PAIR && (warp < 4 || warp >= 8)) {
@@ -824,7 +858,8 @@ fp4_product_kernel(const __grid_constant__ FpMaps<PAIR> maps, FpArgs a, YT* y) {
             }
 #pragma unroll 1
             for (int k = k0; k < k1; ++k) {
-                if (ok && ring.again && !free && !mbar_wait(&empty[ring.s], ring.phase ^ 1, a.err)) ok = false;
+                if (ok && ring.again && !free && !mbar_wait(&empty[ring.s], ring.phase ^ 1, nullptr, tries)) ok = false;
+                if (!ok) continue;
                 const uint32_t at = ring.s * C::stage;
                 uint64_t* full_s = &full[ring.s];
                 ring.next(C::stages);
@@ -861,14 +896,16 @@ fp4_product_kernel(const __grid_constant__ FpMaps<PAIR> maps, FpArgs a, YT* y) {
             const int64_t other = (int64_t)blockIdx.x + C::ctas;  // the first of them
             uint64_t* flags = a.flags + kFpStoreWarps * other + flag;
             const float* theirs = a.partial + other * (128 * NT) + 16 * half * 128 + 32 * quarter + lane;
-            if (ok && !fp_wait<PAIR>(&accfull[buf], (piece >> 1) & 1, a.err)) ok = false;
+            if (ok && !fp_wait<PAIR>(&accfull[buf], (piece >> 1) & 1, tries)) ok = false;
+            ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
-            if (parts && ok && !fp_wait_flags(flags, kFpStoreWarps * C::ctas, parts, a.err)) ok = false;
+            if (parts && ok && !fp_wait_flags(flags, kFpStoreWarps * C::ctas, parts, TW ? tries : kFpFlagTries)) ok = false;
             const uint32_t d = tmem + ((uint32_t)(32 * quarter) << 16) + NT * buf;
             YT* yp = y + (t.p0 + 16 * half) * a.R + row;  // this lane's row of y's columns
             float* pp = a.partial + (int64_t)blockIdx.x * (128 * NT) + 16 * half * 128 + 32 * quarter + lane;
+            if (!ok && begins && row < a.R) fp_store_nan(yp, a.R, 16 * half, n, 16 * C::groups);
 #pragma unroll 1
-            for (int c0 = 16 * half; c0 < n; c0 += 16 * C::groups) {
+            for (int c0 = ok ? 16 * half : n; c0 < n; c0 += 16 * C::groups) {
                 uint32_t v[16];
                 tmem_ld_32x32b_x16(d + c0, v);
                 tmem_wait_ld();
@@ -909,10 +946,11 @@ fp4_product_kernel(const __grid_constant__ FpMaps<PAIR> maps, FpArgs a, YT* y) {
                 theirs += 16 * C::groups * 128;
             }
             __syncwarp();
-            if (!begins && lane == 0) {
+            if (!begins && lane == 0 && !(TW && a.withhold == 1)) {
                 __threadfence();
                 asm volatile("st.release.gpu.global.u64 [%0], %1;"
-                             ::"l"(a.flags + kFpStoreWarps * (int64_t)blockIdx.x + flag), "l"(kFpRaised) : "memory");
+                             ::"l"(a.flags + kFpStoreWarps * (int64_t)blockIdx.x + flag), "l"(ok ? kFpRaised : kFpBroken)
+                             : "memory");
             }
             for (int64_t c = lane; c < parts; c += 32)  // read once: down again for the next call
                 flags[c * (kFpStoreWarps * C::ctas)] = 0;
@@ -924,6 +962,7 @@ fp4_product_kernel(const __grid_constant__ FpMaps<PAIR> maps, FpArgs a, YT* y) {
             }
         }
     }
+    if (!ok) *reinterpret_cast<volatile uint64_t*>(a.err) = kFpBroken;
     tc_fence_before();
     __syncthreads();
     if (PAIR) cluster_sync();  // neither CTA leaves while the other may reach into it

@@ -160,6 +160,23 @@ __device__ __forceinline__ void bulk_g2s_elect(void* dst, const void* src, uint3
         : "memory");
 }
 
+// The same, where the elected lane's own `go` is not 0: for a lane that has given up
+// a wait must issue nothing more, and the lanes of a warp may disagree there.
+__device__ __forceinline__ void mbar_expect_tx_elect(uint64_t* bar, uint32_t bytes, uint32_t go) {
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n setp.ne.and.b32 e, %2, 0, e;\n"
+        " @e mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;\n}"
+        ::"r"(smem_u32(bar)), "r"(bytes), "r"(go)
+        : "memory");
+}
+__device__ __forceinline__ void bulk_g2s_elect(void* dst, const void* src, uint32_t bytes, uint64_t* bar, uint32_t go) {
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n setp.ne.and.b32 e, %4, 0, e;\n"
+        " @e cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];\n}"
+        ::"r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)), "r"(go)
+        : "memory");
+}
+
 // L2 policy for data read exactly once (weights streamed into the ring)
 __device__ __forceinline__ uint64_t l2_evict_first_policy() {
     uint64_t pol;
@@ -188,6 +205,16 @@ __device__ __forceinline__ void tma_load_2d_elect(void* dst, const CUtensorMap* 
         "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
         " @e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n}"
         ::"r"(smem_u32(dst)), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y)
+        : "memory");
+}
+
+// the same where the elected lane's `go` is not 0
+__device__ __forceinline__ void tma_load_2d_elect(void* dst, const CUtensorMap* map, int x, int y, uint64_t* bar,
+                                                  uint32_t go) {
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n setp.ne.and.b32 e, %5, 0, e;\n"
+        " @e cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];\n}"
+        ::"r"(smem_u32(dst)), "l"(map), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(go)
         : "memory");
 }
 
@@ -256,14 +283,16 @@ __device__ __forceinline__ uint32_t mapa_u32(uint32_t addr, uint32_t rank) {
     return r;
 }
 
-// tma_load_2d_elect of a pair of CTAs: into this CTA's shared memory, completion
-// counted on the barrier at cluster address `bar`, in either of the two
-__device__ __forceinline__ void tma_load_2d_pair_elect(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar) {
+// tma_load_2d_elect of a pair of CTAs, where the elected lane's `go` is not 0: into this
+// CTA's shared memory, completion counted on the barrier at cluster address `bar`, in
+// either of the two
+__device__ __forceinline__ void tma_load_2d_pair_elect(void* dst, const CUtensorMap* map, int x, int y, uint32_t bar,
+                                                       uint32_t go) {
     asm volatile(
-        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n setp.ne.and.b32 e, %5, 0, e;\n"
         " @e cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
         " [%0], [%1, {%3, %4}], [%2];\n}"
-        ::"r"(smem_u32(dst)), "l"(map), "r"(bar), "r"(x), "r"(y)
+        ::"r"(smem_u32(dst)), "l"(map), "r"(bar), "r"(x), "r"(y), "r"(go)
         : "memory");
 }
 

@@ -46,12 +46,27 @@ __device__ __forceinline__ void tc_commit_elect(uint64_t* bar) {
         ::"r"(smem_u32(bar))
         : "memory");
 }
-// arrives at the barrier in this place of both CTAs of the pair
-__device__ __forceinline__ void tc_commit_pair_elect(uint64_t* bar) {
+// where the elected lane's `go` is not 0: this CTA's products, those of a pair (arrival in
+// this CTA), and arrivals at the barrier in this place of both CTAs of the pair
+__device__ __forceinline__ void tc_commit_elect(uint64_t* bar, uint32_t go) {
     asm volatile(
-        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n"
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n setp.ne.and.b32 e, %1, 0, e;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}"
+        ::"r"(smem_u32(bar)), "r"(go)
+        : "memory");
+}
+__device__ __forceinline__ void tc_commit_of_pair_elect(uint64_t* bar, uint32_t go) {
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n setp.ne.and.b32 e, %1, 0, e;\n"
+        " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}"
+        ::"r"(smem_u32(bar)), "r"(go)
+        : "memory");
+}
+__device__ __forceinline__ void tc_commit_pair_elect(uint64_t* bar, uint32_t go) {
+    asm volatile(
+        "{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n setp.ne.and.b32 e, %2, 0, e;\n"
         " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n}"
-        ::"r"(smem_u32(bar)), "h"((uint16_t)3)
+        ::"r"(smem_u32(bar)), "h"((uint16_t)3), "r"(go)
         : "memory");
 }
 __device__ __forceinline__ void tc_mma_ts_elect(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc,

@@ -230,3 +230,14 @@ def test_product_sizes_up_to_31_bits():
     assert pairs > cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, 32, 32, 1, 1 << 30)
     assert cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, 40, 32, 1, most) == pairs
     assert cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, most, 32, 1, 1) >= pairs
+
+
+def test_wait_test_takes_only_what_it_knows():
+    assert code("coli_moe_fp4_set_wait_test", 2) == INVAL
+    try:
+        for withhold in (0, 1):
+            assert code("coli_moe_fp4_set_wait_test", withhold) == 0
+            for change in (dict(yt=1), dict(fmt=1)):   # refused before any launch
+                assert code("coli_moe_fp4_product", *{**PRODUCT, **change}.values()) == UNSUPPORTED
+    finally:
+        assert code("coli_moe_fp4_set_wait_test", -1) == 0

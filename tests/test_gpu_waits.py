@@ -3,7 +3,8 @@ test option of coli_moe_layer_set_wait_test, CTA 0's producer never issues one
 ring stage, the consumer warps' wait on it gives up after a short limit, the
 kernel and the combine return, coli_moe_status reports COLI_E_TIMEOUT, and the
 next call on the same workspace (option cleared) is correct and bit-identical
-to a call that never saw the option."""
+to a call that never saw the option.  The same of the 4-bit floating point product's
+waits (coli_moe_fp4_set_wait_test)."""
 import dataclasses
 
 import numpy as np
@@ -48,3 +49,67 @@ def test_wait_gives_up_and_the_next_call_is_correct(T, group):
     np.testing.assert_array_equal(out.view(np.uint32), y_clean.view(np.uint32))
     assert rel_err(out, y_ref) <= 2e-3
     L.close()
+
+
+def fp4_call(E, R, K, sizes):
+    """Random operands of a grouped MXFP4 product, the call as a function of y and ws, and ws's size."""
+    g = torch.Generator(device="cuda").manual_seed(R + K)
+    P = sum(sizes)
+    off = torch.tensor([0, *np.cumsum(sizes)], dtype=torch.int32, device="cuda")
+
+    def side(n):
+        nc, ns = cm.coli_moe_fp4_bytes(cm.COLI_MXFP4, n, K)
+        return (torch.randint(0, 256, (nc,), generator=g, device="cuda", dtype=torch.uint8),
+                torch.randint(120, 130, (ns,), generator=g, device="cuda", dtype=torch.uint8))
+    x, w = side(P), side(E * R)
+    return (lambda y, ws: cm.coli_moe_fp4_product(cm.COLI_MXFP4, *x, P, K, *w, E, R, y, ws, offsets=off),
+            cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, P, K, E, R))
+
+
+# one CTA by itself with tiles cut in several, whole waves of tiles and more, pairs of CTAs likewise
+@pytest.mark.parametrize("E,R,K,sizes", [(4, 1024, 6144, [1, 0, 3, 2]), (1, 128 * 150, 4096, [3]), (1, 10240, 6144, [60]),
+                                         (2, 5120, 6144, [300, 200])])
+@pytest.mark.parametrize("withhold", [0, 1])
+def test_product_wait_gives_up_is_reported_and_stays_until_cleared(E, R, K, sizes, withhold):
+    """A stage that is never copied, or pieces of cut tiles that are never announced: the call
+    returns, what lacks its sums is NaN, the rest is right; the status stays through the
+    next calls, which give only NaN, until the workspace is cleared."""
+    call, size = fp4_call(E, R, K, sizes)
+    ws = torch.full((size,), 255, dtype=torch.uint8, device="cuda")
+    good, y = (torch.full((sum(sizes), R), 9.0, device="cuda") for _ in range(2))
+    call(good, ws)
+    assert cm.coli_moe_fp4_product_status(ws) == 0 and torch.isfinite(good).all()
+    cm.coli_moe_fp4_set_wait_test(withhold)
+    try:
+        call(y, ws)
+    finally:
+        cm.coli_moe_fp4_set_wait_test(-1)
+    for _ in range(2):
+        with pytest.raises(cm.ColiError) as e:
+            cm.coli_moe_fp4_product_status(ws)
+        assert e.value.code == -6                              # COLI_E_TIMEOUT
+    gone = torch.isnan(y)
+    assert gone.any() and torch.equal(y[~gone], good[~gone])
+    y.fill_(9.0)
+    call(y, ws)                                                # marked: nothing to trust in ws
+    assert torch.isnan(y).all()
+    with pytest.raises(cm.ColiError):
+        cm.coli_moe_fp4_product_status(ws)
+    ws.zero_()
+    call(y, ws)
+    assert cm.coli_moe_fp4_product_status(ws) == 0 and torch.equal(y, good)
+
+
+def test_product_status_of_two_calls_is_read_once():
+    """Two products on one workspace, as gate/up and down of a block have them: the first one's
+    give-up is seen after the second."""
+    call, size = fp4_call(4, 1024, 6144, [1, 0, 3, 2])
+    ws, y = torch.zeros(size, dtype=torch.uint8, device="cuda"), torch.empty(6, 1024, device="cuda")
+    cm.coli_moe_fp4_set_wait_test(0)
+    try:
+        call(y, ws)
+    finally:
+        cm.coli_moe_fp4_set_wait_test(-1)
+    call(y, ws)
+    with pytest.raises(cm.ColiError):
+        cm.coli_moe_fp4_product_status(ws)
