@@ -545,6 +545,17 @@ int coli_moe_block_norm_backward(const coli_norm_desc* desc, const void* x_out, 
                                  float* dpre_gain, void* ws, size_t ws_bytes,
                                  coli_stream_t stream);
 
+/* Rows of many tokens come through copies inside the kernel, whose waits are
+ * bounded (seconds).  One that gives up, which nothing but a fault brings about,
+ * makes every gradient of its row and of the rows after it in the same CTA NaN,
+ * and the sums over tokens; later calls are unaffected.  Test of that: in later
+ * coli_moe_block_norm_backward calls of the calling thread, CTA 0 never copies
+ * row number `withhold` of its own (0 its first), with a short limit; < 0 (the
+ * default): none of this.  f32 streams with bf16 blocks of up to 6144 columns
+ * that take those copies (COLI_E_UNSUPPORTED else).  Never needed in normal use.
+ * Host-only. */
+int coli_moe_block_norm_set_wait_test(int32_t withhold);
+
 /* 4-bit floating point in blocks with a shared scale.  A value is E2M1 (sign,
  * magnitudes 0 0.5 1 1.5 2 3 4 6) times the scale of its block:
  *   COLI_MXFP4  blocks of 32 columns, E8M0 scale byte b = 2^(b - 127) (255: NaN);

@@ -31,6 +31,7 @@ __all__ = [
     "coli_moe_block_norm_backward", "coli_moe_fp4_bytes", "coli_moe_fp4_quantize",
     "coli_moe_fp4_product_workspace_size", "coli_moe_fp4_product",
     "coli_moe_fp4_product_status", "coli_moe_fp4_set_wait_test",
+    "coli_moe_block_norm_set_wait_test",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -60,6 +61,7 @@ EXPORTS = (
     "coli_moe_block_norm_backward", "coli_moe_fp4_bytes", "coli_moe_fp4_quantize",
     "coli_moe_fp4_product_workspace_size", "coli_moe_fp4_product",
     "coli_moe_fp4_product_status", "coli_moe_fp4_set_wait_test",
+    "coli_moe_block_norm_set_wait_test",
 )
 
 
@@ -158,6 +160,7 @@ _SIGS = {
                               ctypes.c_int, _P, _SZ, _P], ctypes.c_int),
     "coli_moe_fp4_product_status": ([_P, ctypes.POINTER(_I32), _P], ctypes.c_int),
     "coli_moe_fp4_set_wait_test": ([_I32], ctypes.c_int),
+    "coli_moe_block_norm_set_wait_test": ([_I32], ctypes.c_int),
 }
 for _name, (_args, _res) in _SIGS.items():
     _f = getattr(lib, _name)
@@ -569,6 +572,11 @@ def coli_moe_block_norm_backward(desc, x_out, o, T, dx_out, dn, dx, d_o, ws, gat
         _buf("d_o", d_o, bt, n, d), _buf("dpost_gain", dpost_gain, _FLOAT32, desc.H, d),
         _buf("dgate", dgate, _FLOAT32, ng, d), _buf("dpre_gain", dpre_gain, _FLOAT32, desc.H, d), p, size,
         _queue(stream, d)))
+
+
+def coli_moe_block_norm_set_wait_test(withhold: int) -> None:
+    """Test of the gradient's bounded waits (see the header); < 0: off."""
+    _ok(lib.coli_moe_block_norm_set_wait_test(withhold))
 
 
 def coli_moe_fp4_bytes(fmt: int, rows: int, K: int):

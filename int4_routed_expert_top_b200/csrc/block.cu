@@ -226,13 +226,17 @@ NormRing norm_ring(const coli_norm_desc& d, int ctas, bool wide, bool x_out, boo
     return r;
 }
 
-template <typename XT, typename BT, int W, int N, bool RING>
+// the row of CTA 0 that later gradients of this thread do not copy
+// (coli_moe_block_norm_set_wait_test), -1: none
+thread_local int32_t g_norm_withhold = -1;
+
+template <typename XT, typename BT, int W, int N, bool RING, bool TW = false>
 struct NormBackward {
     static int launch(const NormShape& s, const NormArgs& a, const NormSums& keep, const NormRing& ring,
                       const void* x_out, const void* o, const float* rstd_post, const float* rstd_pre,
                       const void* dx_out, const void* dn, void* dx, void* d_o, float* dgate, float* partial, int grid,
                       cudaStream_t st) {
-        const auto kern = block_norm_backward_kernel<XT, BT, W, N, RING>;
+        const auto kern = block_norm_backward_kernel<XT, BT, W, N, RING, TW>;
         const int smem = RING ? ring.first + ring.stages * ring.stage : std::min(keep.n, kNormKept) * a.H * 4;
         int rc = set_smem((const void*)kern, smem);
         if (rc) return rc;
@@ -251,7 +255,7 @@ struct NormBackward {
         cfg.numAttrs = 2;
         const cudaError_t e = cudaLaunchKernelEx(&cfg, kern, a, keep, ring, (const XT*)x_out, (const BT*)o, rstd_post,
                                                  rstd_pre, (const XT*)dx_out, (const BT*)dn, (XT*)dx, (BT*)d_o, dgate,
-                                                 partial);
+                                                 partial, (int)g_norm_withhold);
         if (e != cudaSuccess) return fail(COLI_E_CUDA, "block norm backward: %s", cudaGetErrorString(e));
         return check_launch("block norm backward");
     }
@@ -266,6 +270,7 @@ int norm_ring_launch(const NormShape& s, A... args) {
 }
 template <typename... A>
 int norm_ring_dispatch(const coli_norm_desc& d, const NormShape& s, A... args) {
+    if (g_norm_withhold >= 0) return NormBackward<float, __nv_bfloat16, 8, 1, true, true>::launch(s, args...);
     if (d.bt == COLI_F32) return norm_ring_launch<float, float>(s, args...);
     if (d.xt == COLI_F32) return norm_ring_launch<float, __nv_bfloat16>(s, args...);
     return norm_ring_launch<__nv_bfloat16, __nv_bfloat16>(s, args...);
@@ -436,6 +441,8 @@ int coli_moe_block_norm_backward(const coli_norm_desc* desc, const void* x_out, 
         const int ctas = norm_ring_ctas(*desc, T);
         const NormRing ring = norm_ring(*desc, ctas, W == 8, dn != nullptr, dx_out != nullptr, o != nullptr, dn != nullptr);
         grid = norm_backward_grid(T, ring.stages > 0 ? ctas : norm_plain_ctas(*desc, T));
+        if (g_norm_withhold >= 0 && (ring.stages == 0 || desc->xt != COLI_F32 || desc->bt != COLI_BF16 || desc->H > 8 * 768))
+            return fail(COLI_E_UNSUPPORTED, "block_norm_backward: the wait test takes the ring's rows of up to 6144 f32 with bf16 blocks");
         if (ring.stages > 0) {
             NormShape s;
             s.W = 8;
@@ -457,6 +464,11 @@ int coli_moe_block_norm_backward(const coli_norm_desc* desc, const void* x_out, 
     return launch_pdl(reduce, dim3((desc->H + 31) / 32, kNormSums), 32 * (rows <= 128 ? 8 : 32), 0, S(stream),
                       "block norm sums", (const float*)partial, rows, (int)desc->H, keep, dpost_gain,
                       channel ? dgate : nullptr, dpre_gain);
+}
+
+int coli_moe_block_norm_set_wait_test(int32_t withhold) {
+    g_norm_withhold = withhold < 0 ? -1 : withhold;
+    return COLI_OK;
 }
 
 }  // extern "C"

@@ -276,15 +276,22 @@ __device__ __forceinline__ F<8> lds_gain(const uint8_t* smem, int off, int c, in
 // makes two gradients where the gate is the same for every token: dpost_gain = alpha
 // gate z, dgate = alpha post_gain z.
 // partial [clusters][keep.n][H]
-template <typename XT, typename BT, int W, int N, bool RING>
+// A copy that does not land within the limit of its wait (seconds; nothing but a fault keeps
+// it) makes that row and the rest of its CTA's NaN in every gradient, the sums over
+// tokens with them, without further waits or copies.  TW: the wait test
+// (coli_moe_block_norm_set_wait_test): CTA 0 never copies its row `withhold`, and the limit is
+// short.
+constexpr uint32_t kNormTestTries = 4096;
+template <typename XT, typename BT, int W, int N, bool RING, bool TW>
 __global__ void __launch_bounds__(N == 1 ? 768 : 512)
 block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x_out, const BT* o,
                            const float* rstd_post, const float* rstd_pre, const XT* dx_out, const BT* dn, XT* dx,
-                           BT* d_o, float* dgate, float* partial) {
+                           BT* d_o, float* dgate, float* partial, int withhold) {
     extern __shared__ __align__(128) uint8_t nb_smem[];   // the ring, or the sums; at the end the sums
     __shared__ float part[2][96];                         // of even and odd rows
     __shared__ __align__(8) uint64_t full[kNormMaxStages];
     __shared__ float rstds[kNormMaxStages][2];
+    __shared__ int gone;                                  // a wait of this CTA has given up
     float* sums = reinterpret_cast<float*>(nb_smem);
     static_assert(!RING || W == 8, "rows of the ring are read in vectors of eight");
     const int step = (int)blockDim.x * 8, c0 = (int)threadIdx.x * W;
@@ -302,6 +309,7 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
         if (threadIdx.x == 0) {
             for (int i = 0; i < ring.stages; ++i) mbar_init(&full[i], 2);  // the rows, the two rstd
             fence_mbar_init();
+            gone = 0;
         }
     } else {
         for (int i = threadIdx.x; i < kept * a.H; i += blockDim.x) sums[i] = 0.0f;
@@ -312,7 +320,7 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
     const float* post_gain = a.post_norm ? a.post_gain : nullptr;
     // row t into stage `at` (one thread)
     const auto fetch = [&](int64_t t, int at) {
-        if (t >= a.T) return;
+        if (t >= a.T || (TW && t == (int64_t)withhold * gridDim.x)) return;
         uint8_t* st = nb_smem + ring.first + at * ring.stage;
         const uint32_t xb = a.H * (uint32_t)sizeof(XT), bb = a.H * (uint32_t)sizeof(BT);
         mbar_expect_tx(&full[at], (ring.off[0] >= 0 ? xb : 0) + (ring.off[1] >= 0 ? xb : 0) +
@@ -355,6 +363,7 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
     };
     int at = 0, odd = 0;
     uint32_t phase = 0;
+    bool broken = false;                                  // as gone was at the last row's barrier
     for (int64_t t = blockIdx.x; t < a.T; t += gridDim.x, odd ^= 1) {
         const int64_t row = t * a.H;
         F<8> d[N];
@@ -363,9 +372,8 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
         float s[3] = {0.0f, 0.0f, 0.0f};  // v xh, w oh d', w oh xh
         float rx = 0.0f, ro = 1.0f;
         const uint8_t* st = nb_smem + ring.first + at * ring.stage;
-        // a copy that never lands (a wait of seconds) makes the row NaN
-        bool landed = true;
-        if (RING) landed = mbar_wait(&full[at], phase, nullptr);
+        if (RING && !broken && !mbar_wait(&full[at], phase, nullptr, TW ? kNormTestTries : kWaitTries))
+            *(volatile int*)&gone = 1;
         if (dn) rx = RING ? rstds[at][0] : rstd_pre[t];
         if (o && a.post_norm) ro = RING ? rstds[at][1] : rstd_post[t];
         const float c = token && o ? a.alpha * a.gate[t] : 1.0f;
@@ -395,7 +403,6 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
 #pragma unroll
                 for (int j = 0; j < 8; ++j) d[i].v[j] = 0.0f;
             }
-            if (!landed) d[i].v[0] = __uint_as_float(0x7fc00000u);
         }
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -442,7 +449,15 @@ block_norm_backward_kernel(NormArgs a, NormSums keep, NormRing ring, const XT* x
         else if (RING) __syncthreads();
         // every thread has its part of the row: the stage takes the row that comes next in it
         if (RING) {
-            if (threadIdx.x == 0) fetch(t + (int64_t)ring.stages * gridDim.x, at);
+            broken = *(volatile int*)&gone != 0;
+            if (broken) {
+                s[1] = __uint_as_float(0x7fc00000u);
+#pragma unroll
+                for (int i = 0; i < N; ++i)
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) d[i].v[j] = pre_acc[RING ? i : 0].v[j] = s[1];
+            }
+            if (threadIdx.x == 0 && !broken) fetch(t + (int64_t)ring.stages * gridDim.x, at);
             if (++at == ring.stages) {
                 at = 0;
                 phase ^= 1;

@@ -241,3 +241,12 @@ def test_wait_test_takes_only_what_it_knows():
                 assert code("coli_moe_fp4_product", *{**PRODUCT, **change}.values()) == UNSUPPORTED
     finally:
         assert code("coli_moe_fp4_set_wait_test", -1) == 0
+
+
+def test_norm_wait_test_takes_only_what_it_knows():
+    try:
+        assert code("coli_moe_block_norm_set_wait_test", 0) == 0
+        for change in (dict(), dict(T=4000, desc=norm(H=63)), dict(T=4000, desc=norm(bt=0)), dict(T=4000, desc=norm(H=8192))):
+            assert code("coli_moe_block_norm_backward", *{**NORM_B, **change}.values()) == UNSUPPORTED
+    finally:
+        assert code("coli_moe_block_norm_set_wait_test", -1) == 0

@@ -4,7 +4,8 @@ ring stage, the consumer warps' wait on it gives up after a short limit, the
 kernel and the combine return, coli_moe_status reports COLI_E_TIMEOUT, and the
 next call on the same workspace (option cleared) is correct and bit-identical
 to a call that never saw the option.  The same of the 4-bit floating point product's
-waits (coli_moe_fp4_set_wait_test)."""
+waits (coli_moe_fp4_set_wait_test) and of those in the block norm's gradient
+(coli_moe_block_norm_set_wait_test), which makes its rows NaN."""
 import dataclasses
 
 import numpy as np
@@ -113,3 +114,53 @@ def test_product_status_of_two_calls_is_read_once():
     call(y, ws)
     with pytest.raises(cm.ColiError):
         cm.coli_moe_fp4_product_status(ws)
+
+
+@pytest.mark.parametrize("H,gate", [(6144, "channel"), (1024, "token"), (512, "full"), (1024, "none")])
+@pytest.mark.parametrize("post,dn", [(True, True), (False, False)])
+@pytest.mark.parametrize("withhold", [0, 1])
+def test_norm_gradient_wait_gives_up_in_nan(H, gate, post, dn, withhold):
+    """Rows of CTA 0 from the withheld one on are NaN in every gradient, the sums over tokens with
+    them; the others are right, and so is the next call."""
+    T = 2000
+    g = torch.Generator(device="cuda").manual_seed(H)
+
+    def rand(*shape, dt=torch.float32):
+        return torch.randn(*shape, generator=g, device="cuda").to(dt)
+    kind = {"none": 0, "channel": 1, "token": 2, "full": 3}[gate]
+    shape = {"none": None, "channel": (H,), "token": (T,), "full": (T, H)}[gate]
+    gv = None if shape is None else rand(*shape)
+    gains = rand(H), rand(H)
+    desc = cm.NormDesc(H, cm.COLI_F32, cm.COLI_BF16, int(post), kind, 0.7, 1e-5, gains[0].data_ptr(), gains[1].data_ptr())
+    x, o, dxo, dnv = rand(T, H), rand(T, H, dt=torch.bfloat16), rand(T, H), rand(T, H, dt=torch.bfloat16)
+    r = rand(T).abs(), rand(T).abs()
+    ws = torch.empty(cm.coli_moe_block_norm_backward_workspace_size(desc, T), dtype=torch.uint8, device="cuda")
+
+    def run():
+        out = dict(dx=torch.full_like(x, 9.0), d_o=torch.full_like(o, 9.0),
+                   dpost_gain=torch.full((H,), 9.0, device="cuda") if post else None,
+                   dpre_gain=torch.full((H,), 9.0, device="cuda") if dn else None,
+                   dgate=None if gv is None else torch.full_like(gv, 9.0))
+        cm.coli_moe_block_norm_backward(desc, x, o, T, dxo, dnv if dn else None, out["dx"], out["d_o"], ws, gate=gv,
+                                        rstd_post=r[0] if post else None, rstd_pre=r[1] if dn else None,
+                                        dpost_gain=out["dpost_gain"], dgate=out["dgate"], dpre_gain=out["dpre_gain"])
+        return {n: a for n, a in out.items() if a is not None}
+    good = run()
+    cm.coli_moe_block_norm_set_wait_test(withhold)
+    try:
+        bad = run()
+    finally:
+        cm.coli_moe_block_norm_set_wait_test(-1)
+    rows = torch.isnan(bad["dx"]).all(1)
+    assert torch.equal(torch.isnan(bad["dx"]).any(1), rows)                 # whole rows
+    at = torch.nonzero(rows)[:, 0].tolist()
+    step = at[1] - at[0]
+    assert at == list(range(withhold * step, T, step)) and step % 148 == 0   # one CTA's
+    for n, a in bad.items():
+        if n in ("dx", "d_o") or (n == "dgate" and gate in ("token", "full")):
+            assert torch.isnan(a[rows]).all() and torch.equal(a[~rows], good[n][~rows]), n
+        else:
+            assert torch.isnan(a).all(), n
+    again = run()
+    for n in good:
+        assert torch.equal(again[n], good[n]), n
