@@ -607,7 +607,10 @@ int coli_moe_fp4_quantize(coli_fp4 fmt, const void* x, coli_dtype xt, int64_t n_
  * alpha device f32 [E] or NULL (1): for NVFP4 the product of the two g (X and W
  * above are without them).  y device [P, R] of type yt; rows that no expert has
  * are left untouched.  Products are exact, sums in f32 in an order that depends
- * on offsets and sizes alone; one rounding to yt.  1 <= E <= 1024, P < 2^31,
+ * on offsets and sizes alone; one rounding to yt.  The kernel's tiles are chosen by
+ * P / E, the rows of an expert on average (offsets are read on the device): rows
+ * that nearly all belong to a few of many experts are right, but slower than a
+ * call with those experts alone.  1 <= E <= 1024, P < 2^31,
  * E * R < 2^31, K a multiple of 32.  ws: device, 16-byte aligned,
  * coli_moe_fp4_product_workspace_size bytes, set to anything before its first
  * use.  Should a bounded wait inside the kernel give up (some ten seconds: other

@@ -31,17 +31,38 @@ int sm_count() {
     return sms;
 }
 
-// Rows of an expert per tile: 32 for a CTA by itself, 224 for a pair of CTAs.  Pairs
-// where an expert has more than 32 rows on average, since its weights then pass an
-// SM once and not several times (32 experts of 4096 x 6144: 73 us by itself and 75
-// in pairs at 16 rows each, 88 and 74 at 33, 167 and 84 at 97, 524 and 169 at 385), and
-// where that gives tiles for half of the 74 pairs at least; with fewer the cut tiles'
-// joining takes more than it saves (one expert of 4096 x 6144: 22 us by itself and 27 in
-// pairs for 385 rows, 32 tiles; of 18944 x 6144: 43 and 15 us for 193 rows, 74 tiles).
+// Rows of an expert per tile: 32 for a CTA by itself, 224 for a pair of CTAs, whose
+// weights then pass an SM once and not several times, at the price of a kernel that
+// lays out the rows' scales and of longer starts and ends.  With experts of n = P / E rows
+// on average (the counts are on the device), a stage of a tile of 32 takes 0.25 us and
+// one of a pair as long as 1.6 of those, a row of tiles has E * R / 128 * K / 256 stages
+// over 148 SMs, and pairs take some 5 us (20 stages) more to begin and end.  So pairs where
+// (row tiles of 32) - 1.6 (row tiles of 224) of these rows take more than 20 stages an SM:
+//                                          by itself, in pairs (us)
+//   32 experts of 4096 x 6144, 16 rows         72.9   76.6
+//                              33 rows         91.2   77.9
+//                              97 rows          174   85.3
+//                             385 rows          546    164
+//   one matrix of 10240 x 6144, 33 rows        14.0   18.0
+//                               65 rows        16.3   17.5
+//                 10240 x 2048, 50 rows         8.8   10.8
+//                              400 rows        22.5   15.2
+//                 18944 x 6144, 193 rows       45.6   17.1
+//   8 experts of 2048 x 2048, 50 rows           9.6   11.4
+// and where that gives tiles for half of the 74 pairs at least; with fewer the cut tiles'
+// joining takes more than it saves (one matrix of 4096 x 6144, 385 rows, 32 tiles: 22.9 and
+// 28.2 us).  Once true it stays true for more rows (a tile of 224 begun counts for nothing
+// until its rows make up for it), and with it the larger workspace.
 constexpr int kFpSmallNT = 32, kFpLargeNT = 224;
-bool pairs_apply(int64_t P, int E, int R) {
-    const int64_t tiles = (int64_t)E * ((R - 1) / 256 + 1) * ((P + (int64_t)kFpLargeNT * E - 1) / ((int64_t)kFpLargeNT * E));
-    return P > (int64_t)kFpSmallNT * E && tiles >= 40;
+bool pairs_apply(int64_t P, int K, int E, int R) {
+    const int64_t n = (P + E - 1) / E;
+    if (n <= kFpSmallNT) return false;
+    const int64_t full = (n - 1) / kFpLargeNT, rest = (n - full * kFpLargeNT + 31) / 32;  // row tiles
+    const int64_t tiles = (int64_t)E * ((R - 1) / 256 + 1) * (full + 1);
+    const int64_t stages = (int64_t)E * ((R - 1) / 128 + 1) * ((K + 255) / 256);  // of a row of tiles
+    const int64_t saved = 27 * full + std::max<int64_t>(0, 5 * rest - 8);         // rows of tiles, times 5
+    constexpr int64_t enough = 20 * 5 * 148;
+    return tiles >= 40 && (saved > enough || stages * saved > enough);
 }
 
 // bytes [rows][K/2], boxes of 128 bytes x box_rows, 128-byte swizzle
@@ -198,7 +219,7 @@ int coli_moe_fp4_product_workspace_size(coli_fp4 fmt, int64_t P, int32_t K, int3
     if (!bytes) return fail(COLI_E_INVAL, "fp4_product_workspace_size: NULL pointer");
     if (E < 1 || E > kFpMaxE || R < 1 || (E > 1 && R % 128) || (int64_t)E * R > INT32_MAX)
         return fail(COLI_E_INVAL, "fp4_product: bad sizes E=%d R=%d", E, R);
-    *bytes = kFpHeadBytes + (pairs_apply(P, E, R) ? partial_bytes(kFpLargeNT) + pair_scale_bytes(fmt, P, K, E)
+    *bytes = kFpHeadBytes + (pairs_apply(P, K, E, R) ? partial_bytes(kFpLargeNT) + pair_scale_bytes(fmt, P, K, E)
                                                   : partial_bytes(kFpSmallNT));
     return COLI_OK;
 }
@@ -232,7 +253,7 @@ int coli_moe_fp4_product(coli_fp4 fmt, const void* x_codes, const void* x_scales
     a.partial = reinterpret_cast<float*>(static_cast<char*>(ws) + kFpHeadBytes);
     a.xtiles = reinterpret_cast<uint4*>(static_cast<char*>(ws) + kFpHeadBytes + partial_bytes(kFpLargeNT));  // pairs
     a.max_xtiles = pair_row_tiles(P, E);
-    if (pairs_apply(P, E, R)) return launch_product_t<kFpLargeNT, true>(fmt, yt, a, x_codes, w_codes, y, S(stream));
+    if (pairs_apply(P, K, E, R)) return launch_product_t<kFpLargeNT, true>(fmt, yt, a, x_codes, w_codes, y, S(stream));
     return launch_product_t<kFpSmallNT, false>(fmt, yt, a, x_codes, w_codes, y, S(stream));
 }
 

@@ -199,7 +199,8 @@ def test_sort_workspace_of_more_tokens_serves_fewer(k, E):
 
 
 def test_product_workspace_of_more_rows_serves_fewer():
-    for E, R, K in ((1, 1, 32), (1, 4096, 6144), (1, 10240, 256), (32, 4096, 6144), (256, 128, 64), (1024, 128, 32)):
+    for E, R, K in ((1, 1, 32), (1, 4096, 6144), (1, 10240, 256), (1, 10240, 2048), (1, 2560, 6144), (8, 2560, 1024),
+                    (32, 256, 64), (32, 4096, 6144), (256, 128, 64), (1024, 128, 32)):
         rows = sorted({n + d for n in (1, 32, 224, 448, 1000, 7168, 32 * E, 224 * E, 30000, 1 << 24) for d in range(0, 3)}
                       | set(range(0, 3000, 7)))
         assert never_smaller([cm.coli_moe_fp4_product_workspace_size(cm.COLI_NVFP4, P, K, E, R) for P in rows])

@@ -327,11 +327,12 @@ def pair_inputs(fmt, sizes, R, K, seed):
 
 
 @pytest.mark.parametrize("fmt", list(FMT))
-@pytest.mark.parametrize("sizes,R,K", [([1, 32, 94, 225, 0, 127, 449, 33], 2560, 1536), ([700], 5120, 2208)])
+@pytest.mark.parametrize("sizes,R,K", [([1, 32, 94, 225, 0, 127, 449, 33], 2560, 2080), ([700], 5120, 2208)])
 def test_product_of_pairs_reads_no_stale_scales(fmt, sizes, R, K):
     """Two sets of inputs in turn through the same buffers and workspace, many times: the same
     bits every time, those of a first call, which are right."""
     P, E = sum(sizes), len(sizes)
+    assert in_pairs(fmt, E, R, K, P)
     sets, want = [], []
     for seed in (1, 2):
         ((xc, xb), (wc, wb)), off = pair_inputs(fmt, sizes, R, K, seed)
@@ -358,14 +359,99 @@ def test_product_of_pairs_reads_no_stale_scales(fmt, sizes, R, K):
 
 def test_product_of_pairs_with_offsets_that_overlap_stays_in_bounds():
     """Offsets that are not ascending name more row tiles than P rows have."""
-    P, R, K, E = 900, 2560, 512, 8
+    P, R, K, E = 900, 2560, 2048, 8
     rng = np.random.default_rng(3)
     xc, xb = weights("mx", P, K, rng)
     wc, wb = weights("mx", E * R, K, rng)
     size = cm.coli_moe_fp4_product_workspace_size(cm.COLI_MXFP4, P, K, E, R)
+    assert in_pairs("mx", E, R, K, P)
     y, ws = torch.full((P + 300, R), 9.0, device="cuda"), torch.full((size + 65536,), 7, dtype=torch.uint8, device="cuda")
     off = dev(np.array([0, P, 0, P, 0, P, 0, P, 0], np.int32))
     cm.coli_moe_fp4_product(cm.COLI_MXFP4, dev(xc.reshape(-1)), dev(ff.tile_scales(xb)), P, K, dev(wc.reshape(-1)),
                             dev(ff.tile_scales(wb)), E, R, y[:P], ws[:size], offsets=off)
     assert cm.coli_moe_fp4_product_status(ws) == 0
     assert (y[P:] == 9.0).all() and (ws[size:] == 7).all()
+
+
+def in_pairs(fmt, E, R, K, n):
+    """Whether a product takes pairs of CTAs, by the workspace that these need."""
+    size = cm.coli_moe_fp4_product_workspace_size
+    return size(FMT[fmt], n, K, E, R) > size(FMT[fmt], 1, K, E, R)
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+# row counts about the ends of half tiles and tiles, last weight rows and columns of every sort
+@pytest.mark.parametrize("R,K,n", [(35300, 96, 440), (70300, 32, 225), (14100, 1056, 224), (10240, 2048, 193), (6000, 2208, 449),
+                                   (33920, 1024, 129), (33000, 1184, 128), (10300, 6144, 97), (70400, 256, 250)])
+def test_product_in_pairs_one_group(fmt, R, K, n):
+    assert in_pairs(fmt, 1, R, K, n)
+    for yt in (F, B):
+        check_product(fmt, 1, R, K, [n], yt)
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+@pytest.mark.parametrize("R,K,sizes", [(3456, 1024, [0, 300, 0, 1, 200, 817]), (2688, 2080, [130, 859, 5, 0]),
+                                       (640, 800, [129, 0, 225, 3, 400] * 9), (128, 2560, [33, 70, 224, 225, 500] * 12)])
+def test_product_in_pairs_groups(fmt, R, K, sizes):
+    assert in_pairs(fmt, len(sizes), R, K, sum(sizes))
+    for yt in (F, B):
+        check_product(fmt, len(sizes), R, K, sizes, yt, seed=len(sizes))
+
+
+@pytest.mark.parametrize("tiles,K,n", [(75, 1024, 193), (76, 1280, 200), (151, 512, 193), (222, 768, 97), (75, 512, 449)])
+def test_product_in_pairs_few_tiles_left_over(tiles, K, n):
+    assert in_pairs("mx", 1, 256 * tiles, K, n)
+    check_product("mx", 1, 256 * tiles, K, [n])
+
+
+@pytest.mark.parametrize("fmt", list(FMT))
+def test_product_in_pairs_accuracy_and_wide_scales(fmt):
+    assert check_product(fmt, 1, 10240, 6144, [97]) <= 5e-6
+    check_product(fmt, 3, 5120, 2048, [90, 370, 200], wide=True, alpha=False)
+
+
+def test_product_in_pairs_nan_scale_stays_in_its_row():
+    rng = np.random.default_rng(8)
+    xc, xb = weights("mx", 440, 96, rng)
+    wc, wb = weights("mx", 35300, 96, rng)
+    xb[7, 2], xb[300, 0], wb[100, 0], wb[35299, 1] = 255, 255, 255, 255
+    y = torch.isnan(product("mx", xc, xb, wc, wb, 1, 35300, None, None, F, 440, 96))
+    want = torch.zeros_like(y)
+    for r in (7, 300):
+        want[r] = True
+    for c in (100, 35299):
+        want[:, c] = True
+    assert torch.equal(y, want)
+
+
+def test_product_in_pairs_one_expert_with_offsets():
+    rng = np.random.default_rng(11)
+    P, R, K = 440, 35300, 256
+    xc, xb = weights("mx", P, K, rng)
+    wc, wb = weights("mx", R, K, rng)
+    y = product("mx", xc, xb, wc, wb, 1, R, [3, P - 5], None, F, P, K)
+    assert (y[:3] == 9.0).all() and (y[P - 5:] == 9.0).all()
+    X, W = dev(ff.values(xc, xb, "mx")), dev(ff.values(wc, wb, "mx"))
+    assert ((y[3:P - 5].double() - (X @ W.T)[3:P - 5]).abs() <= 28 * 2.0 ** -22 * (X.abs() @ W.abs().T)[3:P - 5]).all()
+
+
+def test_product_in_pairs_on_two_streams_at_once():
+    """Pairs of two calls and CTAs by themselves of a third taking turns on the SMs."""
+    rng = np.random.default_rng(12)
+    calls = []
+    for n, R in ((200, 38400), (700, 12800), (3, 38400)):
+        xc, xb = weights("mx", n, 512, rng)
+        wc, wb = weights("mx", R, 512, rng)
+        args = [dev(xc.reshape(-1)), dev(ff.tile_scales(xb)), n, 512, dev(wc.reshape(-1)), dev(ff.tile_scales(wb)), 1, R]
+        assert in_pairs("mx", 1, R, 512, n) == (n > 3)
+        size = cm.coli_moe_fp4_product_workspace_size(FMT["mx"], n, 512, 1, R)
+        want, ws = torch.empty(n, R, device="cuda"), torch.zeros(size, dtype=torch.uint8, device="cuda")
+        cm.coli_moe_fp4_product(FMT["mx"], *args, want, ws)
+        calls.append((args, want, torch.empty_like(want), ws, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for args, _, y, ws, stream in calls:
+            cm.coli_moe_fp4_product(FMT["mx"], *args, y, ws, stream=stream)
+    torch.cuda.synchronize()
+    for _, want, y, ws, _ in calls:
+        assert cm.coli_moe_fp4_product_status(ws) == 0 and torch.equal(y, want)

@@ -68,7 +68,7 @@ def fp4_call(E, R, K, sizes):
 
 
 # one CTA by itself with tiles cut in several, whole waves of tiles and more, pairs of CTAs likewise
-@pytest.mark.parametrize("E,R,K,sizes", [(4, 1024, 6144, [1, 0, 3, 2]), (1, 128 * 150, 4096, [3]), (1, 10240, 6144, [60]),
+@pytest.mark.parametrize("E,R,K,sizes", [(4, 1024, 6144, [1, 0, 3, 2]), (1, 128 * 150, 4096, [3]), (1, 10240, 6144, [97]),
                                          (2, 5120, 6144, [300, 200])])
 @pytest.mark.parametrize("withhold", [0, 1])
 def test_product_wait_gives_up_is_reported_and_stays_until_cleared(E, R, K, sizes, withhold):
