@@ -36,12 +36,12 @@
 // CTA 0 issues the products for both.  A stage is then 33 KB per SM instead of the
 // 43 KB of a 128 x 192 tile for 1.17 times the work.
 //
-// Measured (B200): 8 rows, one to an expert, of 4096 x 6144: 23.2 us, 4.6 TB/s of
-// weights (launch, schedule and first loads are some 6 us of it); 512 rows on 64
-// experts of 6144 x 2048: 73 us, 6.3 TB/s, 0.97 of a copy's rate; 32768 rows on 32
-// experts of 4096 x 6144 with skewed counts: 363 us, 4.5 PFLOP/s, the tensor pipe
-// 70% active; one matrix of 18944 x 6144 and 14336 rows: 5.4 PFLOP/s, 7.0 with all
-// codes zero: under sustained load the chip's power limit sets the clock (1.4 GHz).
+// Measured (B200, calls one after the other in a graph): 8 rows, one to an expert, of 4096 x
+// 6144: 21.5 us, 5.0 TB/s of weights (launch, schedule and first loads are some 6 us of it);
+// 512 rows on 64 experts of 6144 x 2048: 74 us, 6.1 TB/s, 0.94 of a copy's rate; 32768 rows on
+// 32 experts of 4096 x 6144 with skewed counts: 346 to 355 us on several boxes, 4.7 PFLOP/s, the
+// tensor pipe 74% active (NVFP4: 376 us); one matrix of 18944 x 6144 and 14336 rows:
+// 5.5 PFLOP/s: under sustained load the chip's power limit sets the clock (1.4 GHz).
 //
 // CTA roles: warp 0 copies (codes by 2-D TMA with the 128-byte swizzle, the
 // weights' scales by bulk copy), warp 1 copies scales to TMEM and issues the
@@ -234,7 +234,7 @@ struct FpShape {
     static constexpr int groups = store_warps / 4;           // warps to a quarter of the lanes
     static constexpr int threads = 32 * (PAIR ? 12 : 10);
     // the launch bound: 128 registers a thread of a pair, so that the next product's gather of
-    // scales (14336 of them) fits beside its CTAs (400 rows of 10240 x 2048: 14.7 us, 15.4 with 131)
+    // scales (14336 of them) fits beside its CTAs (400 rows of 10240 x 2048 on one box: 14.7 us, 15.4 with 131)
     static constexpr int bound = PAIR ? 512 : threads;
     static constexpr int step = 16 * ctas;                   // N is a multiple of it
     static constexpr int atoms = NV ? 4 : 2;                 // 512-byte scale tiles per 256 columns
@@ -588,7 +588,8 @@ template <class C> __device__ __forceinline__ int fp_boxes(int count) { return m
 // each CTA, CTA 1's writes need a release to the cluster before every arrival at CTA 0,
 // which takes some 1650 cycles: 842 us for 32768 rows on 32 experts of 4096 x 6144 with one
 // warp that releases, 396 with four, 357 without the release, which nothing then orders;
-// 338 this way, of which this kernel is some 3; 400 rows of 10240 x 2048: 13.9 and 15.5.)
+// 346 this way; 400 rows of 10240 x 2048: 13.0 and 15.3, this kernel's chain of loads before
+// the product's own.)
 // A warp takes two words of a tile's rows at a time: 16 loads of a lane in flight.
 constexpr int kFpTileScaleThreads = 256;
 template <int NT, int M, int NB>

@@ -22,7 +22,7 @@
 // A row's four inputs and its barriers leave an SM waiting for HBM most of the
 // time if it only loads a row when it gets to it (4096 x 6144, f32 stream, bf16
 // blocks: 193 us).  With many tokens the rows therefore come through a ring in
-// shared memory: one thread issues the bulk copies of the rows ahead (88 us, 5.2
+// shared memory: one thread issues the bulk copies of the rows ahead (89 us, 5.1
 // TB/s, with one barrier a row; with the two that follow the formulas 110 us).  The
 // sums are then in registers.  Rows that leave no
 // room for two stages, unaligned rows and few tokens take the loads as they come.
