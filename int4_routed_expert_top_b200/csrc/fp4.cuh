@@ -39,7 +39,7 @@
 // Measured (B200, calls one after the other in a graph): 8 rows, one to an expert, of 4096 x
 // 6144: 21.5 us, 5.0 TB/s of weights (launch, schedule and first loads are some 6 us of it);
 // 512 rows on 64 experts of 6144 x 2048: 74 us, 6.1 TB/s, 0.94 of a copy's rate; 32768 rows on
-// 32 experts of 4096 x 6144 with skewed counts: 346 to 355 us on several boxes, 4.7 PFLOP/s, the
+// 32 experts of 4096 x 6144 with skewed counts: 346 to 355 us from run to run, 4.7 PFLOP/s, the
 // tensor pipe 74% active (NVFP4: 376 us); one matrix of 18944 x 6144 and 14336 rows:
 // 5.5 PFLOP/s: under sustained load the chip's power limit sets the clock (1.4 GHz).
 //
@@ -234,7 +234,7 @@ struct FpShape {
     static constexpr int groups = store_warps / 4;           // warps to a quarter of the lanes
     static constexpr int threads = 32 * (PAIR ? 12 : 10);
     // the launch bound: 128 registers a thread of a pair, so that the next product's gather of
-    // scales (14336 of them) fits beside its CTAs (400 rows of 10240 x 2048 on one box: 14.7 us, 15.4 with 131)
+    // scales (14336 of them) fits beside its CTAs (400 rows of 10240 x 2048 in one run: 14.7 us, 15.4 with 131)
     static constexpr int bound = PAIR ? 512 : threads;
     static constexpr int step = 16 * ctas;                   // N is a multiple of it
     static constexpr int atoms = NV ? 4 : 2;                 // 512-byte scale tiles per 256 columns
